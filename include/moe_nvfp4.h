@@ -82,7 +82,9 @@ enum {
   MOE_ERR_SHAPE = 2,     /* unsupported shape: a K not multiple of 64, an N not multiple of 128 */
   MOE_ERR_CUDA = 3,      /* a CUDA call or kernel launch failed */
   MOE_ERR_TIMEOUT = 4,   /* a device-side wait gave up (reported by moe_nvfp4_check_status) */
-  MOE_ERR_WORKSPACE = 5  /* workspace smaller than moe_nvfp4_layer_workspace_size() */
+  MOE_ERR_WORKSPACE = 5, /* workspace smaller than moe_nvfp4_layer_workspace_size() */
+  MOE_ERR_PAGES = 6      /* the paged cache has too few free pages (moe_attention.h; reported by
+                            moe_nvfp4_check_status) */
 };
 
 /* Token-scale layouts (the e4m3 scales of quantized activation rows). Both
@@ -148,7 +150,8 @@ const char* moe_nvfp4_error_string(int status);
 
 /* Reads and clears the device-side status word of the current device after
  * synchronizing `stream`: MOE_OK, or MOE_ERR_TIMEOUT if a kernel's bounded
- * wait gave up since the last check (its outputs are then invalid). Returns
+ * wait gave up since the last check (its outputs are then invalid), or what a
+ * cache operator of moe_attention.h found on the device. Returns
  * MOE_ERR_CUDA if the synchronization itself fails. The word's device address
  * is looked up on a device's first call and kept for the life of the process:
  * it is not valid after the device's context is reset (cudaDeviceReset). */

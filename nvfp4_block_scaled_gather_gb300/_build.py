@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_nvfp4.so")
-SOURCES = ["moe_api.cu", "moe_kernels.cu", "nvfp4_gemm.cu", "nvfp4_gemv.cu", "moe_static.cu"]
+SOURCES = ["moe_api.cu", "moe_kernels.cu", "nvfp4_gemm.cu", "nvfp4_gemv.cu", "moe_static.cu",
+           "attention_api.cu", "attention.cu", "kv_pages.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -1,0 +1,74 @@
+// Host-side launchers of the attention operators; arguments are validated by
+// attention_api.cu before these are called.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime_api.h>
+
+#include "moe_attention.h"
+
+namespace moe {
+
+constexpr int kMaxGroup = 128;   // query heads per kv head
+constexpr int kMaxHeadDim = 128;
+
+// Rows of heads, 16-bit elements.
+struct Heads {
+  uint16_t* p;
+  long long ts, hs;  // token and head strides, elements
+};
+
+// ------------------------------ pages (kv_pages.cu) ------------------------------
+// Scratch of the upkeep calls, carved from the caller's workspace: a list of
+// page copies (src < 0: none), its count, and for compaction the new id of
+// every page. keep uses new_len in the same place as src.
+struct KvWs {
+  int* count;   // copies in the list
+  int* src;     // [entries]
+  int* dst;     // [entries]
+  int* rows;    // [entries] rows to copy
+  int* moved;   // [n_pages]
+  size_t bytes;
+};
+inline int kv_ws_entries(const moe_kv_cache_t& c) { return c.n_pages > c.max_seqs ? c.n_pages : c.max_seqs; }
+KvWs kv_carve(void* base, const moe_kv_cache_t& c);
+
+cudaError_t launch_kv_extend(const moe_kv_cache_t& c, const int* seqs, const int* add, int n, const KvWs& ws,
+                             int* status, cudaStream_t s);
+cudaError_t launch_kv_append(const moe_kv_cache_t& c, int layer, const int* seqs, const int* cu, int n, int total,
+                             const Heads& k, const Heads& v, int* status, cudaStream_t s);
+cudaError_t launch_kv_fork(const moe_kv_cache_t& c, const int* src, const int* dst, int n, int* status,
+                           cudaStream_t s);
+cudaError_t launch_kv_truncate(const moe_kv_cache_t& c, const int* seqs, const int* new_len, int n, int* status,
+                               cudaStream_t s);
+cudaError_t launch_kv_keep(const moe_kv_cache_t& c, const int* seqs, const int* drafted, const int* keep, int max_keep,
+                           const int* kept, int n, const KvWs& ws, int* status, cudaStream_t s);
+cudaError_t launch_kv_copy_pages(const moe_kv_cache_t& c, const int* src, const int* dst, int n, int* status,
+                                 cudaStream_t s);
+cudaError_t launch_kv_compact(const moe_kv_cache_t& c, const KvWs& ws, cudaStream_t s);
+cudaError_t launch_tree_mask(const int* parents, const int* cu, int n, int total, int* mask, int words, int* status,
+                             cudaStream_t s);
+
+// ---------------------------- attention (attention.cu) ----------------------------
+// One call: keys and values either packed rows (pages == null: k, v, cu_k) or
+// the planes of a paged cache.
+struct AttnArgs {
+  Heads q, k, v, out;
+  float* lse;               // may be null
+  const int* cu_q;          // [n + 1]
+  const int* cu_k;          // [n + 1], packed rows
+  int n, total_q, total_k;
+  int heads_q, heads_kv, head_dim;
+  float scale;
+  // paged cache
+  const int* seqs;          // [n]
+  const int* table;
+  const int* length;
+  int paged, max_seqs, max_pages, n_pages, page_size;
+  const int* mask;          // tree bits, or null (chain)
+  int mask_words;
+  int* status;
+};
+cudaError_t launch_attention(const AttnArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace moe

@@ -27,7 +27,8 @@ int current_device() {
   return dev;
 }
 
-// Device address of g_status_word on the current device (set up once per device).
+}  // namespace
+
 int* status_ptr() {
   const int dev = current_device();
   if (dev < 0) return nullptr;
@@ -39,6 +40,8 @@ int* status_ptr() {
   }
   return g_status_ptr[dev];
 }
+
+namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -161,6 +164,7 @@ const char* moe_nvfp4_error_string(int status) {
     case MOE_ERR_CUDA: return "CUDA error";
     case MOE_ERR_TIMEOUT: return "device wait timed out";
     case MOE_ERR_WORKSPACE: return "workspace too small";
+    case MOE_ERR_PAGES: return "out of cache pages";
     default: return "unknown status";
   }
 }
