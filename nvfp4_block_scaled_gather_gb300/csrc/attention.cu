@@ -1,9 +1,36 @@
-// Attention over whole prompts and over a paged cache.
+// Attention over whole prompts and over a paged cache, on tcgen05 (sm_103a).
 //
-// One warp per (query token, head): online softmax over the keys that the
-// query sees, in fp32, a lane holding every 32nd element of the head. This is
-// the plainest form that is right for every case; it reads every key once per
-// query and head, so it is bound by that re-reading.
+// For a tile of 128 query rows and a block of 128 keys:
+//   S = Q K^T                     (tensor cores, fp32 in tensor memory)
+//   m' = max(m, rowmax S), P = exp2(c S - c m'), l = l 2^(c m - c m') + rowsum P      with c = scale log2 e
+//   O = O 2^(c m - c m') + P V    (tensor cores, P in 16 bits from tensor memory)
+// and at the end out = O / l. One pass over the keys; S and P never leave the
+// SM. P is rounded to 16 bits because the tensor cores take it so: its error
+// is that of the output's own rounding. m follows the running maximum lazily:
+// as long as no score of the row exceeds m by 8 powers of two, P <= 256 is
+// held against the old m (exact: the factor cancels in O / l) and O is not
+// touched.
+//
+//  * A query row is a (token, head of the group): the heads that share a kv
+//    head fill a tile together (128 / group tokens a tile), so a decode step
+//    reads each key once for all of them.
+//  * A work item is a pair of query tiles of one sequence and kv head (or one
+//    tile: few rows) against a run of key blocks. Two softmax warpgroups work
+//    in turn: with two tiles each has its own over the same blocks; with one
+//    tile each has every other block, and they are joined at the end.
+//  * Long sequences with few rows are cut into pieces (cut_of), whose partial
+//    O, m, l a second kernel joins in order.
+//  * Persistent CTAs, one per SM, walk the items; each sequence's later tiles
+//    (the longer ones) first.
+//  * Warp roles: warps 0-3 and 4-7 softmax, 8-9 load (16-byte cp.async copies
+//    into the 128-byte swizzle, any page size, zeros past the end), warp 10
+//    issues the MMAs. A ring of 128-row tiles carries K and V.
+//  * Blocks in which some row sees a key that another does not are masked, and
+//    values there that are not finite are zeroed before the MMA (0 * NaN would
+//    reach rows that do not see them); the rows that do see them get them
+//    added at the end.
+//  * Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT,
+//    drains its copies and MMAs, frees tensor memory and returns.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -18,108 +45,918 @@
 namespace moe {
 namespace {
 
+constexpr int kTile = 128;       // query rows of a tile, keys of a block
+constexpr int kThreads = 384;    // warps 0-3 and 4-7 softmax, 8-9 load, 10 MMA, 11 none
+constexpr int kLoaders = 64;
+constexpr int kGroups = 64;      // sequences are counted in this many runs
+constexpr int kItems = 4;        // work items between the loader and the other roles
+constexpr int kItemReaders = 1 + 8 + 2;  // MMA thread, softmax warps, loader warps
+constexpr int kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // S (and P over it) and O of each softmax warpgroup, 128 columns apart
+constexpr int kHeader = 3072;
+constexpr float kLazy = 8.0f;    // powers of two that a score may exceed the running maximum by
+
+template <int DP>
+struct Sizes {
+  static constexpr int tile = kTile * DP * 2;       // bytes of 128 rows
+  static constexpr int stages = DP == 128 ? 5 : 8;  // 160 KB, 128 KB in flight
+  static constexpr int smem = 2 * tile + stages * tile + kHeader;
+};
+
+// ------------------------------- PTX helpers --------------------------------
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// 16 bytes global -> shared through L2; zeros where there is no source.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// One arrival on the barrier once all of this thread's earlier copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D (tensor memory) += A B, 16-bit operands, A and B in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes (a thread: its row's 32 values).
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptors, 128-byte swizzle (16-byte piece c of row r
+// at piece c ^ (r % 8) of its 128 bytes), descriptor version 1, swizzle mode
+// 2. A tile of 128 rows is stored as halves of 64 columns, 128 bytes a row.
+// K-major (Q and K: the head dimension is summed over): 8-row groups 1024
+// bytes apart (stride offset).
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// MN-major (V: the rows are summed over): 64-column halves 128 * 128 bytes
+// apart (leading offset), 8-row groups 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((kTile * 128) >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor, kind::f16: fp32 accumulators, both operands bf16 or
+// both fp16, M = 128, N = n; B MN-major if mn.
+__device__ __forceinline__ uint32_t idesc_f16(int type, int n, bool mn) {
+  const uint32_t f = type == MOE_BF16 ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kTile >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int kType>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (kType == MOE_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 template <int kType>
 __device__ __forceinline__ float to_f32(uint16_t bits) {
   return kType == MOE_BF16 ? __bfloat162float(__ushort_as_bfloat16(bits)) : __half2float(__ushort_as_half(bits));
 }
+// Clears the halves of a word that are not finite; whether there were any.
 template <int kType>
-__device__ __forceinline__ uint16_t from_f32(float x) {
-  return kType == MOE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+__device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
+  constexpr uint32_t kLo = kType == MOE_BF16 ? 0x7F80u : 0x7C00u, kHi = kLo << 16;
+  const bool lo = (w & kLo) == kLo, hi = (w & kHi) == kHi;
+  if (lo) w &= 0xFFFF0000u;
+  if (hi) w &= 0x0000FFFFu;
+  return lo || hi;
 }
 
 __device__ __forceinline__ void report(int* status, int what) { atomicCAS(status, 0, what); }
 
+// ------------------------------- bounded waits -------------------------------
+struct Ctl {
+  volatile int* abort_flag;
+  int* status;
+};
+constexpr long long kBudget = 2000000000LL;  // clock cycles of one wait, about a second
+
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl c) {
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*c.abort_flag) return false;
+    if (clock64() - t0 > kBudget) {
+      *c.abort_flag = 1;
+      atomicExch(c.status, (int)MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+// False if this or another role gave up.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ctl& c) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, c);
+}
+
+// ---------------------------------- the plan ----------------------------------
+struct Seq {
+  int first, nq;   // queries: first row, count
+  int k0, nk;      // keys: first packed row or row of the table, count
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+  Seq s;
+  s.first = max(ld_cg(a.cu_q + b), 0);
+  s.nq = max(min(ld_cg(a.cu_q + b + 1), a.total_q) - s.first, 0);
+  s.nk = 0;
+  if (a.paged) {
+    s.k0 = ld_cg(a.seqs + b);
+    if (s.k0 >= 0 && s.k0 < a.max_seqs) {
+      s.nk = ld_cg(a.length + s.k0);
+      if (s.nk < 0 || (long long)s.nk > (long long)a.max_pages * a.page_size) {
+        s.nk = 0;
+        report(a.status, MOE_ERR_INVALID);
+      }
+    } else {
+      s.k0 = 0;
+      if (s.nq > 0) report(a.status, MOE_ERR_INVALID);
+    }
+  } else {
+    s.k0 = max(ld_cg(a.cu_k + b), 0);
+    s.nk = max(min(ld_cg(a.cu_k + b + 1), a.total_k) - s.k0, 0);
+  }
+  return s;
+}
+
+struct Shape {  // of a sequence's work
+  int pairs;    // query tile pairs
+  Cut cut;
+  long long part_rows;
+};
+__device__ __forceinline__ Shape shape_of(const AttnArgs& a, const Seq& s, int tokens_per_tile) {
+  Shape w;
+  w.pairs = (s.nq + 2 * tokens_per_tile - 1) / (2 * tokens_per_tile);
+  const int blocks = (s.nk + kTile - 1) / kTile;
+  w.cut = a.part_o && s.nq > 0 ? cut_of(blocks, (long long)w.pairs * a.heads_kv) : Cut{1, blocks};
+  w.part_rows = w.cut.pieces > 1 ? (long long)s.nq * a.heads_q * w.cut.pieces : 0;
+  return w;
+}
+
+struct __align__(16) Item {
+  int first, tokens;      // first query row (token) of the pair, its tokens
+  int i0, nq;             // place of the first token in its sequence, the sequence's queries
+  int k0, nk;             // as Seq
+  int b0, blocks;         // run of key blocks
+  int kvh, two;           // kv head; 1: two tiles
+  int pieces, end;        // pieces of the sequence; 1: no more items (nothing else holds)
+  long long part;         // first partial row of the piece
+  int rows, piece;        // the sequence's partial rows per piece; which piece
+};
+static_assert(sizeof(Item) == 64, "four 16-byte reads");
+
+// How many of the first keys a query sees: all up to its own (chain), or those
+// before the drafted ones (tree; the rest is in its bits).
+__device__ __forceinline__ int limit_of(const AttnArgs& a, int nk, int nq, int i) {
+  const int l = nk - nq + (a.mask ? 0 : i + 1);
+  return min(max(l, 0), nk);
+}
+
+// Bits of the keys pos .. pos + 31 that query i (row t) of the sequence sees.
+__device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, int t, int nk, int nq, int limit, int pos) {
+  const int n = limit - pos;
+  uint32_t w = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+  if (!a.mask) return w;
+  const int j = pos - (nk - nq);  // place of key pos among the drafted
+  if (j <= -32 || j >= nq) return w;
+  const int* row = a.mask + (long long)t * a.mask_words;
+  uint32_t bits;
+  if (j < 0) {
+    bits = (uint32_t)ld_cg(row) << -j;
+  } else {
+    const int i = j >> 5;
+    const uint32_t lo = i < a.mask_words ? (uint32_t)ld_cg(row + i) : 0u;
+    const uint32_t hi = i + 1 < a.mask_words ? (uint32_t)ld_cg(row + i + 1) : 0u;
+    bits = __funnelshift_r(lo, hi, j & 31);
+  }
+  const int left = nq - j;  // drafted tokens from here on
+  if (left < 32) bits &= (1u << left) - 1u;
+  return w | bits;
+}
+__device__ __forceinline__ bool sees_any(const AttnArgs& a, int t, int nk, int nq, int limit) {
+  bool any = limit > 0;
+  if (a.mask && !any)
+    for (int pos = 0; pos < nk; pos += 32) any |= seen_bits(a, t, nk, nq, limit, pos) != 0;
+  return any;
+}
+
+// Place in the ring of an item's tiles (after the item's first): with two
+// query tiles K0 V0 K1 V1 ..., with one K0 K1 V0 K2 V1 ... (K runs ahead by
+// one block, as both softmax warpgroups start on a block each).
+__device__ __forceinline__ int k_place(int two, int b) { return two ? 2 * b : (b == 0 ? 0 : 2 * b - 1); }
+__device__ __forceinline__ int v_place(int two, int b, int n) {
+  return two ? 2 * b + 1 : (b < n - 1 ? 2 * b + 2 : 2 * n - 1);
+}
+
+template <int kType, int DP>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
+  using Sz = Sizes<DP>;
+  constexpr int kStages = Sz::stages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the swizzle needs it; the same for every thread
+    if (threadIdx.x == 0) report(a.status, MOE_ERR_CUDA);
+    return;
+  }
+  const uint32_t sQ = smem_u32(smem), sKV = sQ + 2 * Sz::tile;
+  uint8_t* head = smem + (2 + kStages) * Sz::tile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(head);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (8 + s); };
+  auto qfull_bar = [&](int s) { return bar0 + 8u * (16 + s); };
+  auto qempty_bar = [&](int s) { return bar0 + 8u * (18 + s); };
+  auto sfull_bar = [&](int w) { return bar0 + 8u * (20 + w); };
+  auto pfull_bar = [&](int w) { return bar0 + 8u * (22 + w); };
+  auto ofull_bar = [&](int w) { return bar0 + 8u * (24 + w); };
+  auto oempty_bar = [&](int w) { return bar0 + 8u * (26 + w); };
+  const uint32_t join_bar = bar0 + 8u * 28, drain_bar = bar0 + 8u * 29;
+  auto ifull_bar = [&](int i) { return bar0 + 8u * (30 + i); };
+  auto iempty_bar = [&](int i) { return bar0 + 8u * (34 + i); };
+  // after the barriers (304 bytes)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 320);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 324);
+  volatile int* poisoned = reinterpret_cast<volatile int*>(head + 336);    // [kItems]
+  Item* s_item = reinterpret_cast<Item*>(head + 384);                      // [kItems]
+  float2* s_ml = reinterpret_cast<float2*>(head + 640);                    // [128]
+  long long* s_part = reinterpret_cast<long long*>(head + 1664);           // [kGroups + 1]
+  int* s_count = reinterpret_cast<int*>(head + 2192);                      // [kGroups + 1]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(full_bar(s), kLoaders);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(qfull_bar(w), kLoaders);
+      mbar_init(qempty_bar(w), 1);
+      mbar_init(sfull_bar(w), 1);
+      mbar_init(pfull_bar(w), 128);
+      mbar_init(ofull_bar(w), 1);
+      mbar_init(oempty_bar(w), 128);
+    }
+    mbar_init(join_bar, 128);
+    mbar_init(drain_bar, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(ifull_bar(i), 1);
+      mbar_init(iempty_bar(i), kItemReaders);
+      poisoned[i] = 0;
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 10) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  pdl_wait();
+  pdl_trigger();
+  const int group = a.heads_q / a.heads_kv;
+  const int tpt = kTile / group;  // tokens of a tile
+  const int per = (a.n + kGroups - 1) / kGroups;  // sequences of a run
+  if (tid < kGroups) {
+    int count = 0;
+    long long part = 0;
+    for (int b = tid * per; b < min((tid + 1) * per, a.n); ++b) {
+      const Shape w = shape_of(a, seq_of(a, b), tpt);
+      count += w.pairs * w.cut.pieces;
+      part += w.part_rows;
+    }
+    s_count[tid] = count;
+    s_part[tid] = part;
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive sums, two runs a lane
+    const int c0 = s_count[2 * lane], c1 = s_count[2 * lane + 1];
+    const long long p0 = s_part[2 * lane], p1 = s_part[2 * lane + 1];
+    int c = c0 + c1;
+    long long p = p0 + p1;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(~0u, c, o);
+      const long long y = __shfl_up_sync(~0u, p, o);
+      if (lane >= o) {
+        c += x;
+        p += y;
+      }
+    }
+    s_count[2 * lane] = c - c0 - c1;
+    s_count[2 * lane + 1] = c - c1;
+    s_part[2 * lane] = p - p0 - p1;
+    s_part[2 * lane + 1] = p - p1;
+    if (lane == 31) s_count[kGroups] = c;
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Ctl ctl{abort_flag, a.status};
+
+  // Every role takes the items from the ring in order.
+  int seq_no = 0;
+  Item it = {};
+  auto next_item = [&](bool whole_warp) -> bool {
+    const int i = seq_no % kItems;
+    if (!wait_bar(ifull_bar(i), (seq_no / kItems) & 1, ctl)) return false;
+    it = s_item[i];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(iempty_bar(i));
+    ++seq_no;
+    return it.end == 0;
+  };
+
+  // 168 registers a thread at launch (3 x 128 threads): 2 x 208 + 88 = 3 x 168
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp < 10) {
+    // ================================ loader ================================
+    const int lw = warp - 8;
+    const int total = s_count[kGroups] * a.heads_kv;
+    int next = blockIdx.x, ring = 0, qring = 0;
+    bool ok = true;
+    // 32 rows (half h of this warp's 64) into a tile at `dst`: this lane's row
+    // starts at element `at` of base, or is zero (at < 0); columns past the
+    // head dimension are zero.
+    auto load_rows = [&](uint32_t dst, const uint16_t* base, int h, long long at) {
+      constexpr int kChunks = DP / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
+      const int c = lane % kChunks, sub = lane / kChunks;
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += kRows) {
+        const int r = r0 + sub;
+        const long long from = __shfl_sync(~0u, at, r);
+        const bool there = from >= 0 && c * 8 < a.head_dim;
+        const int row = lw * 64 + h * 32 + r;
+        cp_async16(dst + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                   base + (there ? from + c * 8 : 0), there);
+      }
+    };
+    while (ok) {
+      // warp 8 decodes the next item and hands it out
+      if (lw == 0) {
+        const int i = seq_no % kItems;
+        ok = wait_bar(iempty_bar(i), ((seq_no / kItems) & 1) ^ 1, ctl);
+        if (ok) {
+          Item x = {};
+          x.end = next >= total;
+          if (!x.end) {
+            const int kvh = next % a.heads_kv;
+            int u = next / a.heads_kv, g = 0;
+            for (int step = kGroups / 2; step; step >>= 1)
+              if (s_count[g + step] <= u) g += step;
+            u -= s_count[g];
+            long long part = s_part[g];
+            int b = g * per;
+            Seq s = seq_of(a, b);
+            Shape w = shape_of(a, s, tpt);
+            while (u >= w.pairs * w.cut.pieces && b + 1 < a.n) {
+              u -= w.pairs * w.cut.pieces;
+              part += w.part_rows;
+              s = seq_of(a, ++b);
+              w = shape_of(a, s, tpt);
+            }
+            const int pair = max(w.pairs - 1 - u / w.cut.pieces, 0);
+            x.piece = u % w.cut.pieces;
+            x.i0 = pair * 2 * tpt;
+            x.first = s.first + x.i0;
+            x.tokens = min(2 * tpt, s.nq - x.i0);
+            x.two = x.tokens > tpt;
+            x.nq = s.nq;
+            x.k0 = s.k0;
+            x.nk = s.nk;
+            x.kvh = kvh;
+            // the keys that any row of the pair sees end here
+            const int keys = a.mask ? s.nk : limit_of(a, s.nk, s.nq, x.i0 + x.tokens - 1);
+            x.b0 = x.piece * w.cut.blocks;
+            x.blocks = max(0, min((keys + kTile - 1) / kTile - x.b0, w.cut.blocks));
+            x.pieces = w.cut.pieces;
+            x.rows = s.nq * a.heads_q;
+            x.part = part + (long long)x.piece * x.rows;
+          }
+          if (lane == 0) {
+            s_item[i] = x;
+            mbar_arrive(ifull_bar(i));
+          }
+          next += gridDim.x;
+        }
+      }
+      if (!next_item(true)) {
+        ok = it.end != 0 && *abort_flag == 0;
+        break;
+      }
+      const int n = it.blocks;
+      if (n == 0) continue;
+      // the query tiles
+      for (int q = 0; q < 1 + it.two; ++q, ++qring) {
+        const int slot = qring & 1;
+        if (!wait_bar(qempty_bar(slot), ((qring >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
+        for (int h = 0; h < 2; ++h) {
+          const int r = lw * 64 + h * 32 + lane, token = r / group;
+          long long at = -1;
+          if (token < tpt && q * tpt + token < it.tokens)
+            at = (long long)(it.first + q * tpt + token) * a.q.ts + (it.kvh * group + r % group) * a.q.hs;
+          load_rows(sQ + slot * Sz::tile, a.q.p, h, at);
+        }
+        cp_async_arrive(qfull_bar(slot));
+      }
+      if (!ok) break;
+      // row of the packed keys or of the cache's planes that holds key `pos`, or -1
+      auto row_of = [&](int block, int h) -> int {
+        const int pos = (it.b0 + block) * kTile + lw * 64 + h * 32 + lane;
+        if (block >= n || pos >= it.nk) return -1;
+        if (!a.paged) return it.k0 + pos;
+        const int at = pos / a.page_size;
+        const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + at);
+        if (p < 0 || p >= a.n_pages) {
+          report(a.status, MOE_ERR_INVALID);
+          return -1;
+        }
+        return p * a.page_size + (pos - at * a.page_size);
+      };
+      const int lim = limit_of(a, it.nk, it.nq, it.i0);  // the least that any row of the pair sees
+      auto load_tile = [&](const Heads& x, int2 row, bool clean, int item_no) -> bool {
+        const int slot = ring % kStages;
+        if (!wait_bar(empty_bar(slot), ((ring / kStages) & 1) ^ 1, ctl)) return false;
+        const uint32_t dst = sKV + slot * Sz::tile;
+        load_rows(dst, x.p, 0, row.x < 0 ? -1 : row.x * x.ts + it.kvh * x.hs);
+        load_rows(dst, x.p, 1, row.y < 0 ? -1 : row.y * x.ts + it.kvh * x.hs);
+        if (!clean) {
+          cp_async_arrive(full_bar(slot));
+        } else {
+          // some row does not see all of these: values that are not finite are
+          // cleared (each thread those that it copied), and the item is marked
+          cp_async_wait_all();
+          bool found = false;
+          constexpr int kChunks = DP / 8, kRows = 32 / kChunks;
+          const int c = lane % kChunks;
+          for (int r0 = 0; r0 < 64; r0 += kRows) {
+            const int rr = lw * 64 + r0 + lane / kChunks;
+            const uint32_t at = dst + (c >> 3) * (kTile * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+            uint4* p = reinterpret_cast<uint4*>(smem + (at - sQ));
+            uint4 v = *p;
+            bool f = clear_nonfinite<kType>(v.x);
+            f |= clear_nonfinite<kType>(v.y);
+            f |= clear_nonfinite<kType>(v.z);
+            f |= clear_nonfinite<kType>(v.w);
+            if (f) *p = v;
+            found |= f;
+          }
+          if (found) poisoned[item_no % kItems] = item_no + 1;
+          fence_proxy_async_shared();
+          mbar_arrive(full_bar(slot));
+        }
+        ++ring;
+        return true;
+      };
+      const int item_no = seq_no - 1;
+      auto is_edge = [&](int block) { return (it.b0 + block + 1) * kTile > lim && lim < it.nk; };
+      auto rows_of = [&](int block) { return make_int2(row_of(block, 0), row_of(block, 1)); };
+      int2 cur = rows_of(0), nxt = rows_of(1);
+      ok = load_tile(a.k, cur, false, item_no);
+      if (it.two) {
+        for (int b = 0; b < n && ok; ++b) {
+          ok = load_tile(a.v, cur, is_edge(b), item_no);
+          cur = nxt;
+          nxt = rows_of(b + 2);
+          if (ok && b + 1 < n) ok = load_tile(a.k, cur, false, item_no);
+        }
+      } else {
+        for (int b = 0; b < n && ok; ++b) {
+          const int2 row = cur;
+          cur = nxt;
+          if (b + 1 < n) ok = load_tile(a.k, cur, false, item_no);
+          nxt = rows_of(b + 2);
+          if (ok) ok = load_tile(a.v, row, is_edge(b), item_no);
+        }
+      }
+    }
+    if (!ok || *abort_flag) cp_async_wait_all();  // nothing of ours may be in flight at exit
+  } else {
+    // ============================== MMA issuer ==============================
+    if (warp == 10 && lane == 0) {
+      const uint32_t id_s = idesc_f16(kType, kTile, false), id_o = idesc_f16(kType, DP, true);
+      int ring = 0, qring = 0, uses[2] = {0, 0}, steps_done[2] = {0, 0};
+      bool ok = true;
+      while (ok && next_item(false)) {
+        const int n = it.blocks, two = it.two;
+        if (n == 0) continue;
+        const int steps = two ? 2 * n : n;
+        auto wait_tile = [&](int place) { return wait_bar(full_bar((ring + place) % kStages), ((ring + place) / kStages) & 1, ctl); };
+        auto score = [&](int t) -> bool {
+          const int w = t & 1, b = two ? t >> 1 : t, place = k_place(two, b), tile = two ? w : 0;
+          if ((two ? t < 2 : t == 0) && !wait_bar(qfull_bar((qring + tile) & 1), ((qring + tile) >> 1) & 1, ctl)) return false;
+          if ((!two || w == 0) && !wait_tile(place)) return false;
+          tc_fence_after();
+          fence_proxy_async_shared();  // the tiles were written by cp.async
+          const int slot = (ring + place) % kStages;
+          const uint64_t qd = desc_kmajor(sQ + ((qring + tile) & 1) * Sz::tile), kd = desc_kmajor(sKV + slot * Sz::tile);
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint64_t off = (uint64_t)((k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2);
+            tc_mma_ss(tmem + kColS + w * 128, qd + off, kd + off, id_s, k != 0);
+          }
+          tc_commit(sfull_bar(w));
+          if (!two || w == 1) tc_commit(empty_bar(slot));
+          if (t >= steps - 1 - two) tc_commit(qempty_bar((qring + tile) & 1));
+          return true;
+        };
+        auto values = [&](int t) -> bool {
+          const int w = t & 1, b = two ? t >> 1 : t, place = v_place(two, b, n);
+          if (t < 2) {
+            if (!wait_bar(oempty_bar(w), (uses[w] & 1) ^ 1, ctl)) return false;
+            ++uses[w];
+          }
+          if (!wait_bar(pfull_bar(w), steps_done[w] & 1, ctl)) return false;
+          ++steps_done[w];
+          if ((!two || w == 0) && !wait_tile(place)) return false;
+          tc_fence_after();
+          fence_proxy_async_shared();
+          const int slot = (ring + place) % kStages;
+          const uint64_t vd = desc_mnmajor(sKV + slot * Sz::tile);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
+            tc_mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o,
+                      t >= 2 || k != 0);
+          if (!two || w == 1) tc_commit(empty_bar(slot));
+          if (t >= steps - 2) tc_commit(ofull_bar(w));
+          return true;
+        };
+        ok = score(0) && (steps < 2 || score(1));
+        for (int t = 0; t < steps && ok; ++t) ok = values(t) && (t + 2 >= steps || score(t + 2));
+        ring += 2 * n;
+        qring += 1 + two;
+      }
+      if (!ok || *abort_flag) {
+        // wait for every MMA issued so far before tensor memory is freed
+        tc_commit(drain_bar);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < kBudget) {
+        }
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // =============================== softmax ===============================
+    const int w = warp >> 2;             // which of the two warpgroups
+    const int r = tid & 127;             // row of the tile = lane of tensor memory
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = lanes + kColS + w * 128, tO = lanes + kColO + w * 128;
+    const float c = a.scale * 1.4426950408889634f;
+    int steps_done = 0, uses = 0, uses1 = 0, joins = 0;  // uses of this O, of the second one
+    bool ok = true;
+    while (ok && next_item(true)) {
+      const int n = it.blocks, two = it.two;
+      const int steps = two ? 2 * n : n;
+      const int token = r / group, tok = (two ? w * tpt : 0) + token;  // in the tile, in the pair
+      const bool valid = token < tpt && tok < it.tokens;
+      const int i = it.i0 + tok, t_row = it.first + tok;
+      const int limit = valid ? limit_of(a, it.nk, it.nq, i) : 0;
+      const int lim = limit_of(a, it.nk, it.nq, it.i0 + (two ? w * tpt : 0));  // the least of the tile's rows
+      float m = -INFINITY, l = 0.0f;  // m in units of the raw scores
+      for (int t = w; t < steps; t += 2) {
+        const int pos = (it.b0 + (two ? t >> 1 : t)) * kTile;
+        const bool edge = pos + kTile > lim;  // some row does not see all of the block
+        uint32_t bits[kTile / 32];
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < kTile; j += 32)
+            bits[j / 32] = valid ? seen_bits(a, t_row, it.nk, it.nq, limit, pos + j) : 0u;
+        }
+        if (!wait_bar(sfull_bar(w), steps_done & 1, ctl)) { ok = false; break; }
+        ++steps_done;
+        tc_fence_after();
+        uint32_t s[kTile];
+#pragma unroll
+        for (int j = 0; j < kTile; j += 32) tc_ld32(tS + j, s + j);
+        tc_wait_ld();
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if (!((bits[j / 32] >> (j % 32)) & 1u)) s[j] = 0xFF800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(s[u]);
+#pragma unroll
+        for (int j = 4; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
+        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        const bool move = top > m && !((top - m) * c <= kLazy);
+        if (t >= 2 && __any_sync(~0u, move)) {
+          // S(t) is complete, so is every earlier MMA: O can be rescaled
+          const float f = move ? ex2((m - top) * c) : 1.0f;
+          l *= f;
+          uint32_t o[32];
+#pragma unroll 1
+          for (int j = 0; j < DP; j += 32) {
+            tc_ld32(tO + j, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc_st32(tO + j, o);
+          }
+        }
+        if (move) m = top;
+        const float base = m == -INFINITY ? 0.0f : -m * c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < kTile; h += 64) {
+          uint32_t p[32];
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(s[h + j]), c, base));
+            const float p1 = ex2(fmaf(__uint_as_float(s[h + j + 1]), c, base));
+            sum[j & 2] += p0;
+            sum[(j & 2) + 1] += p1;
+            p[j / 2] = pack2<kType>(p0, p1);
+          }
+          tc_st32(tS + h / 2, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(pfull_bar(w));
+      }
+      if (!ok) break;
+      // ------------------------------ epilogue ------------------------------
+      const bool other = !two && n > 1;  // one tile: the second warpgroup holds half of the result
+      if (!two && w == 1) {
+        if (n > 1) {
+          // not before the last item's result has been read
+          if (!wait_bar(oempty_bar(1), (uses & 1) ^ 1, ctl)) break;
+          ++uses;
+          s_ml[r] = make_float2(m, l);
+          mbar_arrive(join_bar);
+        }
+        continue;
+      }
+      float f0 = 1.0f, f1 = 0.0f;
+      if (n > 0) {
+        if (!wait_bar(ofull_bar(w), uses & 1, ctl)) break;
+        ++uses;
+        if (other) {
+          if (!wait_bar(ofull_bar(1), uses1 & 1, ctl) || !wait_bar(join_bar, joins & 1, ctl)) break;
+          ++joins;
+          const float2 ml = s_ml[r];
+          const float top = fmaxf(m, ml.x);
+          f0 = m == -INFINITY ? 1.0f : ex2((m - top) * c);
+          f1 = ml.x == -INFINITY ? 1.0f : ex2((ml.x - top) * c);
+          l = l * f0 + ml.y * f1;
+          m = top;
+        }
+        uses1 += two || other;
+        tc_fence_after();
+      }
+      const bool bad = n > 0 && poisoned[(seq_no - 1) % kItems] == seq_no;
+      const bool cut = it.pieces > 1;
+      const int h = it.kvh * group + r % group;
+      const long long part = it.part + (long long)i * a.heads_q + h;
+      const bool keep = cut && valid && part < a.part_rows;
+      // a row that sees no key gives 0; one whose scores are all -inf has no value
+      float inv = 1.0f;
+      if (!cut) inv = l != 0.0f ? 1.0f / l : (valid && sees_any(a, t_row, it.nk, it.nq, limit) ? NAN : 0.0f);
+      uint16_t* out = a.out.p + (long long)t_row * a.out.ts + (long long)h * a.out.hs;
+      uint32_t o[32];
+      for (int j = 0; j < DP; j += 32) {
+        if (n > 0) {
+          tc_ld32(tO + j, o);
+          tc_wait_ld();
+          if (other) {
+            uint32_t o1[32];
+            tc_ld32(tO + 128 + j, o1);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+          }
+          if (l == 0.0f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (bad && valid) {
+          // add the values that are not finite, for the keys that this row sees
+          const int from = max(it.b0, limit_of(a, it.nk, it.nq, it.i0) / kTile) * kTile;
+          for (int pos = from; pos < min((it.b0 + n) * kTile, it.nk); ++pos) {
+            if (!((seen_bits(a, t_row, it.nk, it.nq, limit, pos & ~31) >> (pos & 31)) & 1u)) continue;
+            long long row = (long long)it.k0 + pos;
+            if (a.paged) {
+              const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + pos / a.page_size);
+              if (p < 0 || p >= a.n_pages) continue;
+              row = (long long)p * a.page_size + pos % a.page_size;
+            }
+            const uint16_t* v = a.v.p + row * a.v.ts + (long long)it.kvh * a.v.hs;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (j + e < a.head_dim) {
+                const float x = to_f32<kType>(v[j + e]);
+                if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+              }
+          }
+        }
+        if (j + 32 >= DP && n > 0) {  // O has been read
+          tc_fence_before();
+          mbar_arrive(oempty_bar(w));
+          if (other) mbar_arrive(oempty_bar(1));
+        }
+        if (keep) {
+          float4* to = reinterpret_cast<float4*>(a.part_o + part * a.head_dim + j);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            if (j + e < a.head_dim)
+              to[e / 4] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                      __uint_as_float(o[e + 3]));
+        } else if (!cut && valid) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            if (j + e < a.head_dim) {
+              uint4 v;
+              v.x = pack2<kType>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+              v.y = pack2<kType>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+              v.z = pack2<kType>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+              v.w = pack2<kType>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+              *reinterpret_cast<uint4*>(out + j + e) = v;
+            }
+        }
+      }
+      if (valid) {
+        const long long row = (long long)t_row * a.heads_q + h;
+        if (cut) {
+          if (keep) a.part_ml[part] = make_float2(m * c, l);
+          else report(a.status, MOE_ERR_INVALID);
+          if (it.piece == 0)
+            a.part_of[row] = make_int4(keep ? (int)part : -1, it.pieces, it.rows, sees_any(a, t_row, it.nk, it.nq, limit));
+        } else {
+          if (a.part_of) a.part_of[row] = make_int4(-1, 0, 0, 0);
+          if (a.lse) a.lse[row] = l != 0.0f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 10) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Joins the pieces of cut sequences, in their order: one warp per query and head.
 template <int kType>
-__global__ void __launch_bounds__(128) attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(w / a.heads_q), h = (int)(w - (long long)t * a.heads_q);
-  if (t >= a.total_q || t < ld_cg(a.cu_q) || t >= ld_cg(a.cu_q + a.n)) return;
-  int lo = 0, hi = a.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ld_cg(a.cu_q + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  const int first = max(ld_cg(a.cu_q + lo), 0), nq = min(ld_cg(a.cu_q + lo + 1), a.total_q) - first;
-  const int i = t - first;
-  if (i >= nq) return;
-  const int kvh = h / (a.heads_q / a.heads_kv);
-  int nk = 0, k0 = 0, seq = 0;
-  if (a.paged) {
-    seq = ld_cg(a.seqs + lo);
-    if (seq >= 0 && seq < a.max_seqs) {
-      nk = ld_cg(a.length + seq);
-      if (nk < 0 || (long long)nk > (long long)a.max_pages * a.page_size) nk = 0;
-    } else if (lane == 0) {
-      report(a.status, MOE_ERR_INVALID);
-    }
-  } else {
-    k0 = max(ld_cg(a.cu_k + lo), 0);
-    nk = max(min(ld_cg(a.cu_k + lo + 1), a.total_k) - k0, 0);
-  }
-  const int context = nk - nq;  // keys before the queries' own
-  constexpr int kPer = kMaxHeadDim / 32;
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.0f;
+  const long long rows = (long long)a.total_q * a.heads_q;
+  for (long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 4LL) {
+    const int t = (int)(row / a.heads_q), h = (int)(row - (long long)t * a.heads_q);
+    if (t < ld_cg(a.cu_q) || t >= ld_cg(a.cu_q + a.n)) continue;
+    const int4 of = ld_cg(a.part_of + row);
+    if (of.x < 0 || of.y <= 1 || of.z <= 0 || of.x + (long long)(of.y - 1) * of.z >= a.part_rows) continue;
+    float top = -INFINITY;
+    for (int i = lane; i < of.y; i += 32) top = fmaxf(top, a.part_ml[of.x + (long long)i * of.z].x);
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int d = lane + 32 * e;
-    q[e] = d < a.head_dim ? to_f32<kType>(a.q.p[t * a.q.ts + h * a.q.hs + d]) * a.scale : 0.0f;
-    o[e] = 0.0f;
-  }
-  bool seen_any = false;
-  for (int j = 0; j < nk; ++j) {
-    const int c = j - context;  // place among the drafted
-    bool seen = c <= i;
-    if (a.mask && c >= 0)
-      seen = c < nq && (c >> 5) < a.mask_words && (ld_cg(a.mask + (long long)t * a.mask_words + (c >> 5)) >> (c & 31)) & 1;
-    if (!seen) continue;
-    long long row = k0 + j;
-    if (a.paged) {
-      const int p = ld_cg(a.table + (long long)seq * a.max_pages + j / a.page_size);
-      if (p < 0 || p >= a.n_pages) {
-        if (lane == 0) report(a.status, MOE_ERR_INVALID);
-        continue;
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+    float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int e = lane * 4;
+    for (int i = 0; i < of.y; ++i) {
+      const long long at = of.x + (long long)i * of.z;
+      const float2 ml = a.part_ml[at];
+      if (ml.y == 0.0f) continue;  // saw nothing
+      const float f = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
+      l += f * ml.y;
+      if (e < a.head_dim) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * a.head_dim + e);
+        o[0] += f * v.x;
+        o[1] += f * v.y;
+        o[2] += f * v.z;
+        o[3] += f * v.w;
       }
-      row = (long long)p * a.page_size + j % a.page_size;
     }
-    seen_any = true;
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int d = lane + 32 * e;
-      if (d < a.head_dim) s += q[e] * to_f32<kType>(a.k.p[row * a.k.ts + kvh * a.k.hs + d]);
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    const float mn = fmaxf(m, s);
-    const float base = mn == -INFINITY ? 0.0f : mn;
-    const float alpha = __expf(m - base), p = __expf(s - base);
-    l = l * alpha + p;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int d = lane + 32 * e;
-      if (d < a.head_dim) o[e] = o[e] * alpha + p * to_f32<kType>(a.v.p[row * a.v.ts + kvh * a.v.hs + d]);
-    }
-    m = mn;
+    const float inv = l != 0.0f ? 1.0f / l : (of.w ? NAN : 0.0f);
+    if (e < a.head_dim)
+      *reinterpret_cast<uint2*>(a.out.p + (long long)t * a.out.ts + (long long)h * a.out.hs + e) =
+          make_uint2(pack2<kType>(o[0] * inv, o[1] * inv), pack2<kType>(o[2] * inv, o[3] * inv));
+    if (a.lse && lane == 0) a.lse[row] = l != 0.0f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int d = lane + 32 * e;
-    if (d < a.head_dim) a.out.p[t * a.out.ts + h * a.out.hs + d] = from_f32<kType>(seen_any ? o[e] / l : 0.0f);
-  }
-  if (a.lse && lane == 0) a.lse[(long long)t * a.heads_q + h] = seen_any ? m + __logf(l) : -INFINITY;
+}
+
+template <int kType, int DP>
+cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s) {
+  cudaError_t err = cudaFuncSetAttribute(attention_kernel<kType, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Sizes<DP>::smem);
+  if (err != cudaSuccess) return err;
+  // no more CTAs than there can be items
+  const int tpt = kTile / (a.heads_q / a.heads_kv);
+  long long items = ((long long)a.total_q / (2 * tpt) + a.n) * a.heads_kv;
+  if (a.part_o) items = items * kSplitItems;
+  const int sms = num_sms();
+  err = launch_pdl(attention_kernel<kType, DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads),
+                   Sizes<DP>::smem, s, a);
+  if (err != cudaSuccess || !a.part_o) return err;
+  const long long blocks = ((long long)a.total_q * a.heads_q + 3) / 4, most = sms * 16LL;
+  return launch_pdl(join_kernel<kType>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(128), 0, s, a);
 }
 
 }  // namespace
 
+AttnWs attention_ws(int n, int total_q, int heads_q, int heads_kv, int head_dim, long long max_keys) {
+  AttnWs w = {};
+  const long long blocks = (max_keys + kTile - 1) / kTile;
+  const Cut most = cut_of((int)blocks, heads_kv);  // one query tile pair: the most pieces
+  const long long rows = (long long)total_q * heads_q;
+  if (most.pieces > 1 && rows > 0) {
+    // a sequence of T pairs has at most 256 T heads_kv rows and, if it is cut,
+    // T heads_kv < kSplitItems and at most kSplitItems / (T heads_kv) + 1 pieces
+    const long long by_seq = (long long)n * 256 * 2 * kSplitItems;
+    w.part_rows = rows * (blocks / kSplitMinBlocks < kSplitItems ? blocks / kSplitMinBlocks : kSplitItems);
+    if (by_seq < w.part_rows) w.part_rows = by_seq;
+    if (w.part_rows > 0x7fffffffLL) w.part_rows = 0x7fffffffLL;
+  }
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  w.o = 0;
+  w.ml = up((size_t)w.part_rows * head_dim * sizeof(float));
+  w.of = w.ml + up((size_t)w.part_rows * sizeof(float2));
+  w.bytes = w.of + up(w.part_rows > 0 ? (size_t)rows * sizeof(int4) : 0);
+  if (w.bytes < 256) w.bytes = 256;
+  return w;
+}
+
 cudaError_t launch_attention(const AttnArgs& a, int dtype, cudaStream_t s) {
-  const long long rows = (long long)a.total_q * a.heads_q;
-  const dim3 grid((unsigned)((rows + 3) / 4));
-  return dtype == MOE_BF16 ? launch_pdl(attention_kernel<MOE_BF16>, grid, dim3(128), 0, s, a)
-                           : launch_pdl(attention_kernel<MOE_FP16>, grid, dim3(128), 0, s, a);
+  if (dtype == MOE_BF16) return a.head_dim <= 64 ? launch_typed<MOE_BF16, 64>(a, s) : launch_typed<MOE_BF16, 128>(a, s);
+  return a.head_dim <= 64 ? launch_typed<MOE_FP16, 64>(a, s) : launch_typed<MOE_FP16, 128>(a, s);
 }
 
 }  // namespace moe

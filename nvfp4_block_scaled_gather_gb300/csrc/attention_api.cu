@@ -192,7 +192,10 @@ int moe_attention_prompt(const moe_heads_t* q, const moe_heads_t* k, const moe_h
 
 size_t moe_attention_cached_workspace_size(const moe_kv_cache_t* cache, int n, int total_q, int heads_q) {
   if (cache_status(cache) != MOE_OK || n < 0 || total_q < 0 || heads_q <= 0) return 0;
-  return 256;
+  if ((long long)total_q * heads_q > (1LL << 30)) return 0;
+  return attention_ws(n, total_q, heads_q, cache->heads_kv, cache->head_dim,
+                      (long long)cache->max_pages * cache->page_size)
+      .bytes;
 }
 
 int moe_attention_cached(const moe_heads_t* q, const moe_kv_cache_t* cache, int layer, const int32_t* seqs,
@@ -233,6 +236,15 @@ int moe_attention_cached(const moe_heads_t* q, const moe_kv_cache_t* cache, int 
   a.page_size = cache->page_size;
   a.mask = mask;
   a.mask_words = mask_words;
+  const AttnWs ws = attention_ws(n, total_q, heads_q, cache->heads_kv, cache->head_dim,
+                                 (long long)cache->max_pages * cache->page_size);
+  if (ws.part_rows > 0) {
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    a.part_o = reinterpret_cast<float*>(base + ws.o);
+    a.part_ml = reinterpret_cast<float2*>(base + ws.ml);
+    a.part_of = reinterpret_cast<int4*>(base + ws.of);
+    a.part_rows = ws.part_rows;
+  }
   a.status = status_ptr();
   if (!a.status) return MOE_ERR_CUDA;
   return status_of(launch_attention(a, cache->dtype, stream));

@@ -9,6 +9,11 @@
 
 namespace moe {
 
+// Device address of the status word on the current device (moe_api.cu; looked
+// up once per device), where kernels report what only they can see; null on a
+// CUDA error.
+int* status_ptr();
+
 constexpr int kMaxGroup = 128;   // query heads per kv head
 constexpr int kMaxHeadDim = 128;
 
@@ -50,8 +55,25 @@ cudaError_t launch_tree_mask(const int* parents, const int* cu, int n, int total
                              cudaStream_t s);
 
 // ---------------------------- attention (attention.cu) ----------------------------
-// One call: keys and values either packed rows (pages == null: k, v, cu_k) or
-// the planes of a paged cache.
+// How a sequence's keys are cut into pieces that are worked on by themselves
+// (128 keys are a block). The cut goes by the sequence alone, so that its
+// results do not depend on the call's other sequences.
+constexpr int kSplitItems = 152;     // pieces x heads x query tiles that one sequence is cut into at most (one a SM)
+constexpr int kSplitMinBlocks = 4;   // blocks of a piece at least
+struct Cut {
+  int pieces, blocks;                // pieces of `blocks` blocks, the last one what is left
+};
+__host__ __device__ inline Cut cut_of(int blocks, long long tiles_and_heads) {
+  long long most = blocks / kSplitMinBlocks;
+  const long long want = (kSplitItems + tiles_and_heads - 1) / tiles_and_heads;
+  if (want < most) most = want;
+  if (most <= 1) return {1, blocks};
+  const int per = (int)((blocks + most - 1) / most);
+  return {(blocks + per - 1) / per, per};
+}
+
+// One call: keys and values either packed rows (paged == 0: cu_k) or the
+// planes of a paged cache.
 struct AttnArgs {
   Heads q, k, v, out;
   float* lse;               // may be null
@@ -68,7 +90,18 @@ struct AttnArgs {
   const int* mask;          // tree bits, or null (chain)
   int mask_words;
   int* status;
+  // partial results of cut sequences (null: no sequence of the call is cut)
+  float* part_o;            // [part_rows, head_dim], not divided by the sum
+  float2* part_ml;          // [part_rows] maximum (in powers of two) and sum
+  int4* part_of;            // [total_q * heads_q] first row, pieces, rows between pieces, whether it sees any key
+  long long part_rows;
 };
+// The partial rows that any call with these bounds can need, and their bytes.
+struct AttnWs {
+  long long part_rows;
+  size_t o, ml, of, bytes;  // offsets and the total
+};
+AttnWs attention_ws(int n, int total_q, int heads_q, int heads_kv, int head_dim, long long max_keys);
 cudaError_t launch_attention(const AttnArgs& a, int dtype, cudaStream_t s);
 
 }  // namespace moe

@@ -34,9 +34,6 @@ inline size_t token_sf_bytes(long long R_max, long long G_max, long long K, int 
 }
 
 int num_sms();  // SM count of the current device (cached per device)
-// Device address of the status word on the current device (looked up once per
-// device), where kernels report what only they can see; null on a CUDA error.
-int* status_ptr();
 
 // Host-side argument checks of moe_nvfp4_layer (everything but the
 // workspace): MOE_OK, MOE_ERR_INVALID or MOE_ERR_SHAPE. T == 0 is valid.
