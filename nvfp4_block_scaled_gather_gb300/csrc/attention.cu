@@ -22,9 +22,12 @@
 //    O, m, l a second kernel joins in order.
 //  * Persistent CTAs, one per SM, walk the items; each sequence's later tiles
 //    (the longer ones) first.
-//  * Warp roles: warps 0-3 and 4-7 softmax, 8-9 load (16-byte cp.async copies
-//    into the 128-byte swizzle, any page size, zeros past the end), warp 10
-//    issues the MMAs. A ring of 128-row tiles carries K and V.
+//  * Warp roles: warps 0-3 and 4-7 softmax; warp 8 hands out the items and
+//    loads tiles by TMA into a ring (128-byte swizzle; a box is the rows of a
+//    page, or all 128); warp 9 cleans values (below); warps 10 and 11 issue the
+//    MMAs of one softmax warpgroup each. Pages whose size is no multiple of 8
+//    rows, and strides of 0, cannot be boxes: there warps 8 and 9 copy the tiles
+//    by 16-byte cp.async.
 //  * Blocks in which some row sees a key that another does not are masked, and
 //    values there that are not finite are zeroed before the MMA (0 * NaN would
 //    reach rows that do not see them); the rows that do see them get them
@@ -33,6 +36,7 @@
 //    drains its copies and MMAs, frees tensor memory and returns.
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -46,11 +50,11 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 128;       // query rows of a tile, keys of a block
-constexpr int kThreads = 384;    // warps 0-3 and 4-7 softmax, 8-9 load, 10 MMA, 11 none
-constexpr int kLoaders = 64;
+constexpr int kThreads = 384;
+constexpr int kLoaders = 64;     // threads that load by cp.async
 constexpr int kGroups = 64;      // sequences are counted in this many runs
 constexpr int kItems = 4;        // work items between the loader and the other roles
-constexpr int kItemReaders = 1 + 8 + 2;  // MMA thread, softmax warps, loader warps
+constexpr int kItemReaders = 12;  // every warp
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S (and P over it) and O of each softmax warpgroup, 128 columns apart
 constexpr int kHeader = 3072;
@@ -91,6 +95,17 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// One box of a 3-d tensor (head dimension, heads, rows) to shared memory.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -116,6 +131,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
       "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
       : "memory");
+}
+// True in one lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
 }
 // 32 columns of this warp's 32 lanes (a thread: its row's 32 values).
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t* r) {
@@ -168,6 +189,30 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 values in one 64-bit register: one instruction multiplies or adds both.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split_pair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 template <int kType>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -307,16 +352,35 @@ __device__ __forceinline__ bool sees_any(const AttnArgs& a, int t, int nk, int n
   return any;
 }
 
-// Place in the ring of an item's tiles (after the item's first): with two
-// query tiles K0 V0 K1 V1 ..., with one K0 K1 V0 K2 V1 ... (K runs ahead by
-// one block, as both softmax warpgroups start on a block each).
-__device__ __forceinline__ int k_place(int two, int b) { return two ? 2 * b : (b == 0 ? 0 : 2 * b - 1); }
-__device__ __forceinline__ int v_place(int two, int b, int n) {
-  return two ? 2 * b + 1 : (b < n - 1 ? 2 * b + 2 : 2 * n - 1);
-}
+// The tensor maps of a call (boxes of 64 columns).
+struct Maps {
+  CUtensorMap q, k, v;
+  int use;       // 0: the tiles are copied by cp.async
+  int box;       // rows of a box of K and V
+};
+
+// A place in the ring of tiles and the parity of its round.
+template <int kStages>
+struct Place {
+  int slot;
+  uint32_t parity;
+  __device__ __forceinline__ void step(int by) {  // by <= kStages
+    slot += by;
+    if (slot >= kStages) {
+      slot -= kStages;
+      parity ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void skip(int by) {
+    slot += by;
+    parity ^= (uint32_t)(slot / kStages) & 1u;
+    slot %= kStages;
+  }
+};
 
 template <int kType, int DP>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnArgs a,
+                                                                  const __grid_constant__ Maps maps) {
   using Sz = Sizes<DP>;
   constexpr int kStages = Sz::stages;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -336,27 +400,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   auto pfull_bar = [&](int w) { return bar0 + 8u * (22 + w); };
   auto ofull_bar = [&](int w) { return bar0 + 8u * (24 + w); };
   auto oempty_bar = [&](int w) { return bar0 + 8u * (26 + w); };
-  const uint32_t join_bar = bar0 + 8u * 28, drain_bar = bar0 + 8u * 29;
+  const uint32_t join_bar = bar0 + 8u * 28, drain_bar = bar0 + 8u * 29, drain2_bar = bar0 + 8u * 46;
   auto ifull_bar = [&](int i) { return bar0 + 8u * (30 + i); };
   auto iempty_bar = [&](int i) { return bar0 + 8u * (34 + i); };
-  // after the barriers (304 bytes)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 320);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 324);
-  volatile int* poisoned = reinterpret_cast<volatile int*>(head + 336);    // [kItems]
+  auto land_bar = [&](int s) { return bar0 + 8u * (38 + s); };  // values that are cleaned before they are full
+  // after the barriers (47 of them, 376 bytes)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 376);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 380);
+  volatile int* poisoned = reinterpret_cast<volatile int*>(head + 2464);   // [kItems]
   Item* s_item = reinterpret_cast<Item*>(head + 384);                      // [kItems]
   float2* s_ml = reinterpret_cast<float2*>(head + 640);                    // [128]
   long long* s_part = reinterpret_cast<long long*>(head + 1664);           // [kGroups + 1]
   int* s_count = reinterpret_cast<int*>(head + 2192);                      // [kGroups + 1]
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < 8; ++s) {
-      mbar_init(full_bar(s), kLoaders);
-      mbar_init(empty_bar(s), 1);
+      mbar_init(full_bar(s), maps.use ? 1 : kLoaders);
+      mbar_init(empty_bar(s), 2);  // both MMA warps, or one twice
+      mbar_init(land_bar(s), 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(qfull_bar(w), kLoaders);
-      mbar_init(qempty_bar(w), 1);
+      mbar_init(qfull_bar(w), maps.use ? 1 : kLoaders);
+      mbar_init(qempty_bar(w), 2);
       mbar_init(sfull_bar(w), 1);
       mbar_init(pfull_bar(w), 128);
       mbar_init(ofull_bar(w), 1);
@@ -364,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     mbar_init(join_bar, 128);
     mbar_init(drain_bar, 1);
+    mbar_init(drain2_bar, 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(ifull_bar(i), 1);
       mbar_init(iempty_bar(i), kItemReaders);
@@ -424,12 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   // Every role takes the items from the ring in order.
   int seq_no = 0;
   Item it = {};
-  auto next_item = [&](bool whole_warp) -> bool {
+  auto next_item = [&]() -> bool {
     const int i = seq_no % kItems;
     if (!wait_bar(ifull_bar(i), (seq_no / kItems) & 1, ctl)) return false;
     it = s_item[i];
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) mbar_arrive(iempty_bar(i));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(iempty_bar(i));
     ++seq_no;
     return it.end == 0;
   };
@@ -441,228 +508,358 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // ================================ loader ================================
     const int lw = warp - 8;
     const int total = s_count[kGroups] * a.heads_kv;
-    int next = blockIdx.x, ring = 0, qring = 0;
+    int next = blockIdx.x;
+    Place<kStages> ring = {0, 0};
+    Place<2> qring = {0, 0};
+    uint32_t landed = 0;  // parities of the land barriers, a bit each
     bool ok = true;
-    // 32 rows (half h of this warp's 64) into a tile at `dst`: this lane's row
-    // starts at element `at` of base, or is zero (at < 0); columns past the
-    // head dimension are zero.
-    auto load_rows = [&](uint32_t dst, const uint16_t* base, int h, long long at) {
-      constexpr int kChunks = DP / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row, rows of an instruction
-      const int c = lane % kChunks, sub = lane / kChunks;
-#pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += kRows) {
-        const int r = r0 + sub;
-        const long long from = __shfl_sync(~0u, at, r);
-        const bool there = from >= 0 && c * 8 < a.head_dim;
-        const int row = lw * 64 + h * 32 + r;
-        cp_async16(dst + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                   base + (there ? from + c * 8 : 0), there);
+    // Warp 8 decodes the next item and hands it out.
+    auto hand_out = [&]() -> bool {
+      const int i = seq_no % kItems;
+      if (!wait_bar(iempty_bar(i), ((seq_no / kItems) & 1) ^ 1, ctl)) return false;
+      Item x = {};
+      x.end = next >= total;
+      if (!x.end) {
+        const int kvh = next % a.heads_kv;
+        int u = next / a.heads_kv, g = 0;
+        for (int step = kGroups / 2; step; step >>= 1)
+          if (s_count[g + step] <= u) g += step;
+        u -= s_count[g];
+        long long part = s_part[g];
+        int b = g * per;
+        Seq s = seq_of(a, b);
+        Shape w = shape_of(a, s, tpt);
+        while (u >= w.pairs * w.cut.pieces && b + 1 < a.n) {
+          u -= w.pairs * w.cut.pieces;
+          part += w.part_rows;
+          s = seq_of(a, ++b);
+          w = shape_of(a, s, tpt);
+        }
+        const int pair = max(w.pairs - 1 - u / w.cut.pieces, 0);
+        x.piece = u % w.cut.pieces;
+        x.i0 = pair * 2 * tpt;
+        x.first = s.first + x.i0;
+        x.tokens = min(2 * tpt, s.nq - x.i0);
+        x.two = x.tokens > tpt;
+        x.nq = s.nq;
+        x.k0 = s.k0;
+        x.nk = s.nk;
+        x.kvh = kvh;
+        // the keys that any row of the pair sees end here
+        const int keys = a.mask ? s.nk : limit_of(a, s.nk, s.nq, x.i0 + x.tokens - 1);
+        x.b0 = x.piece * w.cut.blocks;
+        x.blocks = max(0, min((keys + kTile - 1) / kTile - x.b0, w.cut.blocks));
+        x.pieces = w.cut.pieces;
+        x.rows = s.nq * a.heads_q;
+        x.part = part + (long long)x.piece * x.rows;
       }
+      if (lane == 0) {
+        s_item[i] = x;
+        mbar_arrive(ifull_bar(i));
+      }
+      next += gridDim.x;
+      return true;
     };
-    while (ok) {
-      // warp 8 decodes the next item and hands it out
-      if (lw == 0) {
-        const int i = seq_no % kItems;
-        ok = wait_bar(iempty_bar(i), ((seq_no / kItems) & 1) ^ 1, ctl);
-        if (ok) {
-          Item x = {};
-          x.end = next >= total;
-          if (!x.end) {
-            const int kvh = next % a.heads_kv;
-            int u = next / a.heads_kv, g = 0;
-            for (int step = kGroups / 2; step; step >>= 1)
-              if (s_count[g + step] <= u) g += step;
-            u -= s_count[g];
-            long long part = s_part[g];
-            int b = g * per;
-            Seq s = seq_of(a, b);
-            Shape w = shape_of(a, s, tpt);
-            while (u >= w.pairs * w.cut.pieces && b + 1 < a.n) {
-              u -= w.pairs * w.cut.pieces;
-              part += w.part_rows;
-              s = seq_of(a, ++b);
-              w = shape_of(a, s, tpt);
+    // Row of the packed keys or of the cache's planes that holds key `pos`, or
+    // -1 (no such key, or a page id out of range).
+    auto row_of = [&](int pos) -> int {
+      if (pos >= it.nk) return -1;
+      if (!a.paged) return it.k0 + pos;
+      const int at = pos / a.page_size;
+      const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + at);
+      if (p < 0 || p >= a.n_pages) {
+        report(a.status, MOE_ERR_INVALID);
+        return -1;
+      }
+      return p * a.page_size + (pos - at * a.page_size);
+    };
+    // 16-byte chunk c of row r of a tile.
+    auto chunk_at = [](uint32_t tile, int r, int c) -> uint32_t {
+      return tile + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    };
+    auto at_smem = [&](uint32_t at) { return reinterpret_cast<uint4*>(smem + (at - sQ)); };
+    auto clean_chunk = [&](uint32_t at) -> bool {  // whether anything had to be cleared
+      uint4 v = *at_smem(at);
+      bool f = clear_nonfinite<kType>(v.x);
+      f |= clear_nonfinite<kType>(v.y);
+      f |= clear_nonfinite<kType>(v.z);
+      f |= clear_nonfinite<kType>(v.w);
+      if (f) *at_smem(at) = v;
+      return f;
+    };
+    constexpr int kChunks = DP / 8;  // of a row
+    if (maps.use && lw == 0) {
+      // ----------------------------- TMA loads -----------------------------
+      const int boxes = kTile / maps.box;
+      const uint32_t box_bytes = (uint32_t)maps.box * 128u, q_bytes = (uint32_t)(tpt * group * 128);
+      // per ring place: whether it was filled, by which barrier, in which parity
+      uint32_t filled = 0, by_land = 0, parity = 0, qfilled = 0, qparity = 0;
+      while (ok) {
+        ok = hand_out() && next_item();
+        if (!ok) break;
+        const int n = __shfl_sync(~0u, it.blocks, 0);
+        if (n == 0) continue;
+        const int lim = limit_of(a, it.nk, it.nq, it.i0);  // the least that any row of the pair sees
+        // lane i: row of box i of the block
+        const int first = it.b0 * kTile + lane * maps.box;
+        int row = lane < boxes ? row_of(first) : -1;
+        for (int q = 0; q < 1 + it.two && ok; ++q) {
+          ok = wait_bar(qempty_bar(qring.slot), qring.parity ^ 1, ctl);
+          if (ok && elect_one()) {
+            mbar_expect_tx(qfull_bar(qring.slot), q_bytes * (DP / 64));
+#pragma unroll
+            for (int h = 0; h < DP / 64; ++h)
+              tma_load(sQ + qring.slot * Sz::tile + h * kTile * 128, &maps.q, h * 64, it.kvh * group,
+                       it.first + q * tpt, qfull_bar(qring.slot));
+          }
+          __syncwarp();
+          if (ok) {
+            qfilled |= 1u << qring.slot;
+            qparity = (qparity & ~(1u << qring.slot)) | (qring.parity << qring.slot);
+          }
+          qring.step(1);
+        }
+        for (int b = 0; b < n && ok; ++b) {
+          const int end = (it.b0 + b + 1) * kTile;
+          const uint32_t there = __ballot_sync(~0u, row >= 0);
+          const int nrow = lane < boxes && b + 1 < n ? row_of(first + (b + 1) * kTile) : -1;
+          const uint32_t bytes = (uint32_t)__popc(there) * box_bytes * (DP / 64);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            if (ok) ok = wait_bar(empty_bar(ring.slot), ring.parity ^ 1, ctl);
+            if (!ok) break;
+            const bool dirty = v == 1 && (end > it.nk || (end > lim && lim < it.nk));
+            const uint32_t bar = dirty ? land_bar(ring.slot) : full_bar(ring.slot);
+            const uint32_t dst = sKV + ring.slot * Sz::tile;
+            const CUtensorMap* map = v ? &maps.v : &maps.k;
+            const uint32_t bit = 1u << ring.slot;
+            filled |= bit;
+            if (dirty) landed ^= bit;  // parity of the next one to land
+            by_land = dirty ? by_land | bit : by_land & ~bit;
+            parity = ((dirty ? ~landed : ring.parity << ring.slot) & bit) | (parity & ~bit);
+            if (elect_one()) mbar_expect_tx(bar, bytes);
+            for (int i = 0; i < boxes; ++i) {
+              const int z = __shfl_sync(~0u, row, i);
+              if (z < 0) continue;
+              if (elect_one()) {
+#pragma unroll
+                for (int h = 0; h < DP / 64; ++h)
+                  tma_load(dst + h * kTile * 128 + i * box_bytes, map, h * 64, it.kvh, z, bar);
+              }
             }
-            const int pair = max(w.pairs - 1 - u / w.cut.pieces, 0);
-            x.piece = u % w.cut.pieces;
-            x.i0 = pair * 2 * tpt;
-            x.first = s.first + x.i0;
-            x.tokens = min(2 * tpt, s.nq - x.i0);
-            x.two = x.tokens > tpt;
-            x.nq = s.nq;
-            x.k0 = s.k0;
-            x.nk = s.nk;
-            x.kvh = kvh;
-            // the keys that any row of the pair sees end here
-            const int keys = a.mask ? s.nk : limit_of(a, s.nk, s.nq, x.i0 + x.tokens - 1);
-            x.b0 = x.piece * w.cut.blocks;
-            x.blocks = max(0, min((keys + kTile - 1) / kTile - x.b0, w.cut.blocks));
-            x.pieces = w.cut.pieces;
-            x.rows = s.nq * a.heads_q;
-            x.part = part + (long long)x.piece * x.rows;
+            __syncwarp();
+            ring.step(1);
           }
-          if (lane == 0) {
-            s_item[i] = x;
-            mbar_arrive(ifull_bar(i));
-          }
-          next += gridDim.x;
+          row = nrow;
         }
       }
-      if (!next_item(true)) {
-        ok = it.end != 0 && *abort_flag == 0;
-        break;
+      if (*abort_flag) {
+        // a role gave up: every load issued lands before the CTA exits
+        const long long t0 = clock64();
+        for (int i = 0; i < kStages; ++i)
+          if ((filled >> i) & 1u)
+            while (!mbar_try_wait((by_land >> i) & 1u ? land_bar(i) : full_bar(i), (parity >> i) & 1u) &&
+                   clock64() - t0 < kBudget) {
+            }
+        for (int i = 0; i < 2; ++i)
+          if ((qfilled >> i) & 1u)
+            while (!mbar_try_wait(qfull_bar(i), (qparity >> i) & 1u) && clock64() - t0 < kBudget) {
+            }
       }
-      const int n = it.blocks;
-      if (n == 0) continue;
-      // the query tiles
-      for (int q = 0; q < 1 + it.two; ++q, ++qring) {
-        const int slot = qring & 1;
-        if (!wait_bar(qempty_bar(slot), ((qring >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
-        for (int h = 0; h < 2; ++h) {
-          const int r = lw * 64 + h * 32 + lane, token = r / group;
-          long long at = -1;
-          if (token < tpt && q * tpt + token < it.tokens)
-            at = (long long)(it.first + q * tpt + token) * a.q.ts + (it.kvh * group + r % group) * a.q.hs;
-          load_rows(sQ + slot * Sz::tile, a.q.p, h, at);
-        }
-        cp_async_arrive(qfull_bar(slot));
-      }
-      if (!ok) break;
-      // row of the packed keys or of the cache's planes that holds key `pos`, or -1
-      auto row_of = [&](int block, int h) -> int {
-        const int pos = (it.b0 + block) * kTile + lw * 64 + h * 32 + lane;
-        if (block >= n || pos >= it.nk) return -1;
-        if (!a.paged) return it.k0 + pos;
-        const int at = pos / a.page_size;
-        const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + at);
-        if (p < 0 || p >= a.n_pages) {
-          report(a.status, MOE_ERR_INVALID);
-          return -1;
-        }
-        return p * a.page_size + (pos - at * a.page_size);
-      };
-      const int lim = limit_of(a, it.nk, it.nq, it.i0);  // the least that any row of the pair sees
-      auto load_tile = [&](const Heads& x, int2 row, bool clean, int item_no) -> bool {
-        const int slot = ring % kStages;
-        if (!wait_bar(empty_bar(slot), ((ring / kStages) & 1) ^ 1, ctl)) return false;
-        const uint32_t dst = sKV + slot * Sz::tile;
-        load_rows(dst, x.p, 0, row.x < 0 ? -1 : row.x * x.ts + it.kvh * x.hs);
-        load_rows(dst, x.p, 1, row.y < 0 ? -1 : row.y * x.ts + it.kvh * x.hs);
-        if (!clean) {
-          cp_async_arrive(full_bar(slot));
-        } else {
-          // some row does not see all of these: values that are not finite are
-          // cleared (each thread those that it copied), and the item is marked
-          cp_async_wait_all();
-          bool found = false;
-          constexpr int kChunks = DP / 8, kRows = 32 / kChunks;
-          const int c = lane % kChunks;
-          for (int r0 = 0; r0 < 64; r0 += kRows) {
-            const int rr = lw * 64 + r0 + lane / kChunks;
-            const uint32_t at = dst + (c >> 3) * (kTile * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-            uint4* p = reinterpret_cast<uint4*>(smem + (at - sQ));
-            uint4 v = *p;
-            bool f = clear_nonfinite<kType>(v.x);
-            f |= clear_nonfinite<kType>(v.y);
-            f |= clear_nonfinite<kType>(v.z);
-            f |= clear_nonfinite<kType>(v.w);
-            if (f) *p = v;
-            found |= f;
+    } else if (maps.use) {
+      // -------------- values that some row does not see, and tails --------------
+      while (ok && next_item()) {
+        const int n = it.blocks;
+        if (n == 0) continue;
+        const int item_no = seq_no - 1;
+        const int lim = limit_of(a, it.nk, it.nq, it.i0);
+        Place<kStages> at = ring;
+        for (int b = 0; b < n; ++b, at.step(2)) {
+          const int end = (it.b0 + b + 1) * kTile;
+          const bool edge = end > lim && lim < it.nk;
+          if (end <= it.nk && !edge) continue;
+          Place<kStages> v = at;
+          v.step(1);
+          if (!wait_bar(land_bar(v.slot), (landed >> v.slot) & 1, ctl)) { ok = false; break; }
+          landed ^= 1u << v.slot;
+          const uint32_t tile = sKV + v.slot * Sz::tile;
+          const int rows = min(kTile, it.nk - (end - kTile));  // rows of this sequence
+          for (int i = rows * kChunks + lane; i < kTile * kChunks; i += 32)
+            *at_smem(chunk_at(tile, i / kChunks, i % kChunks)) = make_uint4(0u, 0u, 0u, 0u);
+          if (edge) {
+            // carries out of the exponent tell whether anything is to be cleared
+            constexpr uint32_t kExp = kType == MOE_BF16 ? 0x7F807F80u : 0x7C007C00u;
+            constexpr uint32_t kOne = kType == MOE_BF16 ? 0x00800080u : 0x04000400u;
+            uint32_t acc = 0;
+#pragma unroll 8
+            for (int i = lane; i < rows * kChunks; i += 32) {
+              const uint4 x = *at_smem(tile + (uint32_t)i * 16 + (i * 16 >= rows * 128 ? (kTile - rows) * 128 : 0));
+              acc |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
+            }
+            if (__any_sync(~0u, (acc & 0x80008000u) != 0)) {
+              for (int i = lane; i < rows * kChunks; i += 32) clean_chunk(chunk_at(tile, i / kChunks, i % kChunks));
+              if (lane == 0) poisoned[item_no % kItems] = item_no + 1;
+            }
           }
-          if (found) poisoned[item_no % kItems] = item_no + 1;
           fence_proxy_async_shared();
-          mbar_arrive(full_bar(slot));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full_bar(v.slot));
         }
-        ++ring;
-        return true;
+        ring.skip(2 * n);
+      }
+    } else {
+      // --------------------------- cp.async copies ---------------------------
+      // 32 rows (half h of this warp's 64) into a tile at `dst`: this lane's row
+      // starts at element `at` of base, or is zero (at < 0); columns past the
+      // head dimension are zero.
+      constexpr int kRows = 32 / kChunks;  // rows of an instruction
+      auto load_rows = [&](uint32_t dst, const uint16_t* base, int h, long long at) {
+        const int c = lane % kChunks, sub = lane / kChunks;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kRows) {
+          const int r = r0 + sub;
+          const long long from = __shfl_sync(~0u, at, r);
+          const bool there = from >= 0 && c * 8 < a.head_dim;
+          cp_async16(chunk_at(dst, lw * 64 + h * 32 + r, c), base + (there ? from + c * 8 : 0), there);
+        }
       };
-      const int item_no = seq_no - 1;
-      auto is_edge = [&](int block) { return (it.b0 + block + 1) * kTile > lim && lim < it.nk; };
-      auto rows_of = [&](int block) { return make_int2(row_of(block, 0), row_of(block, 1)); };
-      int2 cur = rows_of(0), nxt = rows_of(1);
-      ok = load_tile(a.k, cur, false, item_no);
-      if (it.two) {
-        for (int b = 0; b < n && ok; ++b) {
-          ok = load_tile(a.v, cur, is_edge(b), item_no);
-          cur = nxt;
-          nxt = rows_of(b + 2);
-          if (ok && b + 1 < n) ok = load_tile(a.k, cur, false, item_no);
+      while (ok) {
+        if (lw == 0) ok = hand_out();
+        ok = ok && next_item();
+        if (!ok) break;
+        const int n = it.blocks, item_no = seq_no - 1;
+        if (n == 0) continue;
+        for (int q = 0; q < 1 + it.two && ok; ++q) {
+          ok = wait_bar(qempty_bar(qring.slot), qring.parity ^ 1, ctl);
+          if (!ok) break;
+          for (int h = 0; h < 2; ++h) {
+            const int r = lw * 64 + h * 32 + lane, token = r / group;
+            long long at = -1;
+            if (token < tpt && q * tpt + token < it.tokens)
+              at = (long long)(it.first + q * tpt + token) * a.q.ts + (it.kvh * group + r % group) * a.q.hs;
+            load_rows(sQ + qring.slot * Sz::tile, a.q.p, h, at);
+          }
+          cp_async_arrive(qfull_bar(qring.slot));
+          qring.step(1);
         }
-      } else {
+        const int lim = limit_of(a, it.nk, it.nq, it.i0);
+        auto rows_of = [&](int block) {
+          const int pos = (it.b0 + block) * kTile + lw * 64 + lane;
+          return block < n ? make_int2(row_of(pos), row_of(pos + 32)) : make_int2(-1, -1);
+        };
+        int2 rows = rows_of(0);
         for (int b = 0; b < n && ok; ++b) {
-          const int2 row = cur;
-          cur = nxt;
-          if (b + 1 < n) ok = load_tile(a.k, cur, false, item_no);
-          nxt = rows_of(b + 2);
-          if (ok) ok = load_tile(a.v, row, is_edge(b), item_no);
+          const int2 later = rows_of(b + 1);
+          const bool edge = (it.b0 + b + 1) * kTile > lim && lim < it.nk;
+          for (int v = 0; v < 2; ++v) {
+            const Heads& x = v ? a.v : a.k;
+            ok = wait_bar(empty_bar(ring.slot), ring.parity ^ 1, ctl);
+            if (!ok) break;
+            const uint32_t dst = sKV + ring.slot * Sz::tile;
+            load_rows(dst, x.p, 0, rows.x < 0 ? -1 : rows.x * x.ts + it.kvh * x.hs);
+            load_rows(dst, x.p, 1, rows.y < 0 ? -1 : rows.y * x.ts + it.kvh * x.hs);
+            if (v == 0 || !edge) {
+              cp_async_arrive(full_bar(ring.slot));
+            } else {  // each thread cleans what it copied
+              cp_async_wait_all();
+              bool found = false;
+              for (int r0 = 0; r0 < 64; r0 += kRows)
+                found |= clean_chunk(chunk_at(dst, lw * 64 + r0 + lane / kChunks, lane % kChunks));
+              if (found) poisoned[item_no % kItems] = item_no + 1;
+              fence_proxy_async_shared();
+              mbar_arrive(full_bar(ring.slot));
+            }
+            ring.step(1);
+          }
+          rows = later;
         }
       }
+      if (*abort_flag) cp_async_wait_all();  // nothing of ours may be in flight at exit
     }
-    if (!ok || *abort_flag) cp_async_wait_all();  // nothing of ours may be in flight at exit
   } else {
     // ============================== MMA issuer ==============================
-    if (warp == 10 && lane == 0) {
-      const uint32_t id_s = idesc_f16(kType, kTile, false), id_o = idesc_f16(kType, DP, true);
-      int ring = 0, qring = 0, uses[2] = {0, 0}, steps_done[2] = {0, 0};
-      bool ok = true;
-      while (ok && next_item(false)) {
-        const int n = it.blocks, two = it.two;
-        if (n == 0) continue;
-        const int steps = two ? 2 * n : n;
-        auto wait_tile = [&](int place) { return wait_bar(full_bar((ring + place) % kStages), ((ring + place) / kStages) & 1, ctl); };
-        auto score = [&](int t) -> bool {
-          const int w = t & 1, b = two ? t >> 1 : t, place = k_place(two, b), tile = two ? w : 0;
-          if ((two ? t < 2 : t == 0) && !wait_bar(qfull_bar((qring + tile) & 1), ((qring + tile) >> 1) & 1, ctl)) return false;
-          if ((!two || w == 0) && !wait_tile(place)) return false;
-          tc_fence_after();
-          fence_proxy_async_shared();  // the tiles were written by cp.async
-          const int slot = (ring + place) % kStages;
-          const uint64_t qd = desc_kmajor(sQ + ((qring + tile) & 1) * Sz::tile), kd = desc_kmajor(sKV + slot * Sz::tile);
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint64_t off = (uint64_t)((k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2);
-            tc_mma_ss(tmem + kColS + w * 128, qd + off, kd + off, id_s, k != 0);
-          }
-          tc_commit(sfull_bar(w));
-          if (!two || w == 1) tc_commit(empty_bar(slot));
-          if (t >= steps - 1 - two) tc_commit(qempty_bar((qring + tile) & 1));
-          return true;
-        };
-        auto values = [&](int t) -> bool {
-          const int w = t & 1, b = two ? t >> 1 : t, place = v_place(two, b, n);
-          if (t < 2) {
-            if (!wait_bar(oempty_bar(w), (uses[w] & 1) ^ 1, ctl)) return false;
-            ++uses[w];
-          }
-          if (!wait_bar(pfull_bar(w), steps_done[w] & 1, ctl)) return false;
-          ++steps_done[w];
-          if ((!two || w == 0) && !wait_tile(place)) return false;
-          tc_fence_after();
+    // Each of the two warps issues one softmax warpgroup's MMAs: S(0), then
+    // O += P(j) V(j) and S(j + 1) in turn (S(j + 1) overwrites P(j), which the
+    // order of one thread's MMAs allows). The whole warp keeps step and one
+    // elected lane issues: in a branch of one lane the compiler moves every
+    // operand to the uniform registers that these instructions take (8192 keys:
+    // 856 us that way, 529 us this way, one issuing warp each time).
+    const int w = warp - 10;
+    const uint32_t id_s = idesc_f16(kType, kTile, false), id_o = idesc_f16(kType, DP, true);
+    const uint32_t tS = tmem + kColS + w * 128, tO = tmem + kColO + w * 128;
+    const uint64_t qd0 = desc_kmajor(sQ), kd0 = desc_kmajor(sKV), vd0 = desc_mnmajor(sKV);
+    Place<kStages> ring = {0, 0};
+    Place<2> qring = {0, 0};
+    uint32_t uses = 0, steps = 0;  // parities of O's items and of S's steps
+    bool ok = true;
+    while (ok && next_item()) {
+      const int n = __shfl_sync(~0u, it.blocks, 0), two = __shfl_sync(~0u, it.two, 0);
+      if (n == 0) continue;
+      const int count = two ? n : (n + 1 - w) / 2;  // blocks of this warpgroup: all, or every other one
+      const bool alone_q = two || n == 1;           // nobody else reads the query tile
+      Place<2> q = qring;
+      if (two && w) q.step(1);
+      Place<kStages> at = ring;                     // K of the next block; its V is the next place
+      if (!two && w) at.step(2);
+      Place<kStages> vat = at;
+      for (int j = 0; j <= count && count > 0; ++j) {
+        if (j > 0) {
+          vat.step(1);
+          if (j == 1 && !wait_bar(oempty_bar(w), uses ^ 1, ctl)) { ok = false; break; }
+          if (!wait_bar(full_bar(vat.slot), vat.parity, ctl)) { ok = false; break; }
           fence_proxy_async_shared();
-          const int slot = (ring + place) % kStages;
-          const uint64_t vd = desc_mnmajor(sKV + slot * Sz::tile);
+          if (!wait_bar(pfull_bar(w), steps, ctl)) { ok = false; break; }
+          steps ^= 1;
+          tc_fence_after();
+          const uint64_t vd = vd0 + (uint64_t)(vat.slot * (Sz::tile >> 4));
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
-            tc_mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o,
-                      t >= 2 || k != 0);
-          if (!two || w == 1) tc_commit(empty_bar(slot));
-          if (t >= steps - 2) tc_commit(ofull_bar(w));
-          return true;
-        };
-        ok = score(0) && (steps < 2 || score(1));
-        for (int t = 0; t < steps && ok; ++t) ok = values(t) && (t + 2 >= steps || score(t + 2));
-        ring += 2 * n;
-        qring += 1 + two;
-      }
-      if (!ok || *abort_flag) {
-        // wait for every MMA issued so far before tensor memory is freed
-        tc_commit(drain_bar);
-        const long long t0 = clock64();
-        while (!mbar_try_wait(drain_bar, 0) && clock64() - t0 < kBudget) {
+            for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
+              tc_mma_ts(tO, tS + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o, j > 1 || k != 0);
+            tc_commit(empty_bar(vat.slot));
+            if (!two) tc_commit(empty_bar(vat.slot));
+            if (j == count) tc_commit(ofull_bar(w));
+          }
+          __syncwarp();
+        }
+        if (j < count) {
+          if (j == 0 && !wait_bar(qfull_bar(q.slot), q.parity, ctl)) { ok = false; break; }
+          if (!wait_bar(full_bar(at.slot), at.parity, ctl)) { ok = false; break; }
+          fence_proxy_async_shared();  // tiles may have been written by cp.async or cleaned
+          tc_fence_after();
+          const uint64_t qd = qd0 + (uint64_t)(q.slot * (Sz::tile >> 4));
+          const uint64_t kd = kd0 + (uint64_t)(at.slot * (Sz::tile >> 4));
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+              const uint64_t off = (uint64_t)((k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2);
+              tc_mma_ss(tS, qd + off, kd + off, id_s, k != 0);
+            }
+            tc_commit(sfull_bar(w));
+            tc_commit(empty_bar(at.slot));
+            if (!two) tc_commit(empty_bar(at.slot));
+            if (j + 1 == count) {
+              tc_commit(qempty_bar(q.slot));
+              if (alone_q) tc_commit(qempty_bar(q.slot));
+            }
+          }
+          __syncwarp();
+          vat = at;
+          at.step(two ? 2 : 4);
         }
       }
+      if (count > 0) uses ^= 1;
+      ring.skip(2 * n);
+      qring.skip(1 + two);
     }
-    __syncwarp();
+    if (!ok || *abort_flag) {
+      // wait for every MMA issued so far before tensor memory is freed
+      const uint32_t bar = w ? drain2_bar : drain_bar;
+      if (elect_one()) tc_commit(bar);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bar, 0) && clock64() - t0 < kBudget) {
+      }
+    }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -674,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const float c = a.scale * 1.4426950408889634f;
     int steps_done = 0, uses = 0, uses1 = 0, joins = 0;  // uses of this O, of the second one
     bool ok = true;
-    while (ok && next_item(true)) {
+    while (ok && next_item()) {
       const int n = it.blocks, two = it.two;
       const int steps = two ? 2 * n : n;
       const int token = r / group, tok = (two ? w * tpt : 0) + token;  // in the tile, in the pair
@@ -706,10 +903,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         float mx[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(s[u]);
+        for (int u = 0; u < 4; ++u) mx[u] = max3(__uint_as_float(s[u]), __uint_as_float(s[u + 4]), __uint_as_float(s[u + 8]));
 #pragma unroll
-        for (int j = 4; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
-        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        for (int j = 12; j + 8 <= kTile; j += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], __uint_as_float(s[j + u]), __uint_as_float(s[j + 4 + u]));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(s[kTile - 4 + u]));
+        const float top = max3(max3(m, mx[0], mx[1]), mx[2], mx[3]);
         const bool move = top > m && !((top - m) * c <= kLazy);
         if (t >= 2 && __any_sync(~0u, move)) {
           // S(t) is complete, so is every earlier MMA: O can be rescaled
@@ -727,21 +928,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         if (move) m = top;
         const float base = m == -INFINITY ? 0.0f : -m * c;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t c2 = pair_of(c, c), base2 = pair_of(base, base);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int h = 0; h < kTile; h += 64) {
           uint32_t p[32];
 #pragma unroll
           for (int j = 0; j < 64; j += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[h + j]), c, base));
-            const float p1 = ex2(fmaf(__uint_as_float(s[h + j + 1]), c, base));
-            sum[j & 2] += p0;
-            sum[(j & 2) + 1] += p1;
+            const uint64_t x = fma2(pair_of(__uint_as_float(s[h + j]), __uint_as_float(s[h + j + 1])), c2, base2);
+            float p0, p1;
+            split_pair(x, p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair_of(p0, p1));
             p[j / 2] = pack2<kType>(p0, p1);
           }
           tc_st32(tS + h / 2, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float l0, l1;
+        split_pair(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(pfull_bar(w));
@@ -913,6 +1119,41 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnA
   }
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// Boxes of 64 columns x box_heads x box_rows of [rows, heads, head_dim]. False
+// where a tensor map cannot describe the tensor.
+bool make_map(CUtensorMap* map, const Heads& h, int dtype, int head_dim, int heads, long long rows, int box_heads,
+              int box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode || !h.p || rows <= 0) return false;
+  // a stride along one element says nothing
+  const cuuint64_t hs = heads > 1 ? (cuuint64_t)h.hs * 2 : (cuuint64_t)head_dim * 2;
+  const cuuint64_t ts = rows > 1 ? (cuuint64_t)h.ts * 2 : (cuuint64_t)head_dim * 2;
+  if (hs == 0 || ts == 0 || hs >= (1ull << 40) || ts >= (1ull << 40)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {hs, ts};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return encode(map, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, h.p,
+                dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kType, int DP>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s) {
   cudaError_t err = cudaFuncSetAttribute(attention_kernel<kType, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -923,8 +1164,15 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s) {
   long long items = ((long long)a.total_q / (2 * tpt) + a.n) * a.heads_kv;
   if (a.part_o) items = items * kSplitItems;
   const int sms = num_sms();
+  Maps maps = {};
+  const int group = a.heads_q / a.heads_kv;
+  const long long rows = a.paged ? (long long)a.n_pages * a.page_size : a.total_k;
+  maps.box = a.paged ? min(a.page_size & -a.page_size, kTile) : kTile;  // rows of a page that lie together
+  maps.use = maps.box >= 8 && make_map(&maps.q, a.q, kType, a.head_dim, a.heads_q, a.total_q, group, tpt) &&
+             make_map(&maps.k, a.k, kType, a.head_dim, a.heads_kv, rows, 1, maps.box) &&
+             make_map(&maps.v, a.v, kType, a.head_dim, a.heads_kv, rows, 1, maps.box);
   err = launch_pdl(attention_kernel<kType, DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads),
-                   Sizes<DP>::smem, s, a);
+                   Sizes<DP>::smem, s, a, maps);
   if (err != cudaSuccess || !a.part_o) return err;
   const long long blocks = ((long long)a.total_q * a.heads_q + 3) / 4, most = sms * 16LL;
   return launch_pdl(join_kernel<kType>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(128), 0, s, a);
