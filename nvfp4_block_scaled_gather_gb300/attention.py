@@ -11,10 +11,11 @@ the library raises RuntimeError. There is no fallback.
 from __future__ import annotations
 
 import ctypes
-import math
+
+import torch
 
 from . import _native
-from ._native import _check, _ptr, _stream
+from ._native import _check
 
 c_int, c_size_t, c_void_p, c_longlong, c_float = (ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong,
                                                   ctypes.c_float)
@@ -72,40 +73,46 @@ def exported_symbols():
     return list(_SIGS)
 
 
-def _dtype_code(t):
-    import torch
-    code = {torch.bfloat16: BF16, torch.float16: FP16}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"tensors are bfloat16 or float16, got {t.dtype}")
-    return code
+_INT32, _FLOAT32 = torch.int32, torch.float32
+_CODES = {torch.bfloat16: BF16, torch.float16: FP16}
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _stream(stream, device: int) -> int:
+    """The stream's handle: the given one, or the device's current one."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
-def _ints(name, t, shape, device):
-    """A contiguous int32 CUDA tensor of this shape."""
-    import torch
-    _need(t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
-          f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
-          f"{t.device}")
-    return _ptr(t)
+def _ints(name, t, n, device: int) -> int:
+    """Address of a contiguous int32 tensor of n elements on this device."""
+    if t.dtype is not _INT32 or t.numel() != n or not t.is_contiguous() or t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements on cuda:{device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _heads(name, t, like=None):
+def _heads(name, t, dtype, device: int):
     """[tokens, heads, dim] with dim contiguous, as moe_heads_t."""
-    _need(t.dim() == 3 and t.is_cuda, f"{name} must be a CUDA tensor [tokens, heads, dim]")
-    if like is not None:
-        _need(t.dtype == like.dtype and t.device == like.device,
-              f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
     ts, hs, ds = t.stride()
+    tokens, heads, dim = t.shape
     # a stride along one element says nothing
-    ts, hs = (ts if t.shape[0] > 1 else 0), (hs if t.shape[1] > 1 else 0)
-    _need(t.shape[2] == 1 or ds == 1, f"{name}: the last dimension must be contiguous")
-    _need(ts % 8 == 0 and hs % 8 == 0, f"{name}: strides must be multiples of 8 elements, got {ts} and {hs}")
+    if tokens <= 1:
+        ts = 0
+    if heads <= 1:
+        hs = 0
+    if (ds != 1 and dim != 1) or ts % 8 or hs % 8:
+        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides multiples of 8 elements, "
+                         f"got {t.stride()}")
     return Heads(t.data_ptr(), ts, hs)
+
+
+def _call(name, fn, *args):
+    status = fn(*args)
+    if status:
+        _check(name, status)
 
 
 class KVCache:
@@ -115,130 +122,134 @@ class KVCache:
     (moe_kv_cache_t)."""
 
     def __init__(self, pages, table, length, held, refs):
-        _need(pages.dim() == 5 and pages.is_contiguous() and pages.is_cuda,
-              "pages must be a contiguous CUDA tensor [2 * layers, n_pages, page_size, kv_heads, head_dim]")
-        _need(table.dim() == 2, "table must be [max_seqs, max_pages]")
+        if pages.dim() != 5 or not pages.is_contiguous() or not pages.is_cuda or pages.dtype not in _CODES:
+            raise ValueError("pages must be a contiguous bfloat16 or float16 CUDA tensor [2 * layers, n_pages, "
+                             "page_size, kv_heads, head_dim]")
+        if table.dim() != 2:
+            raise ValueError("table must be [max_seqs, max_pages]")
         planes, n_pages, page_size, heads, dim = pages.shape
         max_seqs, max_pages = table.shape
-        dev = pages.device
         self.pages, self.table, self.length, self.held, self.refs = pages, table, length, held, refs
-        self.layers, self.device = planes // 2, dev
-        self.struct = CacheStruct(pages.data_ptr(), planes, n_pages, page_size, heads, dim, _dtype_code(pages),
-                                  _ints("table", table, (max_seqs, max_pages), dev).value,
-                                  _ints("length", length, (max_seqs,), dev).value,
-                                  _ints("held", held, (max_seqs,), dev).value,
-                                  _ints("refs", refs, (n_pages,), dev).value, max_seqs, max_pages)
+        self.layers, self.device, self.dtype = planes // 2, pages.get_device(), pages.dtype
+        self.heads_kv, self.head_dim = heads, dim
+        self.struct = CacheStruct(pages.data_ptr(), planes, n_pages, page_size, heads, dim, _CODES[pages.dtype],
+                                  _ints("table", table, max_seqs * max_pages, self.device),
+                                  _ints("length", length, max_seqs, self.device),
+                                  _ints("held", held, max_seqs, self.device),
+                                  _ints("refs", refs, n_pages, self.device), max_seqs, max_pages)
         self._ref = ctypes.byref(self.struct)
 
     @classmethod
-    def empty(cls, layers, n_pages, page_size, kv_heads, head_dim, max_seqs, max_pages, dtype=None, device="cuda"):
+    def empty(cls, layers, n_pages, page_size, kv_heads, head_dim, max_seqs, max_pages, dtype=torch.bfloat16,
+              device="cuda"):
         """A fresh cache."""
-        import torch
         ints = dict(dtype=torch.int32, device=device)
-        return cls(torch.zeros((2 * layers, n_pages, page_size, kv_heads, head_dim), dtype=dtype or torch.bfloat16,
-                               device=device),
+        return cls(torch.zeros((2 * layers, n_pages, page_size, kv_heads, head_dim), dtype=dtype, device=device),
                    torch.full((max_seqs, max_pages), -1, **ints), torch.zeros(max_seqs, **ints),
                    torch.zeros(max_seqs, **ints), torch.zeros(n_pages, **ints))
 
 
+def _scratch(workspace, device: int):
+    if workspace.get_device() != device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{device}")
+    return workspace.data_ptr(), workspace.numel()
+
+
 def pages_workspace(cache: KVCache):
     """The scratch of moe_kv_extend, moe_kv_keep and moe_kv_compact."""
-    import torch
-    return torch.empty(load().moe_kv_workspace_size(cache._ref), dtype=torch.uint8, device=cache.device)
+    return torch.empty(load().moe_kv_workspace_size(cache._ref), dtype=torch.uint8, device=cache.pages.device)
 
 
 def moe_kv_extend(cache: KVCache, seqs, add, workspace, stream=None):
-    n = seqs.numel()
-    _check("moe_kv_extend",
-           load().moe_kv_extend(cache._ref, _ints("seqs", seqs, (n,), cache.device),
-                                _ints("add", add, (n,), cache.device), n, _ptr(workspace), workspace.numel(),
-                                _stream(stream)))
+    n, dev = seqs.numel(), cache.device
+    _call("moe_kv_extend", load().moe_kv_extend, cache._ref, _ints("seqs", seqs, n, dev), _ints("add", add, n, dev), n,
+          *_scratch(workspace, dev), _stream(stream, dev))
 
 
 def moe_kv_append(cache: KVCache, layer: int, seqs, cu, k, v, stream=None):
-    n, total = seqs.numel(), k.shape[0]
-    shape = (total, cache.struct.heads_kv, cache.struct.head_dim)
-    _need(tuple(k.shape) == shape and tuple(v.shape) == shape, f"k and v must be {shape}")
-    _check("moe_kv_append",
-           load().moe_kv_append(cache._ref, layer, _ints("seqs", seqs, (n,), cache.device),
-                                _ints("cu", cu, (n + 1,), cache.device), n, total,
-                                ctypes.byref(_heads("k", k, cache.pages)), ctypes.byref(_heads("v", v, cache.pages)),
-                                _stream(stream)))
+    n, total, dev = seqs.numel(), k.shape[0], cache.device
+    shape = (total, cache.heads_kv, cache.head_dim)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k and v must be {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    _call("moe_kv_append", load().moe_kv_append, cache._ref, layer, _ints("seqs", seqs, n, dev),
+          _ints("cu", cu, n + 1, dev), n, total, ctypes.byref(_heads("k", k, cache.dtype, dev)),
+          ctypes.byref(_heads("v", v, cache.dtype, dev)), _stream(stream, dev))
 
 
 def moe_kv_fork(cache: KVCache, src, dst, stream=None):
-    n = src.numel()
-    _check("moe_kv_fork", load().moe_kv_fork(cache._ref, _ints("src", src, (n,), cache.device),
-                                             _ints("dst", dst, (n,), cache.device), n, _stream(stream)))
+    n, dev = src.numel(), cache.device
+    _call("moe_kv_fork", load().moe_kv_fork, cache._ref, _ints("src", src, n, dev), _ints("dst", dst, n, dev), n,
+          _stream(stream, dev))
 
 
 def moe_kv_truncate(cache: KVCache, seqs, new_len, stream=None):
-    n = seqs.numel()
-    _check("moe_kv_truncate",
-           load().moe_kv_truncate(cache._ref, _ints("seqs", seqs, (n,), cache.device),
-                                  _ints("new_len", new_len, (n,), cache.device), n, _stream(stream)))
+    n, dev = seqs.numel(), cache.device
+    _call("moe_kv_truncate", load().moe_kv_truncate, cache._ref, _ints("seqs", seqs, n, dev),
+          _ints("new_len", new_len, n, dev), n, _stream(stream, dev))
 
 
 def moe_kv_keep(cache: KVCache, seqs, drafted, keep, kept, workspace, stream=None):
-    n = seqs.numel()
-    _need(keep.dim() == 2, "keep must be [n, max_keep]")
-    _check("moe_kv_keep",
-           load().moe_kv_keep(cache._ref, _ints("seqs", seqs, (n,), cache.device),
-                              _ints("drafted", drafted, (n,), cache.device),
-                              _ints("keep", keep, (n, keep.shape[1]), cache.device), keep.shape[1],
-                              _ints("kept", kept, (n,), cache.device), n, _ptr(workspace), workspace.numel(),
-                              _stream(stream)))
+    n, dev = seqs.numel(), cache.device
+    if keep.dim() != 2:
+        raise ValueError("keep must be [n, max_keep]")
+    width = keep.shape[1]
+    _call("moe_kv_keep", load().moe_kv_keep, cache._ref, _ints("seqs", seqs, n, dev),
+          _ints("drafted", drafted, n, dev), _ints("keep", keep, n * width, dev), width, _ints("kept", kept, n, dev), n,
+          *_scratch(workspace, dev), _stream(stream, dev))
 
 
 def moe_kv_copy_pages(cache: KVCache, src, dst, stream=None):
-    n = src.numel()
-    _check("moe_kv_copy_pages", load().moe_kv_copy_pages(cache._ref, _ints("src", src, (n,), cache.device),
-                                                         _ints("dst", dst, (n,), cache.device), n, _stream(stream)))
+    n, dev = src.numel(), cache.device
+    _call("moe_kv_copy_pages", load().moe_kv_copy_pages, cache._ref, _ints("src", src, n, dev),
+          _ints("dst", dst, n, dev), n, _stream(stream, dev))
 
 
 def moe_kv_compact(cache: KVCache, workspace, stream=None):
-    _check("moe_kv_compact", load().moe_kv_compact(cache._ref, _ptr(workspace), workspace.numel(), _stream(stream)))
+    _call("moe_kv_compact", load().moe_kv_compact, cache._ref, *_scratch(workspace, cache.device),
+          _stream(stream, cache.device))
 
 
 def moe_tree_mask(parents, cu, mask, stream=None):
     """mask [total, words] from the drafted tokens' parents [total]."""
-    n, total = cu.numel() - 1, parents.numel()
-    _need(mask.dim() == 2, "mask must be [total, words]")
-    _check("moe_tree_mask",
-           load().moe_tree_mask(_ints("parents", parents, (total,), mask.device), _ints("cu", cu, (n + 1,), mask.device),
-                                n, total, _ints("mask", mask, (total, mask.shape[1]), mask.device), mask.shape[1],
-                                _stream(stream)))
+    n, total, dev = cu.numel() - 1, parents.numel(), mask.get_device()
+    if mask.dim() != 2:
+        raise ValueError("mask must be [total, words]")
+    words = mask.shape[1]
+    _call("moe_tree_mask", load().moe_tree_mask, _ints("parents", parents, total, dev), _ints("cu", cu, n + 1, dev), n,
+          total, _ints("mask", mask, total * words, dev), words, _stream(stream, dev))
 
 
-def _out_and_lse(q, out, lse):
-    import torch
-    _need(tuple(out.shape) == tuple(q.shape), f"out must be {tuple(q.shape)}")
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and tuple(lse.shape) == tuple(q.shape[:2]) and lse.is_contiguous()
-              and lse.device == q.device, f"lse must be a contiguous float32 tensor {tuple(q.shape[:2])}")
-    return ctypes.byref(_heads("out", out, q)), _ptr(lse)
+def _lse(lse, total, heads, device: int):
+    if lse is None:
+        return None
+    if lse.dtype is not _FLOAT32 or lse.shape != (total, heads) or not lse.is_contiguous() or lse.get_device() != device:
+        raise ValueError(f"lse must be a contiguous float32 tensor {(total, heads)} on cuda:{device}")
+    return lse.data_ptr()
 
 
 def moe_attention_prompt(q, k, v, cu_q, cu_k, out, lse=None, scale=None, stream=None):
     """Causal attention over packed whole prompts; scale defaults to head_dim ** -0.5."""
-    n = cu_q.numel() - 1
+    n, dtype, dev = cu_q.numel() - 1, q.dtype, q.get_device()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"q must be bfloat16 or float16, got {dtype}")
+    hq, ho = _heads("q", q, dtype, dev), _heads("out", out, dtype, dev)
+    hk, hv = _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
     total_q, heads_q, dim = q.shape
-    total_k, heads_kv, _ = k.shape
-    _need(k.shape[2] == dim and v.shape == k.shape, "k and v must be [total_k, kv_heads, head_dim]")
-    o, e = _out_and_lse(q, out, lse)
-    _check("moe_attention_prompt",
-           load().moe_attention_prompt(ctypes.byref(_heads("q", q)), ctypes.byref(_heads("k", k, q)),
-                                       ctypes.byref(_heads("v", v, q)), _ints("cu_q", cu_q, (n + 1,), q.device),
-                                       _ints("cu_k", cu_k, (n + 1,), q.device), n, total_q, total_k, heads_q, heads_kv,
-                                       dim, _dtype_code(q), 1.0 / math.sqrt(dim) if scale is None else scale, o, e,
-                                       _stream(stream)))
+    total_k, heads_kv, dim_k = k.shape
+    if dim_k != dim or v.shape != k.shape or out.shape != q.shape:
+        raise ValueError(f"k and v must be [total_k, kv_heads, {dim}] and out like q, got {tuple(k.shape)}, "
+                         f"{tuple(v.shape)} and {tuple(out.shape)}")
+    _call("moe_attention_prompt", load().moe_attention_prompt, ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
+          _ints("cu_q", cu_q, n + 1, dev), _ints("cu_k", cu_k, n + 1, dev), n, total_q, total_k, heads_q, heads_kv, dim,
+          code, dim ** -0.5 if scale is None else scale, ctypes.byref(ho), _lse(lse, total_q, heads_q, dev),
+          _stream(stream, dev))
 
 
 def cached_workspace(cache: KVCache, n: int, total_q: int, heads_q: int):
     """The scratch of moe_attention_cached for calls of n sequences, total_q queries."""
-    import torch
     size = load().moe_attention_cached_workspace_size(cache._ref, n, total_q, heads_q)
-    return torch.empty(size, dtype=torch.uint8, device=cache.device)
+    return torch.empty(size, dtype=torch.uint8, device=cache.pages.device)
 
 
 def moe_attention_cached(q, cache: KVCache, layer: int, seqs, cu_q, out, workspace, mask=None, lse=None, scale=None,
@@ -246,18 +257,19 @@ def moe_attention_cached(q, cache: KVCache, layer: int, seqs, cu_q, out, workspa
     """Attention of drafted tokens (or one token a sequence) over the cache;
     mask: None for a chain, else the tree's bits (moe_tree_mask). scale
     defaults to head_dim ** -0.5."""
-    n = seqs.numel()
+    n, dev = seqs.numel(), cache.device
+    hq, ho = _heads("q", q, cache.dtype, dev), _heads("out", out, cache.dtype, dev)
     total_q, heads_q, dim = q.shape
-    _need(dim == cache.struct.head_dim, f"q must have the cache's head_dim {cache.struct.head_dim}")
-    words = 0
+    if dim != cache.head_dim or out.shape != q.shape:
+        raise ValueError(f"q and out must be [total_q, heads_q, {cache.head_dim}], got {tuple(q.shape)} and "
+                         f"{tuple(out.shape)}")
+    words, bits = 0, None
     if mask is not None:
-        _need(mask.dim() == 2, "mask must be [total_q, words]")
+        if mask.dim() != 2:
+            raise ValueError("mask must be [total_q, words]")
         words = mask.shape[1]
-        mask = _ints("mask", mask, (total_q, words), cache.device)
-    o, e = _out_and_lse(q, out, lse)
-    _check("moe_attention_cached",
-           load().moe_attention_cached(ctypes.byref(_heads("q", q, cache.pages)), cache._ref, layer,
-                                       _ints("seqs", seqs, (n,), cache.device),
-                                       _ints("cu_q", cu_q, (n + 1,), cache.device), n, total_q, heads_q, mask, words,
-                                       1.0 / math.sqrt(dim) if scale is None else scale, o, e, _ptr(workspace),
-                                       workspace.numel(), _stream(stream)))
+        bits = _ints("mask", mask, total_q * words, dev)
+    _call("moe_attention_cached", load().moe_attention_cached, ctypes.byref(hq), cache._ref, layer,
+          _ints("seqs", seqs, n, dev), _ints("cu_q", cu_q, n + 1, dev), n, total_q, heads_q, bits, words,
+          dim ** -0.5 if scale is None else scale, ctypes.byref(ho), _lse(lse, total_q, heads_q, dev),
+          *_scratch(workspace, dev), _stream(stream, dev))
