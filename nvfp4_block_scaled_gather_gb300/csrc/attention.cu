@@ -54,6 +54,7 @@ constexpr int kThreads = 384;
 constexpr int kLoaders = 64;     // threads that load by cp.async
 constexpr int kGroups = 64;      // sequences are counted in this many runs
 constexpr int kItems = 4;        // work items between the loader and the other roles
+constexpr int kPoisoned = 8;     // more than the items that a loader can be ahead by
 constexpr int kItemReaders = 12;  // every warp
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S (and P over it) and O of each softmax warpgroup, 128 columns apart
@@ -138,7 +139,10 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
   return p != 0;
 }
-// 32 columns of this warp's 32 lanes (a thread: its row's 32 values).
+// 32 columns of this warp's 32 lanes (a thread: its row's 32 values). The whole
+// warp has to execute these together: a __syncwarp() stands before them where
+// lanes may have gone separate ways, which also keeps the compiler from pulling
+// a lane's condition out of a loop around them.
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -397,34 +401,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   auto qfull_bar = [&](int s) { return bar0 + 8u * (16 + s); };
   auto qempty_bar = [&](int s) { return bar0 + 8u * (18 + s); };
   auto sfull_bar = [&](int w) { return bar0 + 8u * (20 + w); };
-  auto pfull_bar = [&](int w) { return bar0 + 8u * (22 + w); };
+  auto pfull_bar = [&](int w, int half) { return bar0 + 8u * (half ? 47 + w : 22 + w); };  // 64 keys of P each
   auto ofull_bar = [&](int w) { return bar0 + 8u * (24 + w); };
   auto oempty_bar = [&](int w) { return bar0 + 8u * (26 + w); };
   const uint32_t join_bar = bar0 + 8u * 28, drain_bar = bar0 + 8u * 29, drain2_bar = bar0 + 8u * 46;
   auto ifull_bar = [&](int i) { return bar0 + 8u * (30 + i); };
   auto iempty_bar = [&](int i) { return bar0 + 8u * (34 + i); };
   auto land_bar = [&](int s) { return bar0 + 8u * (38 + s); };  // values that are cleaned before they are full
-  // after the barriers (47 of them, 376 bytes)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 376);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 380);
-  volatile int* poisoned = reinterpret_cast<volatile int*>(head + 2464);   // [kItems]
-  Item* s_item = reinterpret_cast<Item*>(head + 384);                      // [kItems]
-  float2* s_ml = reinterpret_cast<float2*>(head + 640);                    // [128]
-  long long* s_part = reinterpret_cast<long long*>(head + 1664);           // [kGroups + 1]
-  int* s_count = reinterpret_cast<int*>(head + 2192);                      // [kGroups + 1]
+  // after the barriers (49 of them, 392 bytes)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 400);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 404);
+  volatile int* poisoned = reinterpret_cast<volatile int*>(head + 416);    // [kPoisoned]
+  Item* s_item = reinterpret_cast<Item*>(head + 448);                      // [kItems]
+  float2* s_ml = reinterpret_cast<float2*>(head + 704);                    // [128]
+  long long* s_part = reinterpret_cast<long long*>(head + 1728);           // [kGroups + 1]
+  int* s_count = reinterpret_cast<int*>(head + 2256);                      // [kGroups + 1]
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < 8; ++s) {
       mbar_init(full_bar(s), maps.use ? 1 : kLoaders);
-      mbar_init(empty_bar(s), 2);  // both MMA warps, or one twice
+      mbar_init(empty_bar(s), 2);  // both MMA warps
       mbar_init(land_bar(s), 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(qfull_bar(w), maps.use ? 1 : kLoaders);
       mbar_init(qempty_bar(w), 2);
       mbar_init(sfull_bar(w), 1);
-      mbar_init(pfull_bar(w), 128);
+      mbar_init(pfull_bar(w, 0), 128);
+      mbar_init(pfull_bar(w, 1), 128);
       mbar_init(ofull_bar(w), 1);
       mbar_init(oempty_bar(w), 128);
     }
@@ -434,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     for (int i = 0; i < kItems; ++i) {
       mbar_init(ifull_bar(i), 1);
       mbar_init(iempty_bar(i), kItemReaders);
-      poisoned[i] = 0;
     }
+    for (int i = 0; i < kPoisoned; ++i) poisoned[i] = 0;
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -513,10 +518,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     Place<2> qring = {0, 0};
     uint32_t landed = 0;  // parities of the land barriers, a bit each
     bool ok = true;
-    // Warp 8 decodes the next item and hands it out.
+    // Decodes the next item and hands it out (after the last: ends).
+    int handed = 0;
     auto hand_out = [&]() -> bool {
-      const int i = seq_no % kItems;
-      if (!wait_bar(iempty_bar(i), ((seq_no / kItems) & 1) ^ 1, ctl)) return false;
+      const int i = handed % kItems;
+      if (!wait_bar(iempty_bar(i), ((handed / kItems) & 1) ^ 1, ctl)) return false;
+      ++handed;
       Item x = {};
       x.end = next >= total;
       if (!x.end) {
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       // per ring place: whether it was filled, by which barrier, in which parity
       uint32_t filled = 0, by_land = 0, parity = 0, qfilled = 0, qparity = 0;
       while (ok) {
-        ok = hand_out() && next_item();
+        ok = next_item();
         if (!ok) break;
         const int n = __shfl_sync(~0u, it.blocks, 0);
         if (n == 0) continue;
@@ -668,7 +675,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
     } else if (maps.use) {
       // -------------- values that some row does not see, and tails --------------
-      while (ok && next_item()) {
+      // This warp also hands out the items, two ahead of the one that it cleans
+      // (never more: the ring of items would wait for this warp itself).
+      for (int i = 0; i < 2 && ok; ++i) ok = hand_out();
+      while (ok) {
+        ok = hand_out() && next_item();
+        if (!ok) break;
         const int n = it.blocks;
         if (n == 0) continue;
         const int item_no = seq_no - 1;
@@ -698,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
             if (__any_sync(~0u, (acc & 0x80008000u) != 0)) {
               for (int i = lane; i < rows * kChunks; i += 32) clean_chunk(chunk_at(tile, i / kChunks, i % kChunks));
-              if (lane == 0) poisoned[item_no % kItems] = item_no + 1;
+              if (lane == 0) poisoned[item_no % kPoisoned] = item_no + 1;
             }
           }
           fence_proxy_async_shared();
@@ -765,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               bool found = false;
               for (int r0 = 0; r0 < 64; r0 += kRows)
                 found |= clean_chunk(chunk_at(dst, lw * 64 + r0 + lane / kChunks, lane % kChunks));
-              if (found) poisoned[item_no % kItems] = item_no + 1;
+              if (found) poisoned[item_no % kPoisoned] = item_no + 1;
               fence_proxy_async_shared();
               mbar_arrive(full_bar(ring.slot));
             }
@@ -787,43 +799,65 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int w = warp - 10;
     const uint32_t id_s = idesc_f16(kType, kTile, false), id_o = idesc_f16(kType, DP, true);
     const uint32_t tS = tmem + kColS + w * 128, tO = tmem + kColO + w * 128;
+    // Both warps go over every tile of the rings in order and let go of each,
+    // its own ones by the completion of the MMAs that read them: a wait tells
+    // two rounds of a barrier apart by parity alone, so a warp that skipped a
+    // tile could take the round before last for the one that it waits for.
     const uint64_t qd0 = desc_kmajor(sQ), kd0 = desc_kmajor(sKV), vd0 = desc_mnmajor(sKV);
     Place<kStages> ring = {0, 0};
     Place<2> qring = {0, 0};
     uint32_t uses = 0, steps = 0;  // parities of O's items and of S's steps
     bool ok = true;
+    auto pass = [&](uint32_t full, uint32_t parity, uint32_t empty) -> bool {  // a tile of the other warp's
+      if (!wait_bar(full, parity, ctl)) return false;
+      if (elect_one()) mbar_arrive(empty);
+      return true;
+    };
     while (ok && next_item()) {
       const int n = __shfl_sync(~0u, it.blocks, 0), two = __shfl_sync(~0u, it.two, 0);
       if (n == 0) continue;
-      const int count = two ? n : (n + 1 - w) / 2;  // blocks of this warpgroup: all, or every other one
-      const bool alone_q = two || n == 1;           // nobody else reads the query tile
+      const int last = two ? n - 1 : n - 1 - ((n - 1 - w) & 1);  // this warpgroup's last block; below w: none
       Place<2> q = qring;
-      if (two && w) q.step(1);
-      Place<kStages> at = ring;                     // K of the next block; its V is the next place
-      if (!two && w) at.step(2);
-      Place<kStages> vat = at;
-      for (int j = 0; j <= count && count > 0; ++j) {
-        if (j > 0) {
+      if (two) {
+        Place<2> o = qring;
+        (w ? q : o).step(1);
+        ok = pass(qfull_bar(o.slot), o.parity, qempty_bar(o.slot));
+      }
+      if (ok) ok = last < w && !two ? pass(qfull_bar(q.slot), q.parity, qempty_bar(q.slot))
+                                    : wait_bar(qfull_bar(q.slot), q.parity, ctl);
+      Place<kStages> at = ring, vat = ring;  // K of block b, V of the block whose P is awaited
+      int pending = -1;
+      bool first = true;
+      for (int b = 0; b <= n && ok; ++b) {
+        if (pending >= 0) {
           vat.step(1);
-          if (j == 1 && !wait_bar(oempty_bar(w), uses ^ 1, ctl)) { ok = false; break; }
-          if (!wait_bar(full_bar(vat.slot), vat.parity, ctl)) { ok = false; break; }
+          if (first) ok = wait_bar(oempty_bar(w), uses ^ 1, ctl);
+          if (!ok || !wait_bar(full_bar(vat.slot), vat.parity, ctl)) { ok = false; break; }
           fence_proxy_async_shared();
-          if (!wait_bar(pfull_bar(w), steps, ctl)) { ok = false; break; }
-          steps ^= 1;
-          tc_fence_after();
           const uint64_t vd = vd0 + (uint64_t)(vat.slot * (Sz::tile >> 4));
-          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
-              tc_mma_ts(tO, tS + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o, j > 1 || k != 0);
-            tc_commit(empty_bar(vat.slot));
-            if (!two) tc_commit(empty_bar(vat.slot));
-            if (j == count) tc_commit(ofull_bar(w));
+          for (int half = 0; half < 2; ++half) {
+            if (ok) ok = wait_bar(pfull_bar(w, half), steps, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
+                tc_mma_ts(tO, tS + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o, !first || k != 0);
+              if (half) {
+                tc_commit(empty_bar(vat.slot));
+                if (pending == last) tc_commit(ofull_bar(w));
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
+          steps ^= 1;
+          first = false;
+          pending = -1;
         }
-        if (j < count) {
-          if (j == 0 && !wait_bar(qfull_bar(q.slot), q.parity, ctl)) { ok = false; break; }
+        if (b == n) break;
+        if (two || (b & 1) == w) {
           if (!wait_bar(full_bar(at.slot), at.parity, ctl)) { ok = false; break; }
           fence_proxy_async_shared();  // tiles may have been written by cp.async or cleaned
           tc_fence_after();
@@ -837,18 +871,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
             tc_commit(sfull_bar(w));
             tc_commit(empty_bar(at.slot));
-            if (!two) tc_commit(empty_bar(at.slot));
-            if (j + 1 == count) {
-              tc_commit(qempty_bar(q.slot));
-              if (alone_q) tc_commit(qempty_bar(q.slot));
-            }
+            if (b == last) tc_commit(qempty_bar(q.slot));
           }
           __syncwarp();
           vat = at;
-          at.step(two ? 2 : 4);
+          pending = b;
+          at.step(2);
+        } else {
+          for (int i = 0; i < 2 && ok; ++i, at.step(1)) ok = pass(full_bar(at.slot), at.parity, empty_bar(at.slot));
         }
       }
-      if (count > 0) uses ^= 1;
+      if (!first) uses ^= 1;
       ring.skip(2 * n);
       qring.skip(1 + two);
     }
@@ -891,6 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         if (!wait_bar(sfull_bar(w), steps_done & 1, ctl)) { ok = false; break; }
         ++steps_done;
+        __syncwarp();
         tc_fence_after();
         uint32_t s[kTile];
 #pragma unroll
@@ -944,13 +978,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             p[j / 2] = pack2<kType>(p0, p1);
           }
           tc_st32(tS + h / 2, p);
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(pfull_bar(w, h / 64));  // O += P V may start on this half
         }
         float l0, l1;
         split_pair(add2(sum[0], sum[1]), l0, l1);
         l += l0 + l1;
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(pfull_bar(w));
       }
       if (!ok) break;
       // ------------------------------ epilogue ------------------------------
@@ -970,7 +1004,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (!wait_bar(ofull_bar(w), uses & 1, ctl)) break;
         ++uses;
         if (other) {
-          if (!wait_bar(ofull_bar(1), uses1 & 1, ctl) || !wait_bar(join_bar, joins & 1, ctl)) break;
+          // (the second warpgroup first: once it is done with this item, O's
+          // last round is known to be over, and the parity tells which it is)
+          if (!wait_bar(join_bar, joins & 1, ctl) || !wait_bar(ofull_bar(1), uses1 & 1, ctl)) break;
           ++joins;
           const float2 ml = s_ml[r];
           const float top = fmaxf(m, ml.x);
@@ -982,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         uses1 += two || other;
         tc_fence_after();
       }
-      const bool bad = n > 0 && poisoned[(seq_no - 1) % kItems] == seq_no;
+      const bool bad = n > 0 && poisoned[(seq_no - 1) % kPoisoned] == seq_no;
       const bool cut = it.pieces > 1;
       const int h = it.kvh * group + r % group;
       const long long part = it.part + (long long)i * a.heads_q + h;
@@ -991,8 +1027,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       float inv = 1.0f;
       if (!cut) inv = l != 0.0f ? 1.0f / l : (valid && sees_any(a, t_row, it.nk, it.nq, limit) ? NAN : 0.0f);
       uint16_t* out = a.out.p + (long long)t_row * a.out.ts + (long long)h * a.out.hs;
+      float* part_o = a.part_o + part * a.head_dim;
       uint32_t o[32];
+#pragma unroll 1
       for (int j = 0; j < DP; j += 32) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+        __syncwarp();
         if (n > 0) {
           tc_ld32(tO + j, o);
           tc_wait_ld();
@@ -1004,46 +1045,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             for (int e = 0; e < 32; ++e)
               o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
           }
-          if (l == 0.0f) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          if (j + 32 >= DP) {  // O has been read
+            tc_fence_before();
+            mbar_arrive(oempty_bar(w));
+            if (other) mbar_arrive(oempty_bar(1));
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (bad && valid) {
-          // add the values that are not finite, for the keys that this row sees
-          const int from = max(it.b0, limit_of(a, it.nk, it.nq, it.i0) / kTile) * kTile;
-          for (int pos = from; pos < min((it.b0 + n) * kTile, it.nk); ++pos) {
-            if (!((seen_bits(a, t_row, it.nk, it.nq, limit, pos & ~31) >> (pos & 31)) & 1u)) continue;
-            long long row = (long long)it.k0 + pos;
-            if (a.paged) {
-              const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + pos / a.page_size);
-              if (p < 0 || p >= a.n_pages) continue;
-              row = (long long)p * a.page_size + pos % a.page_size;
-            }
-            const uint16_t* v = a.v.p + row * a.v.ts + (long long)it.kvh * a.v.hs;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (j + e < a.head_dim) {
-                const float x = to_f32<kType>(v[j + e]);
-                if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
-              }
-          }
-        }
-        if (j + 32 >= DP && n > 0) {  // O has been read
-          tc_fence_before();
-          mbar_arrive(oempty_bar(w));
-          if (other) mbar_arrive(oempty_bar(1));
         }
         if (keep) {
-          float4* to = reinterpret_cast<float4*>(a.part_o + part * a.head_dim + j);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             if (j + e < a.head_dim)
-              to[e / 4] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                      __uint_as_float(o[e + 3]));
+              *reinterpret_cast<float4*>(part_o + j + e) = make_float4(
+                  __uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
         } else if (!cut && valid) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
@@ -1055,6 +1068,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               v.w = pack2<kType>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
               *reinterpret_cast<uint4*>(out + j + e) = v;
             }
+        }
+      }
+      if (bad && valid && (keep || !cut)) {
+        // add the values that are not finite of the keys that this row sees (a
+        // rare path: kept small, not fast)
+        const int from = max(it.b0, limit_of(a, it.nk, it.nq, it.i0) / kTile) * kTile;
+#pragma unroll 1
+        for (int d = 0; d < a.head_dim; ++d) {
+          float sum = 0.0f;
+#pragma unroll 1
+          for (int pos = from; pos < min((it.b0 + n) * kTile, it.nk); ++pos) {
+            if (!((seen_bits(a, t_row, it.nk, it.nq, limit, pos & ~31) >> (pos & 31)) & 1u)) continue;
+            long long row = (long long)it.k0 + pos;
+            if (a.paged) {
+              const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + pos / a.page_size);
+              if (p < 0 || p >= a.n_pages) continue;
+              row = (long long)p * a.page_size + pos % a.page_size;
+            }
+            const float x = to_f32<kType>(a.v.p[row * a.v.ts + (long long)it.kvh * a.v.hs + d]);
+            if (!isfinite(x)) sum += x;
+          }
+          if (sum != 0.0f) {  // not finite, or nothing
+            if (cut) part_o[d] += sum;
+            else out[d] = (uint16_t)pack2<kType>(to_f32<kType>(out[d]) + sum, 0.0f);
+          }
         }
       }
       if (valid) {
@@ -1071,6 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 10) {
