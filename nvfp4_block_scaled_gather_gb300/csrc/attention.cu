@@ -64,8 +64,9 @@ constexpr float kLazy = 8.0f;    // powers of two that a score may exceed the ru
 template <int DP>
 struct Sizes {
   static constexpr int tile = kTile * DP * 2;       // bytes of 128 rows
-  static constexpr int stages = DP == 128 ? 5 : 8;  // 160 KB, 128 KB in flight
-  static constexpr int smem = 2 * tile + stages * tile + kHeader;
+  static constexpr int stages = DP == 128 ? 4 : 8;  // 128 KB in flight
+  static constexpr int stage = 8 * 32 * DP;         // output staging: a warp's 32 rows of DP / 2 values
+  static constexpr int smem = 2 * tile + stages * tile + stage + kHeader;
 };
 
 // ------------------------------- PTX helpers --------------------------------
@@ -163,6 +164,20 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// The two warps that share 32 rows meet (named barrier `id`); whether any thread says so.
+__device__ __forceinline__ bool pair_any(int id, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(any)
+      : "r"(id), "r"(mine ? 1u : 0u)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -260,9 +275,9 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl c) 
     }
   }
 }
-// False if this or another role gave up.
+// By a whole warp, the same answer in every lane: false if this or another role gave up.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ctl& c) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, c);
+  return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_slow(bar, parity, c));
 }
 
 // ---------------------------------- the plan ----------------------------------
@@ -393,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     return;
   }
   const uint32_t sQ = smem_u32(smem), sKV = sQ + 2 * Sz::tile;
-  uint8_t* head = smem + (2 + kStages) * Sz::tile;
+  uint8_t* head = smem + (2 + kStages) * Sz::tile + Sz::stage;
   uint64_t* bars = reinterpret_cast<uint64_t*>(head);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -404,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   auto pfull_bar = [&](int w, int half) { return bar0 + 8u * (half ? 47 + w : 22 + w); };  // 64 keys of P each
   auto ofull_bar = [&](int w) { return bar0 + 8u * (24 + w); };
   auto oempty_bar = [&](int w) { return bar0 + 8u * (26 + w); };
-  const uint32_t join_bar = bar0 + 8u * 28, drain_bar = bar0 + 8u * 29, drain2_bar = bar0 + 8u * 46;
+  const uint32_t drain_bar = bar0 + 8u * 29, drain2_bar = bar0 + 8u * 46;
   auto ifull_bar = [&](int i) { return bar0 + 8u * (30 + i); };
   auto iempty_bar = [&](int i) { return bar0 + 8u * (34 + i); };
   auto land_bar = [&](int s) { return bar0 + 8u * (38 + s); };  // values that are cleaned before they are full
@@ -413,9 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 404);
   volatile int* poisoned = reinterpret_cast<volatile int*>(head + 416);    // [kPoisoned]
   Item* s_item = reinterpret_cast<Item*>(head + 448);                      // [kItems]
-  float2* s_ml = reinterpret_cast<float2*>(head + 704);                    // [128]
-  long long* s_part = reinterpret_cast<long long*>(head + 1728);           // [kGroups + 1]
-  int* s_count = reinterpret_cast<int*>(head + 2256);                      // [kGroups + 1]
+  long long* s_part = reinterpret_cast<long long*>(head + 704);            // [kGroups + 1]
+  int* s_count = reinterpret_cast<int*>(head + 1224);                      // [kGroups + 1]
+  float* s_top = reinterpret_cast<float*>(head + 1488);                    // [2][128]
+  uint8_t* s_stage = smem + (2 + kStages) * Sz::tile;
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
@@ -431,9 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(pfull_bar(w, 0), 128);
       mbar_init(pfull_bar(w, 1), 128);
       mbar_init(ofull_bar(w), 1);
-      mbar_init(oempty_bar(w), 128);
+      mbar_init(oempty_bar(w), 256);
     }
-    mbar_init(join_bar, 128);
     mbar_init(drain_bar, 1);
     mbar_init(drain2_bar, 1);
     for (int i = 0; i < kItems; ++i) {
@@ -506,10 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     return it.end == 0;
   };
 
-  // 168 registers a thread at launch (3 x 128 threads): 2 x 208 + 88 = 3 x 168
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp < 10) {
+  if (warp == 8 || warp == 9) {
     // ================================ loader ================================
     const int lw = warp - 8;
     const int total = s_count[kGroups] * a.heads_kv;
@@ -788,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       if (*abort_flag) cp_async_wait_all();  // nothing of ours may be in flight at exit
     }
-  } else {
+  } else if (warp >= 10) {
     // ============================== MMA issuer ==============================
     // Each of the two warps issues one softmax warpgroup's MMAs: S(0), then
     // O += P(j) V(j) and S(j + 1) in turn (S(j + 1) overwrites P(j), which the
@@ -893,220 +905,287 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       while (!mbar_try_wait(bar, 0) && clock64() - t0 < kBudget) {
       }
     }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // =============================== softmax ===============================
-    const int w = warp >> 2;             // which of the two warpgroups
+    // Both warpgroups work on every step's S, a warpgroup on 64 of its 128 keys:
+    // thread r of either has row r of the tile. The two threads of a row hold
+    // the same maximum m; each has the sum l of its own keys and, of O, half of
+    // the columns. They meet once a step (a barrier of the two warps that share
+    // 32 rows, which tells whether any of these rows' maxima moves); only where
+    // one moves do they exchange maxima. Splitting a row halves the time from S
+    // to P, which with one warpgroup a tile was longer than the other tile's
+    // MMAs.
+    const int half = warp >> 2, quad = warp & 3;
     const int r = tid & 127;             // row of the tile = lane of tensor memory
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = lanes + kColS + w * 128, tO = lanes + kColO + w * 128;
+    const int token = r / group, head_in = r - token * group;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const float c = a.scale * 1.4426950408889634f;
-    int steps_done = 0, uses = 0, uses1 = 0, joins = 0;  // uses of this O, of the second one
-    bool ok = true;
+    uint32_t steps_done = 0, uses = 0;   // bit w: parities of S w's steps, of O w's items
+    bool ok = true, agreed = false;      // agreed: the two warps of a row know from a step that they give up
     while (ok && next_item()) {
       const int n = it.blocks, two = it.two;
       const int steps = two ? 2 * n : n;
-      const int token = r / group, tok = (two ? w * tpt : 0) + token;  // in the tile, in the pair
-      const bool valid = token < tpt && tok < it.tokens;
-      const int i = it.i0 + tok, t_row = it.first + tok;
-      const int limit = valid ? limit_of(a, it.nk, it.nq, i) : 0;
-      const int lim = limit_of(a, it.nk, it.nq, it.i0 + (two ? w * tpt : 0));  // the least of the tile's rows
-      float m = -INFINITY, l = 0.0f;  // m in units of the raw scores
-      for (int t = w; t < steps; t += 2) {
+      const int rows0 = min(tpt, it.tokens) * group, rows1 = two ? (it.tokens - tpt) * group : rows0;
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // of the two S; m in units of the raw scores
+      for (int t = 0; t < steps; ++t) {
+        const int w = t & 1;
+        const int tok0 = two && w ? tpt : 0;            // first token of the tile in the pair
+        const int rows = w ? rows1 : rows0;
+        const bool live = quad * 32 < rows;             // any row of this warp's
         const int pos = (it.b0 + (two ? t >> 1 : t)) * kTile;
-        const bool edge = pos + kTile > lim;  // some row does not see all of the block
-        uint32_t bits[kTile / 32];
-        if (edge) {
+        // some row of the tile does not see all of the block
+        const bool edge = pos + kTile > limit_of(a, it.nk, it.nq, it.i0 + tok0);
+        uint32_t bits[2] = {0u, 0u};
+        if (edge && live && r < rows) {
+          const int i = it.i0 + tok0 + token, limit = limit_of(a, it.nk, it.nq, i);
 #pragma unroll
-          for (int j = 0; j < kTile; j += 32)
-            bits[j / 32] = valid ? seen_bits(a, t_row, it.nk, it.nq, limit, pos + j) : 0u;
+          for (int j = 0; j < 2; ++j)
+            bits[j] = seen_bits(a, it.first + tok0 + token, it.nk, it.nq, limit, pos + half * 64 + j * 32);
         }
-        if (!wait_bar(sfull_bar(w), steps_done & 1, ctl)) { ok = false; break; }
-        ++steps_done;
-        __syncwarp();
-        tc_fence_after();
-        uint32_t s[kTile];
+        bool here = wait_bar(sfull_bar(w), (steps_done >> w) & 1, ctl);
+        steps_done ^= 1u << w;
+        if (live) {
+          const uint32_t tS = lanes + kColS + w * 128, tO = lanes + kColO + w * 128 + half * (DP / 2);
+          float m = w ? m1 : m0, l = w ? l1 : l0;
+          tc_fence_after();
+          uint32_t s[64];
+          tc_ld32(tS + half * 64, s);
+          tc_ld32(tS + half * 64 + 32, s + 32);
+          tc_wait_ld();
+          if (edge) {
 #pragma unroll
-        for (int j = 0; j < kTile; j += 32) tc_ld32(tS + j, s + j);
-        tc_wait_ld();
-        if (edge) {
+            for (int j = 0; j < 64; ++j)
+              if (!((bits[j / 32] >> (j % 32)) & 1u)) s[j] = 0xFF800000u;  // -inf
+          }
+          float mx[4];
 #pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (!((bits[j / 32] >> (j % 32)) & 1u)) s[j] = 0xFF800000u;  // -inf
-        }
-        float mx[4];
+          for (int u = 0; u < 4; ++u)
+            mx[u] = max3(__uint_as_float(s[u]), __uint_as_float(s[u + 4]), __uint_as_float(s[u + 8]));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = max3(__uint_as_float(s[u]), __uint_as_float(s[u + 4]), __uint_as_float(s[u + 8]));
+          for (int j = 12; j + 8 <= 64; j += 8)
 #pragma unroll
-        for (int j = 12; j + 8 <= kTile; j += 8)
+            for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], __uint_as_float(s[j + u]), __uint_as_float(s[j + 4 + u]));
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], __uint_as_float(s[j + u]), __uint_as_float(s[j + 4 + u]));
-#pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(s[kTile - 4 + u]));
-        const float top = max3(max3(m, mx[0], mx[1]), mx[2], mx[3]);
-        const bool move = top > m && !((top - m) * c <= kLazy);
-        if (t >= 2 && __any_sync(~0u, move)) {
-          // S(t) is complete, so is every earlier MMA: O can be rescaled
-          const float f = move ? ex2((m - top) * c) : 1.0f;
-          l *= f;
-          uint32_t o[32];
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(s[60 + u]));
+          float top = max3(max3(m, mx[0], mx[1]), mx[2], mx[3]);
+          // a warp whose wait gave up still meets the other one here, and tells
+          if (!here) top = __int_as_float(0x7fffffff);
+          if (pair_any(1 + quad, !here || (top > m && !((top - m) * c <= kLazy)))) {
+            s_top[half * 128 + r] = top;
+            pair_sync(1 + quad);
+            const float theirs = s_top[(half ^ 1) * 128 + r];
+            here = __all_sync(~0u, __float_as_int(top) != 0x7fffffff && __float_as_int(theirs) != 0x7fffffff);
+            agreed = !here;
+            top = fmaxf(top, theirs);
+            const bool move = here && top > m && !((top - m) * c <= kLazy);
+            if (here && t >= 2 && __any_sync(~0u, move)) {
+              // S(t) is complete, so is every earlier MMA: O can be rescaled
+              const float f = move ? ex2((m - top) * c) : 1.0f;
+              l *= f;
+              uint32_t o[32];
 #pragma unroll 1
-          for (int j = 0; j < DP; j += 32) {
-            tc_ld32(tO + j, o);
-            tc_wait_ld();
+              for (int j = 0; j < DP / 2; j += 32) {
+                tc_ld32(tO + j, o);
+                tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tc_st32(tO + j, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tc_st32(tO + j, o);
+              }
+            }
+            if (move) m = top;
+          }
+          if (here) {
+            const float base = m == -INFINITY ? 0.0f : -m * c;
+            const uint64_t c2 = pair_of(c, c), base2 = pair_of(base, base);
+            uint64_t sum[2] = {0, 0};
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+              const uint64_t x = fma2(pair_of(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), c2, base2);
+              float p0, p1;
+              split_pair(x, p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair_of(p0, p1));
+              p[j / 2] = pack2<kType>(p0, p1);
+            }
+            tc_st32(tS + half * 32, p);
+            float a0, a1;
+            split_pair(add2(sum[0], sum[1]), a0, a1);
+            l += a0 + a1;
+            tc_wait_st();
+          }
+          if (w) {
+            m1 = m;
+            l1 = l;
+          } else {
+            m0 = m;
+            l0 = l;
           }
         }
-        if (move) m = top;
-        const float base = m == -INFINITY ? 0.0f : -m * c;
-        const uint64_t c2 = pair_of(c, c), base2 = pair_of(base, base);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int h = 0; h < kTile; h += 64) {
-          uint32_t p[32];
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const uint64_t x = fma2(pair_of(__uint_as_float(s[h + j]), __uint_as_float(s[h + j + 1])), c2, base2);
-            float p0, p1;
-            split_pair(x, p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair_of(p0, p1));
-            p[j / 2] = pack2<kType>(p0, p1);
-          }
-          tc_st32(tS + h / 2, p);
-          tc_wait_st();
-          tc_fence_before();
-          mbar_arrive(pfull_bar(w, h / 64));  // O += P V may start on this half
-        }
-        float l0, l1;
-        split_pair(add2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
+        ok = here;
+        if (!ok) break;
+        tc_fence_before();
+        mbar_arrive(pfull_bar(w, half));
       }
       if (!ok) break;
       // ------------------------------ epilogue ------------------------------
-      const bool other = !two && n > 1;  // one tile: the second warpgroup holds half of the result
-      if (!two && w == 1) {
-        if (n > 1) {
-          // not before the last item's result has been read
-          if (!wait_bar(oempty_bar(1), (uses & 1) ^ 1, ctl)) break;
-          ++uses;
-          s_ml[r] = make_float2(m, l);
-          mbar_arrive(join_bar);
-        }
-        continue;
-      }
-      float f0 = 1.0f, f1 = 0.0f;
-      if (n > 0) {
-        if (!wait_bar(ofull_bar(w), uses & 1, ctl)) break;
-        ++uses;
-        if (other) {
-          // (the second warpgroup first: once it is done with this item, O's
-          // last round is known to be over, and the parity tells which it is)
-          if (!wait_bar(join_bar, joins & 1, ctl) || !wait_bar(ofull_bar(1), uses1 & 1, ctl)) break;
-          ++joins;
-          const float2 ml = s_ml[r];
-          const float top = fmaxf(m, ml.x);
-          f0 = m == -INFINITY ? 1.0f : ex2((m - top) * c);
-          f1 = ml.x == -INFINITY ? 1.0f : ex2((ml.x - top) * c);
-          l = l * f0 + ml.y * f1;
-          m = top;
-        }
-        uses1 += two || other;
-        tc_fence_after();
-      }
-      const bool bad = n > 0 && poisoned[(seq_no - 1) % kPoisoned] == seq_no;
+      const bool other = !two && n > 1;  // one tile: the second O holds the other half of its blocks
       const bool cut = it.pieces > 1;
-      const int h = it.kvh * group + r % group;
-      const long long part = it.part + (long long)i * a.heads_q + h;
-      const bool keep = cut && valid && part < a.part_rows;
-      // a row that sees no key gives 0; one whose scores are all -inf has no value
-      float inv = 1.0f;
-      if (!cut) inv = l != 0.0f ? 1.0f / l : (valid && sees_any(a, t_row, it.nk, it.nq, limit) ? NAN : 0.0f);
-      uint16_t* out = a.out.p + (long long)t_row * a.out.ts + (long long)h * a.out.hs;
-      float* part_o = a.part_o + part * a.head_dim;
-      uint32_t o[32];
+      const int h = it.kvh * group + head_in;
+      const float top = other ? fmaxf(m0, m1) : m0;
+      const float f0 = other && m0 != -INFINITY ? ex2((m0 - top) * c) : 1.0f;
+      const float f1 = m1 != -INFINITY ? ex2((m1 - top) * c) : 1.0f;
+      if (other) {
+        l0 = l0 * f0 + l1 * f1;
+        m0 = top;
+      }
+      if (n > 0 && quad * 32 < rows0) {  // the row's sum is that of its two threads
 #pragma unroll 1
-      for (int j = 0; j < DP; j += 32) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0u;
-        __syncwarp();
+        for (int w = 0; w <= two && !agreed; ++w) {
+          agreed = pair_any(1 + quad, false);  // (the last exchange has been read) the other one gives up
+          s_top[half * 128 + r] = w ? l1 : l0;
+          pair_sync(1 + quad);
+          const float theirs = s_top[(half ^ 1) * 128 + r];
+          if (w) l1 += theirs;
+          else l0 += theirs;
+        }
+      }
+      ok = !agreed;
+#pragma unroll 1
+      for (int w = 0; w <= two && ok; ++w) {
+        const int tok = (w ? tpt : 0) + token;
+        const bool live = quad * 32 < (w ? rows1 : rows0), valid = r < (w ? rows1 : rows0);
+        const float m = w ? m1 : m0, l = w ? l1 : l0;
+        const uint32_t tO = lanes + kColO + w * 128 + half * (DP / 2);
         if (n > 0) {
-          tc_ld32(tO + j, o);
-          tc_wait_ld();
-          if (other) {
-            uint32_t o1[32];
-            tc_ld32(tO + 128 + j, o1);
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
-          }
-          if (j + 32 >= DP) {  // O has been read
-            tc_fence_before();
-            mbar_arrive(oempty_bar(w));
-            if (other) mbar_arrive(oempty_bar(1));
-          }
+          ok = wait_bar(ofull_bar(w), (uses >> w) & 1, ctl);
+          if (ok && other) ok = wait_bar(ofull_bar(1), (uses >> 1) & 1, ctl);
+          if (!ok) break;
+          uses ^= other ? 3u : 1u << w;
+          __syncwarp();
+          tc_fence_after();
         }
-        if (keep) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            if (j + e < a.head_dim)
-              *reinterpret_cast<float4*>(part_o + j + e) = make_float4(
-                  __uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-        } else if (!cut && valid) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            if (j + e < a.head_dim) {
-              uint4 v;
-              v.x = pack2<kType>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-              v.y = pack2<kType>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-              v.z = pack2<kType>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-              v.w = pack2<kType>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-              *reinterpret_cast<uint4*>(out + j + e) = v;
-            }
-        }
-      }
-      if (bad && valid && (keep || !cut)) {
-        // add the values that are not finite of the keys that this row sees (a
-        // rare path: kept small, not fast)
-        const int from = max(it.b0, limit_of(a, it.nk, it.nq, it.i0) / kTile) * kTile;
+        // (O is complete, so every block's values have been through the cleaning)
+        const bool bad = n > 0 && poisoned[(seq_no - 1) % kPoisoned] == seq_no;
+        const int i = it.i0 + tok, t_row = it.first + tok;
+        const int limit = valid ? limit_of(a, it.nk, it.nq, i) : 0;
+        const long long part = it.part + (long long)i * a.heads_q + h;
+        const bool keep = cut && valid && part < a.part_rows;
+        // a row that sees no key gives 0; one whose scores are all -inf has no value
+        float inv = 1.0f;
+        if (!cut) inv = l != 0.0f ? 1.0f / l : (valid && sees_any(a, t_row, it.nk, it.nq, limit) ? NAN : 0.0f);
+        const long long at = valid && !cut ? (long long)t_row * a.out.ts + (long long)h * a.out.hs : -1;
+        float* part_o = a.part_o + part * a.head_dim + half * (DP / 2);
+        constexpr int kC = DP / 16;            // 16-byte chunks of a warp's half row
+        const uint32_t stage = (uint32_t)(warp * 32 * kC * 16);
+        if (live) {
 #pragma unroll 1
-        for (int d = 0; d < a.head_dim; ++d) {
-          float sum = 0.0f;
-#pragma unroll 1
-          for (int pos = from; pos < min((it.b0 + n) * kTile, it.nk); ++pos) {
-            if (!((seen_bits(a, t_row, it.nk, it.nq, limit, pos & ~31) >> (pos & 31)) & 1u)) continue;
-            long long row = (long long)it.k0 + pos;
-            if (a.paged) {
-              const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + pos / a.page_size);
-              if (p < 0 || p >= a.n_pages) continue;
-              row = (long long)p * a.page_size + pos % a.page_size;
+          for (int j = 0; j < DP / 2; j += 32) {
+            uint32_t o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+            __syncwarp();
+            if (n > 0) {
+              tc_ld32(tO + j, o);
+              tc_wait_ld();
+              if (other) {
+                uint32_t o1[32];
+                tc_ld32(tO + 128 + j, o1);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+              }
             }
-            const float x = to_f32<kType>(a.v.p[row * a.v.ts + (long long)it.kvh * a.v.hs + d]);
-            if (!isfinite(x)) sum += x;
-          }
-          if (sum != 0.0f) {  // not finite, or nothing
-            if (cut) part_o[d] += sum;
-            else out[d] = (uint16_t)pack2<kType>(to_f32<kType>(out[d]) + sum, 0.0f);
+            if (cut) {
+              if (keep) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  if (half * (DP / 2) + j + e < a.head_dim)
+                    *reinterpret_cast<float4*>(part_o + j + e) =
+                        make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                    __uint_as_float(o[e + 3]));
+              }
+            } else {
+              // to shared memory, so that the stores below write whole lines
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint4 v;
+                v.x = pack2<kType>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                v.y = pack2<kType>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                v.z = pack2<kType>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                v.w = pack2<kType>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                const int chunk = (j + e) / 8;
+                *reinterpret_cast<uint4*>(s_stage + stage + (lane * kC + (chunk ^ (lane & (kC - 1)))) * 16) = v;
+              }
+            }
           }
         }
-      }
-      if (valid) {
-        const long long row = (long long)t_row * a.heads_q + h;
-        if (cut) {
-          if (keep) a.part_ml[part] = make_float2(m * c, l);
-          else report(a.status, MOE_ERR_INVALID);
-          if (it.piece == 0)
-            a.part_of[row] = make_int4(keep ? (int)part : -1, it.pieces, it.rows, sees_any(a, t_row, it.nk, it.nq, limit));
-        } else {
-          if (a.part_of) a.part_of[row] = make_int4(-1, 0, 0, 0);
-          if (a.lse) a.lse[row] = l != 0.0f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (n > 0) {  // O has been read
+          tc_fence_before();
+          mbar_arrive(oempty_bar(w));
+          if (other) mbar_arrive(oempty_bar(1));
         }
+        if (live && !cut) {
+          __syncwarp();
+          const int chunk = lane % kC, column = half * (DP / 2) + chunk * 8;
+#pragma unroll
+          for (int y = 0; y < kC; ++y) {
+            const int row = y * (32 / kC) + lane / kC;
+            const long long to = __shfl_sync(~0u, at, row);
+            const uint4 v = *reinterpret_cast<const uint4*>(s_stage + stage + (row * kC + (chunk ^ (row & (kC - 1)))) * 16);
+            if (to >= 0 && column < a.head_dim) *reinterpret_cast<uint4*>(a.out.p + to + column) = v;
+          }
+          __syncwarp();
+        }
+        if (bad && valid && (keep || !cut)) {
+          // add the values that are not finite of the keys that this row sees (a
+          // rare path: kept small, not fast)
+          const int from = max(it.b0, limit_of(a, it.nk, it.nq, it.i0) / kTile) * kTile;
+          uint16_t* out = a.out.p + at + half * (DP / 2);
+#pragma unroll 1
+          for (int d = 0; d < min(DP / 2, a.head_dim - half * (DP / 2)); ++d) {
+            float sum = 0.0f;
+#pragma unroll 1
+            for (int pos = from; pos < min((it.b0 + n) * kTile, it.nk); ++pos) {
+              if (!((seen_bits(a, t_row, it.nk, it.nq, limit, pos & ~31) >> (pos & 31)) & 1u)) continue;
+              long long row = (long long)it.k0 + pos;
+              if (a.paged) {
+                const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + pos / a.page_size);
+                if (p < 0 || p >= a.n_pages) continue;
+                row = (long long)p * a.page_size + pos % a.page_size;
+              }
+              const float x = to_f32<kType>(a.v.p[row * a.v.ts + (long long)it.kvh * a.v.hs + half * (DP / 2) + d]);
+              if (!isfinite(x)) sum += x;
+            }
+            if (sum != 0.0f) {  // not finite, or nothing
+              if (cut) part_o[d] += sum;
+              else out[d] = (uint16_t)pack2<kType>(to_f32<kType>(out[d]) + sum, 0.0f);
+            }
+          }
+        }
+        if (valid && half == 0) {
+          const long long row = (long long)t_row * a.heads_q + h;
+          if (cut) {
+            if (keep) a.part_ml[part] = make_float2(m * c, l);
+            else report(a.status, MOE_ERR_INVALID);
+            if (it.piece == 0)
+              a.part_of[row] = make_int4(keep ? (int)part : -1, it.pieces, it.rows, sees_any(a, t_row, it.nk, it.nq, limit));
+          } else {
+            if (a.part_of) a.part_of[row] = make_int4(-1, 0, 0, 0);
+            if (a.lse) a.lse[row] = l != 0.0f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+        __syncwarp();
       }
+    }
+    // Every meeting of two warps begins with pair_any. If this one gave up
+    // where the other one does not know (or the other way round), that one
+    // will wait in its next meeting, or here: so they meet once more.
+    if (!agreed && pair_any(1 + quad, !ok || *abort_flag != 0)) {
+      s_top[half * 128 + r] = __int_as_float(0x7fffffff);
+      pair_sync(1 + quad);
     }
   }
   __syncwarp();
