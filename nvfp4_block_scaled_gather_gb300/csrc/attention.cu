@@ -52,20 +52,20 @@ namespace {
 constexpr int kTile = 128;       // query rows of a tile, keys of a block
 constexpr int kThreads = 384;
 constexpr int kLoaders = 64;     // threads that load by cp.async
-constexpr int kGroups = 64;      // sequences are counted in this many runs
+constexpr int kPlan = 256;       // sequences whose plan is kept in shared memory, a thread each
 constexpr int kItems = 4;        // work items between the loader and the other roles
 constexpr int kPoisoned = 8;     // more than the items that a loader can be ahead by
 constexpr int kItemReaders = 12;  // every warp
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // S (and P over it) and O of each softmax warpgroup, 128 columns apart
-constexpr int kHeader = 3072;
+constexpr int kHeader = 16384;
 constexpr float kLazy = 8.0f;    // powers of two that a score may exceed the running maximum by
 
 template <int DP>
 struct Sizes {
   static constexpr int tile = kTile * DP * 2;       // bytes of 128 rows
   static constexpr int stages = DP == 128 ? 4 : 8;  // 128 KB in flight
-  static constexpr int stage = 8 * 32 * DP;         // output staging: a warp's 32 rows of DP / 2 values
+  static constexpr int stage = 8 * 32 * 64;         // output staging: 32 rows of 32 values for each of eight warps
   static constexpr int smem = 2 * tile + stages * tile + stage + kHeader;
 };
 
@@ -76,6 +76,11 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// One arrival for a whole warp.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -108,6 +113,16 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// The same box back to global memory, and the waits of the lane that issued it:
+// until shared memory has been read, until all is written.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -310,18 +325,33 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   return s;
 }
 
-struct Shape {  // of a sequence's work
-  int pairs;    // query tile pairs
+struct __align__(16) Planned {
+  Seq seq;
+  int pairs;     // query tile pairs
   Cut cut;
-  long long part_rows;
+  int items;     // pairs x pieces
 };
-__device__ __forceinline__ Shape shape_of(const AttnArgs& a, const Seq& s, int tokens_per_tile) {
-  Shape w;
-  w.pairs = (s.nq + 2 * tokens_per_tile - 1) / (2 * tokens_per_tile);
-  const int blocks = (s.nk + kTile - 1) / kTile;
-  w.cut = a.part_o && s.nq > 0 ? cut_of(blocks, (long long)w.pairs * a.heads_kv) : Cut{1, blocks};
-  w.part_rows = w.cut.pieces > 1 ? (long long)s.nq * a.heads_q * w.cut.pieces : 0;
+static_assert(sizeof(Planned) == 32, "two 16-byte reads");
+__device__ __forceinline__ Planned plan_of(const AttnArgs& a, int b, int tokens_per_tile) {
+  Planned w;
+  w.seq = seq_of(a, b);
+  w.pairs = (w.seq.nq + 2 * tokens_per_tile - 1) / (2 * tokens_per_tile);
+  const int blocks = (w.seq.nk + kTile - 1) / kTile;
+  w.cut = a.part_o && w.seq.nq > 0 ? cut_of(blocks, w.pairs * a.heads_kv) : Cut{1, blocks};
+  w.items = w.pairs * w.cut.pieces;
   return w;
+}
+__device__ __forceinline__ long long part_rows_of(const AttnArgs& a, const Planned& w) {
+  return w.cut.pieces > 1 ? (long long)w.seq.nq * a.heads_q * w.cut.pieces : 0;
+}
+// Items of a sequence (for one kv head) of at least n key blocks: all alike,
+// or (causal) those of the later query tile pairs.
+__device__ __forceinline__ int items_from(const AttnArgs& a, const Planned& w, int n, int tokens_per_tile) {
+  if (w.items == 0 || n > w.cut.blocks) return 0;
+  if (n <= 0 || w.cut.pieces > 1 || a.mask) return w.items;
+  // pair p sees the keys before nk - nq + (p + 1) * 2 * tokens_per_tile
+  const int rest = (n - 1) * kTile - (w.seq.nk - w.seq.nq);
+  return w.pairs - (rest <= 0 ? 0 : min(rest / (2 * tokens_per_tile), w.pairs - 1));
 }
 
 struct __align__(16) Item {
@@ -371,11 +401,126 @@ __device__ __forceinline__ bool sees_any(const AttnArgs& a, int t, int nk, int n
   return any;
 }
 
-// The tensor maps of a call (boxes of 64 columns).
+// By a whole warp: this CTA's item of a round. The items stand in order of
+// falling size (number of key blocks), a kv head after the other, and are
+// dealt to the CTAs forth and back, which comes within a few per cent of the
+// best there is: 992 items of 9 ragged prompts, 992 / 152 to a CTA, end after
+// 82 steps instead of the 112 that dealing them out as they stand takes (80
+// where each CTA takes the longest that is left). With more sequences than the
+// plan holds they are dealt in the order of the call.
+__device__ __forceinline__ Item item_of(const AttnArgs& a, const Planned* s_plan, const long long* s_part, int total,
+                                        int largest, int round, int tpt) {
+  const int lane = threadIdx.x & 31;
+  Item x = {};
+  const long long next =
+      (long long)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  // (a CTA's last round can miss it, but then no later one is left)
+  x.end = next >= (long long)total * a.heads_kv;
+  if (x.end) return x;
+  const int kvh = (int)(next % a.heads_kv);
+  int u = (int)(next / a.heads_kv);  // item of this kv head
+  int b = 0, first = 0;              // its sequence, and where the sequence's items of this size begin
+  Planned w;
+  long long part;
+  if (a.n == 1) {
+    w = s_plan[0];
+    part = 0;
+  } else if (a.n <= kPlan) {
+    // the size n with (items of more than n blocks) <= u < (items of n or more)
+    auto from = [&](int n) {
+      int c = 0;
+      for (int i = lane; i < a.n; i += 32) c += items_from(a, s_plan[i], n, tpt);
+      return __reduce_add_sync(~0u, c);
+    };
+    int n = 0, above = largest + 1;
+    while (above - n > 1) {
+      const int mid = (n + above) >> 1;
+      if (from(mid) > u) n = mid;
+      else above = mid;
+    }
+    u -= from(n + 1);
+    // the sequence among those with items of this size
+    for (int i0 = 0;; i0 += 32) {
+      int more = 0, c = 0;
+      if (i0 + lane < a.n) {
+        more = items_from(a, s_plan[i0 + lane], n + 1, tpt);
+        c = items_from(a, s_plan[i0 + lane], n, tpt) - more;
+      }
+      int sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t reach = __ballot_sync(~0u, sum > u);
+      if (reach || i0 + 32 >= a.n) {
+        const int at = reach ? __ffs(reach) - 1 : 0;
+        b = i0 + at;
+        u -= __shfl_sync(~0u, sum - c, at);
+        first = __shfl_sync(~0u, more, at);
+        break;
+      }
+      u -= __shfl_sync(~0u, sum, 31);
+    }
+    w = s_plan[b];
+    part = s_part[b];
+  } else {
+    // 32 sequences at a time
+    part = 0;
+    for (int i0 = 0;; i0 += 32) {
+      Planned mine = {};
+      if (i0 + lane < a.n) mine = plan_of(a, i0 + lane, tpt);
+      int sum = mine.items;
+      long long rows = part_rows_of(a, mine);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, sum, o);
+        const long long z = __shfl_up_sync(~0u, rows, o);
+        if (lane >= o) {
+          sum += y;
+          rows += z;
+        }
+      }
+      const uint32_t reach = __ballot_sync(~0u, sum > u);
+      if (reach || i0 + 32 >= a.n) {
+        const int at = reach ? __ffs(reach) - 1 : 0;
+        u -= __shfl_sync(~0u, sum - mine.items, at);
+        part += __shfl_sync(~0u, rows - part_rows_of(a, mine), at);
+        w = plan_of(a, i0 + at, tpt);
+        break;
+      }
+      u -= __shfl_sync(~0u, sum, 31);
+      part += __shfl_sync(~0u, rows, 31);
+    }
+  }
+  u += first;
+  const Seq& s = w.seq;
+  const int pair = max(w.pairs - 1 - u / w.cut.pieces, 0);
+  x.piece = u % w.cut.pieces;
+  x.i0 = pair * 2 * tpt;
+  x.first = s.first + x.i0;
+  x.tokens = min(2 * tpt, s.nq - x.i0);
+  x.two = x.tokens > tpt;
+  x.nq = s.nq;
+  x.k0 = s.k0;
+  x.nk = s.nk;
+  x.kvh = kvh;
+  // the keys that any row of the pair sees end here
+  const int keys = a.mask ? s.nk : limit_of(a, s.nk, s.nq, x.i0 + x.tokens - 1);
+  x.b0 = x.piece * w.cut.blocks;
+  x.blocks = max(0, min((keys + kTile - 1) / kTile - x.b0, w.cut.blocks));
+  x.pieces = w.cut.pieces;
+  x.rows = s.nq * a.heads_q;
+  x.part = part + (long long)x.piece * x.rows;
+  return x;
+}
+
+// The tensor maps of a call (boxes of 64 columns, of the output 32).
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, out;
   int use;       // 0: the tiles are copied by cp.async
   int box;       // rows of a box of K and V
+  int store;     // query heads of a box of the output (32 rows); 0: it is not stored by TMA
 };
 
 // A place in the ring of tiles and the parity of its round.
@@ -424,13 +569,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   auto iempty_bar = [&](int i) { return bar0 + 8u * (34 + i); };
   auto land_bar = [&](int s) { return bar0 + 8u * (38 + s); };  // values that are cleaned before they are full
   // after the barriers (49 of them, 392 bytes)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 400);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 404);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 392);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 396);
+  int* s_total = reinterpret_cast<int*>(head + 400);                       // items for one kv head
+  int* s_largest = reinterpret_cast<int*>(head + 404);                     // blocks of the largest
   volatile int* poisoned = reinterpret_cast<volatile int*>(head + 416);    // [kPoisoned]
   Item* s_item = reinterpret_cast<Item*>(head + 448);                      // [kItems]
-  long long* s_part = reinterpret_cast<long long*>(head + 704);            // [kGroups + 1]
-  int* s_count = reinterpret_cast<int*>(head + 1224);                      // [kGroups + 1]
-  float* s_top = reinterpret_cast<float*>(head + 1488);                    // [2][128]
+  float* s_top = reinterpret_cast<float*>(head + 704);                     // [2][128]
+  Planned* s_plan = reinterpret_cast<Planned*>(head + 1728);               // [kPlan]
+  long long* s_part = reinterpret_cast<long long*>(head + 9920);           // [kPlan] first partial row
+  int* s_wsum = reinterpret_cast<int*>(head + 11968);                      // [warps] items, then sizes
+  long long* s_wpart = reinterpret_cast<long long*>(head + 12096);         // [warps]
   uint8_t* s_stage = smem + (2 + kStages) * Sz::tile;
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -444,10 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(qfull_bar(w), maps.use ? 1 : kLoaders);
       mbar_init(qempty_bar(w), 2);
       mbar_init(sfull_bar(w), 1);
-      mbar_init(pfull_bar(w, 0), 128);
-      mbar_init(pfull_bar(w, 1), 128);
+      mbar_init(pfull_bar(w, 0), 4);  // warps
+      mbar_init(pfull_bar(w, 1), 4);
       mbar_init(ofull_bar(w), 1);
-      mbar_init(oempty_bar(w), 256);
+      mbar_init(oempty_bar(w), 8);
     }
     mbar_init(drain_bar, 1);
     mbar_init(drain2_bar, 1);
@@ -471,37 +620,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   pdl_trigger();
   const int group = a.heads_q / a.heads_kv;
   const int tpt = kTile / group;  // tokens of a tile
-  const int per = (a.n + kGroups - 1) / kGroups;  // sequences of a run
-  if (tid < kGroups) {
-    int count = 0;
-    long long part = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, a.n); ++b) {
-      const Shape w = shape_of(a, seq_of(a, b), tpt);
-      count += w.pairs * w.cut.pieces;
-      part += w.part_rows;
-    }
-    s_count[tid] = count;
-    s_part[tid] = part;
+  // the plan, a thread to a sequence
+  int count = 0, size = 0;
+  long long part = 0;
+  for (int b = tid; b < a.n; b += kThreads) {
+    const Planned w = plan_of(a, b, tpt);
+    if (b < kPlan) s_plan[b] = w;
+    count += w.items;
+    size = max(size, w.items ? w.cut.blocks : 0);
+    part += part_rows_of(a, w);
+  }
+  long long p = part;  // inclusive sum of the warp's partial rows (for up to kPlan sequences)
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(~0u, p, o);
+    if (lane >= o) p += y;
+  }
+  count = __reduce_add_sync(~0u, count);
+  size = __reduce_max_sync(~0u, size);
+  if (lane == 31) {
+    s_wsum[warp] = count;
+    s_wsum[16 + warp] = size;
+    s_wpart[warp] = p;
   }
   __syncthreads();
-  if (warp == 0) {  // exclusive sums, two runs a lane
-    const int c0 = s_count[2 * lane], c1 = s_count[2 * lane + 1];
-    const long long p0 = s_part[2 * lane], p1 = s_part[2 * lane + 1];
-    int c = c0 + c1;
-    long long p = p0 + p1;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(~0u, c, o);
-      const long long y = __shfl_up_sync(~0u, p, o);
-      if (lane >= o) {
-        c += x;
-        p += y;
-      }
+  if (tid < kPlan) {
+    p -= part;
+    for (int x = 0; x < warp; ++x) p += s_wpart[x];
+    s_part[tid] = p;
+  }
+  if (tid == 0) {
+    int all = 0, most = 0;
+    for (int x = 0; x < kThreads / 32; ++x) {
+      all += s_wsum[x];
+      most = max(most, s_wsum[16 + x]);
     }
-    s_count[2 * lane] = c - c0 - c1;
-    s_count[2 * lane + 1] = c - c1;
-    s_part[2 * lane] = p - p0 - p1;
-    s_part[2 * lane + 1] = p - p1;
-    if (lane == 31) s_count[kGroups] = c;
+    *s_total = all;
+    *s_largest = most;
   }
   __syncthreads();
   tc_fence_after();
@@ -524,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp == 8 || warp == 9) {
     // ================================ loader ================================
     const int lw = warp - 8;
-    const int total = s_count[kGroups] * a.heads_kv;
-    int next = blockIdx.x;
+    const int largest = *s_largest;
+    int round = 0;  // of items: one for each CTA
     Place<kStages> ring = {0, 0};
     Place<2> qring = {0, 0};
     uint32_t landed = 0;  // parities of the land barriers, a bit each
@@ -536,47 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int i = handed % kItems;
       if (!wait_bar(iempty_bar(i), ((handed / kItems) & 1) ^ 1, ctl)) return false;
       ++handed;
-      Item x = {};
-      x.end = next >= total;
-      if (!x.end) {
-        const int kvh = next % a.heads_kv;
-        int u = next / a.heads_kv, g = 0;
-        for (int step = kGroups / 2; step; step >>= 1)
-          if (s_count[g + step] <= u) g += step;
-        u -= s_count[g];
-        long long part = s_part[g];
-        int b = g * per;
-        Seq s = seq_of(a, b);
-        Shape w = shape_of(a, s, tpt);
-        while (u >= w.pairs * w.cut.pieces && b + 1 < a.n) {
-          u -= w.pairs * w.cut.pieces;
-          part += w.part_rows;
-          s = seq_of(a, ++b);
-          w = shape_of(a, s, tpt);
-        }
-        const int pair = max(w.pairs - 1 - u / w.cut.pieces, 0);
-        x.piece = u % w.cut.pieces;
-        x.i0 = pair * 2 * tpt;
-        x.first = s.first + x.i0;
-        x.tokens = min(2 * tpt, s.nq - x.i0);
-        x.two = x.tokens > tpt;
-        x.nq = s.nq;
-        x.k0 = s.k0;
-        x.nk = s.nk;
-        x.kvh = kvh;
-        // the keys that any row of the pair sees end here
-        const int keys = a.mask ? s.nk : limit_of(a, s.nk, s.nq, x.i0 + x.tokens - 1);
-        x.b0 = x.piece * w.cut.blocks;
-        x.blocks = max(0, min((keys + kTile - 1) / kTile - x.b0, w.cut.blocks));
-        x.pieces = w.cut.pieces;
-        x.rows = s.nq * a.heads_q;
-        x.part = part + (long long)x.piece * x.rows;
-      }
+      const Item x = item_of(a, s_plan, s_part, *s_total, largest, round, tpt);
       if (lane == 0) {
         s_item[i] = x;
         mbar_arrive(ifull_bar(i));
       }
-      next += gridDim.x;
+      ++round;
       return true;
     };
     // Row of the packed keys or of the cache's planes that holds key `pos`, or
@@ -1026,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         ok = here;
         if (!ok) break;
         tc_fence_before();
-        mbar_arrive(pfull_bar(w, half));
+        warp_arrive(pfull_bar(w, half), lane);
       }
       if (!ok) break;
       // ------------------------------ epilogue ------------------------------
@@ -1077,68 +1196,78 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (!cut) inv = l != 0.0f ? 1.0f / l : (valid && sees_any(a, t_row, it.nk, it.nq, limit) ? NAN : 0.0f);
         const long long at = valid && !cut ? (long long)t_row * a.out.ts + (long long)h * a.out.hs : -1;
         float* part_o = a.part_o + part * a.head_dim + half * (DP / 2);
-        constexpr int kC = DP / 16;            // 16-byte chunks of a warp's half row
-        const uint32_t stage = (uint32_t)(warp * 32 * kC * 16);
-        if (live) {
+        const bool by_tma = maps.store > 0 && !cut && !bad && (quad + 1) * 32 <= (w ? rows1 : rows0);
+        // 16-byte chunk of a row of this warp's staging rows (64-byte swizzle)
+        auto at_stage = [&](int row, int chunk) {
+          return s_stage + warp * 2048 + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+        };
 #pragma unroll 1
-          for (int j = 0; j < DP / 2; j += 32) {
-            uint32_t o[32];
+        for (int j = 0; j < DP / 2; j += 32) {
+          uint32_t o[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
-            __syncwarp();
-            if (n > 0) {
-              tc_ld32(tO + j, o);
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+          __syncwarp();
+          if (n > 0 && live) {
+            tc_ld32(tO + j, o);
+            tc_wait_ld();
+            if (other) {
+              uint32_t o1[32];
+              tc_ld32(tO + 128 + j, o1);
               tc_wait_ld();
-              if (other) {
-                uint32_t o1[32];
-                tc_ld32(tO + 128 + j, o1);
-                tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
-              }
+              for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
             }
-            if (cut) {
-              if (keep) {
+          }
+          if (n > 0 && j + 32 >= DP / 2) {  // O has been read
+            tc_fence_before();
+            warp_arrive(oempty_bar(w), lane);
+            if (other) warp_arrive(oempty_bar(1), lane);
+          }
+          const int column = half * (DP / 2) + j;
+          if (cut) {
+            if (keep) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  if (half * (DP / 2) + j + e < a.head_dim)
-                    *reinterpret_cast<float4*>(part_o + j + e) =
-                        make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                    __uint_as_float(o[e + 3]));
-              }
+              for (int e = 0; e < 32; e += 4)
+                if (column + e < a.head_dim)
+                  *reinterpret_cast<float4*>(part_o + j + e) =
+                      make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                  __uint_as_float(o[e + 3]));
+            }
+          } else if (live) {
+            // through shared memory, so that whole lines are written
+            tma_store_read();  // the last store has left the staging rows
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 v;
+              v.x = pack2<kType>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+              v.y = pack2<kType>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+              v.z = pack2<kType>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+              v.w = pack2<kType>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+              *reinterpret_cast<uint4*>(at_stage(lane, e / 8)) = v;
+            }
+            if (by_tma) {
+              fence_proxy_async_shared();
+              __syncwarp();
+              if (elect_one())
+                tma_store(&maps.out, smem_u32(s_stage) + warp * 2048, column, it.kvh * group + (quad * 32) % group,
+                          it.first + (w ? tpt : 0) + quad * 32 / group);
             } else {
-              // to shared memory, so that the stores below write whole lines
+              __syncwarp();
+              const int chunk = lane & 3;
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint4 v;
-                v.x = pack2<kType>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                v.y = pack2<kType>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                v.z = pack2<kType>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                v.w = pack2<kType>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                const int chunk = (j + e) / 8;
-                *reinterpret_cast<uint4*>(s_stage + stage + (lane * kC + (chunk ^ (lane & (kC - 1)))) * 16) = v;
+              for (int y = 0; y < 4; ++y) {
+                const int row = y * 8 + lane / 4;
+                const long long to = __shfl_sync(~0u, at, row);
+                if (to >= 0 && column + chunk * 8 < a.head_dim)
+                  *reinterpret_cast<uint4*>(a.out.p + to + column + chunk * 8) =
+                      *reinterpret_cast<const uint4*>(at_stage(row, chunk));
               }
             }
           }
         }
-        if (n > 0) {  // O has been read
-          tc_fence_before();
-          mbar_arrive(oempty_bar(w));
-          if (other) mbar_arrive(oempty_bar(1));
-        }
-        if (live && !cut) {
-          __syncwarp();
-          const int chunk = lane % kC, column = half * (DP / 2) + chunk * 8;
-#pragma unroll
-          for (int y = 0; y < kC; ++y) {
-            const int row = y * (32 / kC) + lane / kC;
-            const long long to = __shfl_sync(~0u, at, row);
-            const uint4 v = *reinterpret_cast<const uint4*>(s_stage + stage + (row * kC + (chunk ^ (row & (kC - 1)))) * 16);
-            if (to >= 0 && column < a.head_dim) *reinterpret_cast<uint4*>(a.out.p + to + column) = v;
-          }
-          __syncwarp();
-        }
+        __syncwarp();
         if (bad && valid && (keep || !cut)) {
           // add the values that are not finite of the keys that this row sees (a
           // rare path: kept small, not fast)
@@ -1180,6 +1309,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         __syncwarp();
       }
     }
+    tma_store_done();
     // Every meeting of two warps begins with pair_any. If this one gave up
     // where the other one does not know (or the other way round), that one
     // will wait in its next meeting, or here: so they meet once more.
@@ -1253,10 +1383,10 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Boxes of 64 columns x box_heads x box_rows of [rows, heads, head_dim]. False
+// Boxes of 64 (or 32) columns x box_heads x box_rows of [rows, heads, head_dim]. False
 // where a tensor map cannot describe the tensor.
 bool make_map(CUtensorMap* map, const Heads& h, int dtype, int head_dim, int heads, long long rows, int box_heads,
-              int box_rows) {
+              int box_rows, int columns = 64) {
   const EncodeTiled encode = encode_tiled();
   if (!encode || !h.p || rows <= 0) return false;
   // a stride along one element says nothing
@@ -1265,10 +1395,10 @@ bool make_map(CUtensorMap* map, const Heads& h, int dtype, int head_dim, int hea
   if (hs == 0 || ts == 0 || hs >= (1ull << 40) || ts >= (1ull << 40)) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {hs, ts};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t box[3] = {(cuuint32_t)columns, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   const cuuint32_t steps[3] = {1, 1, 1};
   return encode(map, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, h.p,
-                dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1284,6 +1414,11 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s) {
   const int sms = num_sms();
   Maps maps = {};
   const int group = a.heads_q / a.heads_kv;
+  // a warp's 32 rows are whole tokens or a part of one token's heads
+  const int store = min(group, 32);
+  if (32 % store == 0 && group % store == 0 &&
+      make_map(&maps.out, a.out, kType, a.head_dim, a.heads_q, a.total_q, store, 32 / store, 32))
+    maps.store = store;
   const long long rows = a.paged ? (long long)a.n_pages * a.page_size : a.total_k;
   maps.box = a.paged ? min(a.page_size & -a.page_size, kTile) : kTile;  // rows of a page that lie together
   maps.use = maps.box >= 8 && make_map(&maps.q, a.q, kType, a.head_dim, a.heads_q, a.total_q, group, tpt) &&

@@ -63,12 +63,12 @@ constexpr int kSplitMinBlocks = 4;   // blocks of a piece at least
 struct Cut {
   int pieces, blocks;                // pieces of `blocks` blocks, the last one what is left
 };
-__host__ __device__ inline Cut cut_of(int blocks, long long tiles_and_heads) {
-  long long most = blocks / kSplitMinBlocks;
-  const long long want = (kSplitItems + tiles_and_heads - 1) / tiles_and_heads;
+__host__ __device__ inline Cut cut_of(int blocks, int tiles_and_heads) {
+  if (blocks < 2 * kSplitMinBlocks || tiles_and_heads >= kSplitItems) return {1, blocks};
+  int most = blocks / kSplitMinBlocks;
+  const int want = (kSplitItems + tiles_and_heads - 1) / tiles_and_heads;
   if (want < most) most = want;
-  if (most <= 1) return {1, blocks};
-  const int per = (int)((blocks + most - 1) / most);
+  const int per = (blocks + most - 1) / most;
   return {(blocks + per - 1) / per, per};
 }
 
