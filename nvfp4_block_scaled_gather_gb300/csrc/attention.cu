@@ -106,12 +106,23 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 // One box of a 3-d tensor (head dimension, heads, rows) to shared memory.
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                         uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+      "%3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
+}
+__device__ __forceinline__ uint64_t policy_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 // The same box back to global memory, and the waits of the lane that issued it:
 // until shared memory has been read, until all is written.
@@ -247,6 +258,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+// 1 / x to one ulp or so.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 template <int kType>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -618,8 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   pdl_wait();
   pdl_trigger();
-  const int group = a.heads_q / a.heads_kv;
-  const int tpt = kTile / group;  // tokens of a tile
+  const int group = a.group, tpt = a.tile_tokens;
   // the plan, a thread to a sequence
   int count = 0, size = 0;
   long long part = 0;
@@ -729,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (maps.use && lw == 0) {
       // ----------------------------- TMA loads -----------------------------
       const int boxes = kTile / maps.box;
+      const uint64_t normal = policy_normal(), once = policy_evict_first();
       const uint32_t box_bytes = (uint32_t)maps.box * 128u, q_bytes = (uint32_t)(tpt * group * 128);
       // per ring place: whether it was filled, by which barrier, in which parity
       uint32_t filled = 0, by_land = 0, parity = 0, qfilled = 0, qparity = 0;
@@ -738,6 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const int n = __shfl_sync(~0u, it.blocks, 0);
         if (n == 0) continue;
         const int lim = limit_of(a, it.nk, it.nq, it.i0);  // the least that any row of the pair sees
+        // keys that no other item reads leave L2 first (to partial results, for one)
+        const uint64_t policy = it.nq <= 2 * tpt ? once : normal;
         // lane i: row of box i of the block
         const int first = it.b0 * kTile + lane * maps.box;
         int row = lane < boxes ? row_of(first) : -1;
@@ -748,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
             for (int h = 0; h < DP / 64; ++h)
               tma_load(sQ + qring.slot * Sz::tile + h * kTile * 128, &maps.q, h * 64, it.kvh * group,
-                       it.first + q * tpt, qfull_bar(qring.slot));
+                       it.first + q * tpt, qfull_bar(qring.slot), normal);
           }
           __syncwarp();
           if (ok) {
@@ -782,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               if (elect_one()) {
 #pragma unroll
                 for (int h = 0; h < DP / 64; ++h)
-                  tma_load(dst + h * kTile * 128 + i * box_bytes, map, h * 64, it.kvh, z, bar);
+                  tma_load(dst + h * kTile * 128 + i * box_bytes, map, h * 64, it.kvh, z, bar, policy);
               }
             }
             __syncwarp();
@@ -1149,165 +1168,183 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       if (!ok) break;
       // ------------------------------ epilogue ------------------------------
+      // Of two tiles a warpgroup takes one each, of one tile half of the columns.
       const bool other = !two && n > 1;  // one tile: the second O holds the other half of its blocks
       const bool cut = it.pieces > 1;
-      const int h = it.kvh * group + head_in;
-      const float top = other ? fmaxf(m0, m1) : m0;
-      const float f0 = other && m0 != -INFINITY ? ex2((m0 - top) * c) : 1.0f;
-      const float f1 = m1 != -INFINITY ? ex2((m1 - top) * c) : 1.0f;
+      const int w = two ? half : 0, c0 = two ? 0 : half * (DP / 2), columns = two ? DP : DP / 2;
+      const int rows = w ? rows1 : rows0;
+      const bool live = quad * 32 < rows, valid = r < rows;
+      float m = w ? m1 : m0, l = 0.0f, f0 = 1.0f, f1 = 1.0f;
       if (other) {
+        m = fmaxf(m0, m1);
+        f0 = m0 != -INFINITY ? ex2((m0 - m) * c) : 1.0f;
+        f1 = m1 != -INFINITY ? ex2((m1 - m) * c) : 1.0f;
         l0 = l0 * f0 + l1 * f1;
-        m0 = top;
       }
       if (n > 0 && quad * 32 < rows0) {  // the row's sum is that of its two threads
-#pragma unroll 1
-        for (int w = 0; w <= two && !agreed; ++w) {
-          agreed = pair_any(1 + quad, false);  // (the last exchange has been read) the other one gives up
-          s_top[half * 128 + r] = w ? l1 : l0;
-          pair_sync(1 + quad);
-          const float theirs = s_top[(half ^ 1) * 128 + r];
-          if (w) l1 += theirs;
-          else l0 += theirs;
-        }
+        agreed = pair_any(1 + quad, false);  // (the last exchange has been read) the other one gives up
+        s_top[half * 128 + r] = two && half == 0 ? l1 : l0;
+        pair_sync(1 + quad);
+        l = (w ? l1 : l0) + s_top[(half ^ 1) * 128 + r];
       }
       ok = !agreed;
-#pragma unroll 1
-      for (int w = 0; w <= two && ok; ++w) {
-        const int tok = (w ? tpt : 0) + token;
-        const bool live = quad * 32 < (w ? rows1 : rows0), valid = r < (w ? rows1 : rows0);
-        const float m = w ? m1 : m0, l = w ? l1 : l0;
-        const uint32_t tO = lanes + kColO + w * 128 + half * (DP / 2);
-        if (n > 0) {
-          ok = wait_bar(ofull_bar(w), (uses >> w) & 1, ctl);
-          if (ok && other) ok = wait_bar(ofull_bar(1), (uses >> 1) & 1, ctl);
-          if (!ok) break;
-          uses ^= other ? 3u : 1u << w;
-          __syncwarp();
-          tc_fence_after();
+      if (!ok) break;
+      if (n > 0) {
+        // every warp sees every round of both O, its own or not
+        if (two && half) {
+          ok = wait_bar(ofull_bar(0), uses & 1, ctl);
+          warp_arrive(oempty_bar(0), lane);
         }
-        // (O is complete, so every block's values have been through the cleaning)
-        const bool bad = n > 0 && poisoned[(seq_no - 1) % kPoisoned] == seq_no;
-        const int i = it.i0 + tok, t_row = it.first + tok;
-        const int limit = valid ? limit_of(a, it.nk, it.nq, i) : 0;
-        const long long part = it.part + (long long)i * a.heads_q + h;
-        const bool keep = cut && valid && part < a.part_rows;
-        // a row that sees no key gives 0; one whose scores are all -inf has no value
-        float inv = 1.0f;
-        if (!cut) inv = l != 0.0f ? 1.0f / l : (valid && sees_any(a, t_row, it.nk, it.nq, limit) ? NAN : 0.0f);
-        const long long at = valid && !cut ? (long long)t_row * a.out.ts + (long long)h * a.out.hs : -1;
-        float* part_o = a.part_o + part * a.head_dim + half * (DP / 2);
-        const bool by_tma = maps.store > 0 && !cut && !bad && (quad + 1) * 32 <= (w ? rows1 : rows0);
-        // 16-byte chunk of a row of this warp's staging rows (64-byte swizzle)
-        auto at_stage = [&](int row, int chunk) {
-          return s_stage + warp * 2048 + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-        };
+        ok = ok && wait_bar(ofull_bar(w), (uses >> w) & 1, ctl);
+        if (other) ok = ok && wait_bar(ofull_bar(1), (uses >> 1) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // (O is complete, so every block's values have been through the cleaning)
+      const bool bad = n > 0 && poisoned[(seq_no - 1) % kPoisoned] == seq_no;
+      const int h = it.kvh * group + head_in;
+      const int i = it.i0 + w * tpt + token, t_row = it.first + w * tpt + token;
+      // rows of a cut sequence are kept a kv head after the other; eight of a
+      // tile's together as [head_dim / 4][8][4], so that stores and the
+      // join's reads are whole lines and what the join reads is in one place
+      const int row0 = it.kvh * it.nq * group + (it.i0 + w * tpt) * group;
+      const long long part = it.part + row0;
+      const bool keep = cut && valid && part + rows <= a.part_rows;
+      const int eight = min(8, rows - (r & ~7));  // rows of this row's eight
+      float* part_o = a.part_o + part * a.head_dim + (r & ~7) * a.head_dim + (r & 7) * 4;
+      // a row that sees no key gives 0; one whose scores are all -inf has no value
+      float inv = 1.0f;
+      if (!cut) {
+        inv = rcp_approx(l);
+        if (l == 0.0f) inv = valid && sees_any(a, t_row, it.nk, it.nq, limit_of(a, it.nk, it.nq, i)) ? NAN : 0.0f;
+      }
+      f0 *= inv;
+      f1 *= inv;
+      const long long at = valid && !cut ? (long long)t_row * a.out.ts + (long long)h * a.out.hs : -1;
+      const bool by_tma = maps.store > 0 && !cut && !bad && (quad + 1) * 32 <= rows;
+      // 16-byte chunk of a row of this warp's staging rows (64-byte swizzle)
+      auto at_stage = [&](int row, int chunk) {
+        return s_stage + warp * 2048 + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+      };
+      const uint32_t tO = lanes + kColO + w * 128 + c0;
 #pragma unroll 1
-        for (int j = 0; j < DP / 2; j += 32) {
-          uint32_t o[32];
+      for (int j = 0; j < columns; j += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        if (n > 0 && live) {
+          tc_ld32(tO + j, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+          if (other) {
+            uint32_t o1[32];
+            tc_ld32(tO + 128 + j, o1);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
+          }
+        } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (n > 0 && j + 32 >= columns) {  // O has been read
+          tc_fence_before();
+          warp_arrive(oempty_bar(w), lane);
+          if (other) warp_arrive(oempty_bar(1), lane);
+        }
+        const int column = c0 + j;
+        if (cut) {
+          if (keep) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (column + e < a.head_dim)
+                *reinterpret_cast<float4*>(part_o + (column + e) * eight) =
+                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                __uint_as_float(o[e + 3]));
+          }
+        } else if (live) {
+          // through shared memory, so that whole lines are written
+          tma_store_read();  // the last store has left the staging rows
           __syncwarp();
-          if (n > 0 && live) {
-            tc_ld32(tO + j, o);
-            tc_wait_ld();
-            if (other) {
-              uint32_t o1[32];
-              tc_ld32(tO + 128 + j, o1);
-              tc_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
-            }
+          for (int e = 0; e < 32; e += 8) {
+            uint4 v;
+            v.x = pack2<kType>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+            v.y = pack2<kType>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            v.z = pack2<kType>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+            v.w = pack2<kType>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+            *reinterpret_cast<uint4*>(at_stage(lane, e / 8)) = v;
           }
-          if (n > 0 && j + 32 >= DP / 2) {  // O has been read
-            tc_fence_before();
-            warp_arrive(oempty_bar(w), lane);
-            if (other) warp_arrive(oempty_bar(1), lane);
-          }
-          const int column = half * (DP / 2) + j;
-          if (cut) {
-            if (keep) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                if (column + e < a.head_dim)
-                  *reinterpret_cast<float4*>(part_o + j + e) =
-                      make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                  __uint_as_float(o[e + 3]));
-            }
-          } else if (live) {
-            // through shared memory, so that whole lines are written
-            tma_store_read();  // the last store has left the staging rows
+          if (by_tma) {
+            fence_proxy_async_shared();
             __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 v;
-              v.x = pack2<kType>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-              v.y = pack2<kType>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-              v.z = pack2<kType>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-              v.w = pack2<kType>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-              *reinterpret_cast<uint4*>(at_stage(lane, e / 8)) = v;
-            }
-            if (by_tma) {
-              fence_proxy_async_shared();
-              __syncwarp();
-              if (elect_one())
-                tma_store(&maps.out, smem_u32(s_stage) + warp * 2048, column, it.kvh * group + (quad * 32) % group,
-                          it.first + (w ? tpt : 0) + quad * 32 / group);
-            } else {
-              __syncwarp();
-              const int chunk = lane & 3;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int row = y * 8 + lane / 4;
-                const long long to = __shfl_sync(~0u, at, row);
-                if (to >= 0 && column + chunk * 8 < a.head_dim)
-                  *reinterpret_cast<uint4*>(a.out.p + to + column + chunk * 8) =
-                      *reinterpret_cast<const uint4*>(at_stage(row, chunk));
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (bad && valid && (keep || !cut)) {
-          // add the values that are not finite of the keys that this row sees (a
-          // rare path: kept small, not fast)
-          const int from = max(it.b0, limit_of(a, it.nk, it.nq, it.i0) / kTile) * kTile;
-          uint16_t* out = a.out.p + at + half * (DP / 2);
-#pragma unroll 1
-          for (int d = 0; d < min(DP / 2, a.head_dim - half * (DP / 2)); ++d) {
-            float sum = 0.0f;
-#pragma unroll 1
-            for (int pos = from; pos < min((it.b0 + n) * kTile, it.nk); ++pos) {
-              if (!((seen_bits(a, t_row, it.nk, it.nq, limit, pos & ~31) >> (pos & 31)) & 1u)) continue;
-              long long row = (long long)it.k0 + pos;
-              if (a.paged) {
-                const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + pos / a.page_size);
-                if (p < 0 || p >= a.n_pages) continue;
-                row = (long long)p * a.page_size + pos % a.page_size;
-              }
-              const float x = to_f32<kType>(a.v.p[row * a.v.ts + (long long)it.kvh * a.v.hs + half * (DP / 2) + d]);
-              if (!isfinite(x)) sum += x;
-            }
-            if (sum != 0.0f) {  // not finite, or nothing
-              if (cut) part_o[d] += sum;
-              else out[d] = (uint16_t)pack2<kType>(to_f32<kType>(out[d]) + sum, 0.0f);
-            }
-          }
-        }
-        if (valid && half == 0) {
-          const long long row = (long long)t_row * a.heads_q + h;
-          if (cut) {
-            if (keep) a.part_ml[part] = make_float2(m * c, l);
-            else report(a.status, MOE_ERR_INVALID);
-            if (it.piece == 0)
-              a.part_of[row] = make_int4(keep ? (int)part : -1, it.pieces, it.rows, sees_any(a, t_row, it.nk, it.nq, limit));
+            if (elect_one())
+              tma_store(&maps.out, smem_u32(s_stage) + warp * 2048, column, it.kvh * group + (quad * 32) % group,
+                        it.first + w * tpt + quad * 32 / group);
           } else {
-            if (a.part_of) a.part_of[row] = make_int4(-1, 0, 0, 0);
-            if (a.lse) a.lse[row] = l != 0.0f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            __syncwarp();
+            const int chunk = lane & 3;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int row = y * 8 + lane / 4;
+              const long long to = __shfl_sync(~0u, at, row);
+              if (to >= 0 && column + chunk * 8 < a.head_dim)
+                *reinterpret_cast<uint4*>(a.out.p + to + column + chunk * 8) =
+                    *reinterpret_cast<const uint4*>(at_stage(row, chunk));
+            }
           }
         }
-        __syncwarp();
       }
+      __syncwarp();
+      if (n > 0) {
+        if (two && !half) {
+          ok = wait_bar(ofull_bar(1), (uses >> 1) & 1, ctl);
+          warp_arrive(oempty_bar(1), lane);
+        }
+        uses ^= two || other ? 3u : 1u;
+      }
+      if (bad && valid && (keep || !cut)) {
+        // add the values that are not finite of the keys that this row sees (a
+        // rare path: kept small, not fast)
+        const int from = max(it.b0, limit_of(a, it.nk, it.nq, it.i0) / kTile) * kTile;
+#pragma unroll 1
+        for (int d = c0; d < min(c0 + columns, a.head_dim); ++d) {
+          float sum = 0.0f;
+#pragma unroll 1
+          for (int pos = from; pos < min((it.b0 + n) * kTile, it.nk); ++pos) {
+            if (!((seen_bits(a, t_row, it.nk, it.nq, limit_of(a, it.nk, it.nq, i), pos & ~31) >> (pos & 31)) & 1u)) continue;
+            long long row = (long long)it.k0 + pos;
+            if (a.paged) {
+              const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + pos / a.page_size);
+              if (p < 0 || p >= a.n_pages) continue;
+              row = (long long)p * a.page_size + pos % a.page_size;
+            }
+            const float x = to_f32<kType>(a.v.p[row * a.v.ts + (long long)it.kvh * a.v.hs + d]);
+            if (!isfinite(x)) sum += x;
+          }
+          if (sum != 0.0f) {  // not finite, or nothing
+            if (cut) part_o[(d & ~3) * eight + (d & 3)] += sum;
+            else a.out.p[at + d] = (uint16_t)pack2<kType>(to_f32<kType>(a.out.p[at + d]) + sum, 0.0f);
+          }
+        }
+      }
+      if (valid && (two || half == 0)) {
+        const int row = t_row * a.heads_q + h;
+        if (cut) {
+          if (keep) a.part_ml[part + r] = make_float2(m * c, l);
+          else report(a.status, MOE_ERR_INVALID);
+          if (it.piece == 0) {
+            const bool any = sees_any(a, t_row, it.nk, it.nq, limit_of(a, it.nk, it.nq, i));
+            a.part_of[(long long)(it.first - it.i0) * a.heads_q + row0 + r] =
+                make_int4(keep ? (int)part : -1, rows | r << 8 | (any ? 1 << 16 : 0) | it.pieces << 17, it.rows, row);
+          }
+        } else {
+          if (a.part_of) a.part_of[(long long)(it.first - it.i0) * a.heads_q + row0 + r] = make_int4(-1, 0, 0, 0);
+          if (a.lse) a.lse[row] = l != 0.0f ? (m * c + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      __syncwarp();
     }
     tma_store_done();
     // Every meeting of two warps begins with pair_any. If this one gave up
@@ -1327,44 +1364,61 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
 }
 
-// Joins the pieces of cut sequences, in their order: one warp per query and head.
+// Joins the pieces of cut sequences, in their order, with a running maximum: a
+// CTA has eight rows of a tile (whose quads of columns lie together, 128
+// bytes), a thread one quad of one row, four pieces' values in flight. Bound by
+// the latency of its reads where the pieces are few and small, so nothing is
+// read before the values that could be read with them.
+constexpr int kJoinThreads = 256;
 template <int kType>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 5) join_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)a.total_q * a.heads_q;
-  for (long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 4LL) {
-    const int t = (int)(row / a.heads_q), h = (int)(row - (long long)t * a.heads_q);
-    if (t < ld_cg(a.cu_q) || t >= ld_cg(a.cu_q + a.n)) continue;
-    const int4 of = ld_cg(a.part_of + row);
-    if (of.x < 0 || of.y <= 1 || of.z <= 0 || of.x + (long long)(of.y - 1) * of.z >= a.part_rows) continue;
-    float top = -INFINITY;
-    for (int i = lane; i < of.y; i += 32) top = fmaxf(top, a.part_ml[of.x + (long long)i * of.z].x);
+  const int row = threadIdx.x & 7, q = threadIdx.x >> 3;
+  const long long rows = (long long)a.total_q * a.heads_q, g = (long long)blockIdx.x * 8 + row;
+  if (g >= rows) return;
+  const int cu_first = ld_cg(a.cu_q), cu_end = ld_cg(a.cu_q + a.n);
+  const int4 of = ld_cg(a.part_of + g);
+  const int n = of.y & 0xFF, r = (of.y >> 8) & 0xFF, pieces = of.y >> 17;
+  // (rows of no sequence hold anything)
+  if (g < (long long)cu_first * a.heads_q || g >= (long long)cu_end * a.heads_q || of.x < 0 || pieces <= 1 || r >= n ||
+      of.z <= 0 || of.w < 0 || of.w >= rows || of.x + (long long)(pieces - 1) * of.z + n > a.part_rows ||
+      q * 4 >= a.head_dim)
+    return;
+  const int eight = min(8, n - (r & ~7));
+  const float* from = a.part_o + ((long long)of.x + (r & ~7)) * a.head_dim + (r & 7) * 4 + q * 4 * eight;
+  const float2* ml = a.part_ml + of.x + r;
+  float top = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+  for (int i0 = 0; i0 < pieces; i0 += 4) {
+    float4 v[4];
+    uint2 x[4];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-    float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int e = lane * 4;
-    for (int i = 0; i < of.y; ++i) {
-      const long long at = of.x + (long long)i * of.z;
-      const float2 ml = a.part_ml[at];
-      if (ml.y == 0.0f) continue;  // saw nothing
-      const float f = ml.x == -INFINITY ? 1.0f : ex2(ml.x - top);
-      l += f * ml.y;
-      if (e < a.head_dim) {
-        const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * a.head_dim + e);
-        o[0] += f * v.x;
-        o[1] += f * v.y;
-        o[2] += f * v.z;
-        o[3] += f * v.w;
+    for (int u = 0; u < 4; ++u) {  // past the last piece: the last one again, not used
+      const long long at = (long long)min(i0 + u, pieces - 1) * of.z;
+      x[u] = ld_cg(reinterpret_cast<const uint2*>(ml + at));
+      v[u] = ld_cg(reinterpret_cast<const float4*>(from + at * a.head_dim));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float m = __uint_as_float(x[u].x), sum = __uint_as_float(x[u].y);
+      if (i0 + u < pieces && sum != 0.0f) {  // a sum of 0: the piece saw nothing
+        const float now = fmaxf(top, m);
+        const float keep = now == top ? 1.0f : ex2(top - now), f = now == m || m == -INFINITY ? 1.0f : ex2(m - now);
+        l = l * keep + sum * f;
+        o[0] = o[0] * keep + v[u].x * f;
+        o[1] = o[1] * keep + v[u].y * f;
+        o[2] = o[2] * keep + v[u].z * f;
+        o[3] = o[3] * keep + v[u].w * f;
+        top = now;
       }
     }
-    const float inv = l != 0.0f ? 1.0f / l : (of.w ? NAN : 0.0f);
-    if (e < a.head_dim)
-      *reinterpret_cast<uint2*>(a.out.p + (long long)t * a.out.ts + (long long)h * a.out.hs + e) =
-          make_uint2(pack2<kType>(o[0] * inv, o[1] * inv), pack2<kType>(o[2] * inv, o[3] * inv));
-    if (a.lse && lane == 0) a.lse[row] = l != 0.0f ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
+  const float inv = l != 0.0f ? rcp_approx(l) : ((of.y >> 16) & 1 ? NAN : 0.0f);
+  const int t = of.w / a.heads_q, h = of.w - t * a.heads_q;
+  *reinterpret_cast<uint2*>(a.out.p + (long long)t * a.out.ts + (long long)h * a.out.hs + q * 4) =
+      make_uint2(pack2<kType>(o[0] * inv, o[1] * inv), pack2<kType>(o[2] * inv, o[3] * inv));
+  if (a.lse && q == 0) a.lse[of.w] = l != 0.0f ? (top + __log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1427,8 +1481,8 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s) {
   err = launch_pdl(attention_kernel<kType, DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads),
                    Sizes<DP>::smem, s, a, maps);
   if (err != cudaSuccess || !a.part_o) return err;
-  const long long blocks = ((long long)a.total_q * a.heads_q + 3) / 4, most = sms * 16LL;
-  return launch_pdl(join_kernel<kType>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(128), 0, s, a);
+  const long long blocks = ((long long)a.total_q * a.heads_q + 7) / 8;
+  return launch_pdl(join_kernel<kType>, dim3((unsigned)blocks), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace
@@ -1455,7 +1509,10 @@ AttnWs attention_ws(int n, int total_q, int heads_q, int heads_kv, int head_dim,
   return w;
 }
 
-cudaError_t launch_attention(const AttnArgs& a, int dtype, cudaStream_t s) {
+cudaError_t launch_attention(const AttnArgs& args, int dtype, cudaStream_t s) {
+  AttnArgs a = args;
+  a.group = a.heads_q / a.heads_kv;
+  a.tile_tokens = kTile / a.group;
   if (dtype == MOE_BF16) return a.head_dim <= 64 ? launch_typed<MOE_BF16, 64>(a, s) : launch_typed<MOE_BF16, 128>(a, s);
   return a.head_dim <= 64 ? launch_typed<MOE_FP16, 64>(a, s) : launch_typed<MOE_FP16, 128>(a, s);
 }

@@ -90,10 +90,13 @@ struct AttnArgs {
   const int* mask;          // tree bits, or null (chain)
   int mask_words;
   int* status;
+  int group, tile_tokens;   // filled in by the launch: query heads of a kv head, tokens of a tile of 128 rows
   // partial results of cut sequences (null: no sequence of the call is cut)
   float* part_o;            // [part_rows, head_dim], not divided by the sum
   float2* part_ml;          // [part_rows] maximum (in powers of two) and sum
-  int4* part_of;            // [total_q * heads_q] first row, pieces, rows between pieces, whether it sees any key
+  // [total_q * heads_q], a sequence's rows a kv head after the other: first partial row of the row's tile (or -1), the tile's
+  // rows | the row in it << 8 | whether it sees any key << 16 | pieces << 17, rows between pieces, token * heads_q + head
+  int4* part_of;
   long long part_rows;
 };
 // The partial rows that any call with these bounds can need, and their bytes.

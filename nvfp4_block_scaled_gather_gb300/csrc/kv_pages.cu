@@ -488,43 +488,68 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(Kv kv, const int* se
   }
 }
 
-// One thread per drafted token, up its line of parents.
-__global__ void __launch_bounds__(128) tree_mask_kernel(const int* parents, const int* cu, int n, int total, int* mask,
-                                                        int words, int* status) {
+// One CTA per sequence. A token's bits are its own and its parent's: all
+// tokens at once take over the bits of the token that they point to and then
+// point where that one points, so the line walked doubles each round (a walk
+// up the parents one by one waits for a read each time: 12 us for trees of 64).
+constexpr int kTreeThreads = 256;
+constexpr int kTreeMost = 256, kTreeWords = kTreeMost / 32;  // larger trees are walked
+__global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const int* parents, const int* cu, int n, int total,
+                                                                 int* mask, int words, int* status) {
+  __shared__ uint32_t s_bits[2][kTreeMost * kTreeWords];
+  __shared__ int s_up[2][kTreeMost];
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x * 128 + threadIdx.x;
-  if (t >= total || t < ld_cg(cu) || t >= ld_cg(cu + n)) return;
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ld_cg(cu + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  const int first = ld_cg(cu + lo), end = min(ld_cg(cu + lo + 1), total);
-  int* row = mask + (long long)t * words;
-  for (int w = 0; w < words; ++w) row[w] = 0;
-  if (first < 0 || t >= end || end - first > 32LL * words) {
-    report(status, MOE_ERR_INVALID);
+  const int tid = threadIdx.x;
+  const int first = ld_cg(cu + blockIdx.x), end = min(ld_cg(cu + blockIdx.x + 1), total), m = end - first;
+  if (first < 0 || m <= 0) {
+    if (first < 0 && tid == 0) report(status, MOE_ERR_INVALID);
     return;
   }
-  int j = t - first, word = j >> 5;
-  uint32_t bits = 0;
-  while (true) {  // parents come before their children, so the walk ends
-    if ((j >> 5) != word) {
-      row[word] = (int)bits;
-      word = j >> 5;
-      bits = 0;
-    }
-    bits |= 1u << (j & 31);
-    const int up = ld_cg(parents + first + j);
-    if (up < 0 || up >= j) {
-      if (up != -1) report(status, MOE_ERR_INVALID);
-      break;
-    }
-    j = up;
+  const int* from = parents + first;
+  int* rows = mask + (long long)first * words;
+  if (m > 32LL * words) {
+    if (tid == 0) report(status, MOE_ERR_INVALID);
+    for (long long x = tid; x < (long long)m * words; x += kTreeThreads) rows[x] = 0;
+    return;
   }
-  row[word] = (int)bits;
+  auto up_of = [&](int j) {  // an earlier token, or -1
+    const int up = ld_cg(from + j);
+    if (up >= -1 && up < j) return up;
+    report(status, MOE_ERR_INVALID);
+    return -1;
+  };
+  if (m <= kTreeMost) {
+    const int used = (m + 31) / 32;
+    if (tid < m) s_up[0][tid] = up_of(tid);
+    for (int x = tid; x < m * used; x += kTreeThreads) {
+      const int i = x / used, w = x - i * used;
+      s_bits[0][x] = w == (i >> 5) ? 1u << (i & 31) : 0u;
+    }
+    __syncthreads();
+    int now = 0;
+    for (int reach = 1; reach < m; reach *= 2, now ^= 1) {
+      for (int x = tid; x < m * used; x += kTreeThreads) {
+        const int i = x / used, up = s_up[now][i];
+        s_bits[now ^ 1][x] = s_bits[now][x] | (up >= 0 ? s_bits[now][x + (up - i) * used] : 0u);
+      }
+      if (tid < m) {
+        const int up = s_up[now][tid];
+        s_up[now ^ 1][tid] = up >= 0 ? s_up[now][up] : -1;
+      }
+      __syncthreads();
+    }
+    for (int x = tid; x < m * words; x += kTreeThreads) {
+      const int i = x / words, w = x - i * words;
+      rows[x] = w < used ? (int)s_bits[now][i * used + w] : 0;
+    }
+    return;
+  }
+  for (int i = tid; i < m; i += kTreeThreads) {
+    int* row = rows + (long long)i * words;
+    for (int w = 0; w < words; ++w) row[w] = 0;
+    for (int j = i; j >= 0; j = up_of(j)) row[j >> 5] |= (int)(1u << (j & 31));
+  }
 }
 
 int copy_grid(const Kv& kv, long long entries) {
@@ -611,7 +636,7 @@ cudaError_t launch_kv_compact(const moe_kv_cache_t& c, const KvWs& ws, cudaStrea
 
 cudaError_t launch_tree_mask(const int* parents, const int* cu, int n, int total, int* mask, int words, int* status,
                              cudaStream_t s) {
-  return launch_pdl(tree_mask_kernel, dim3((total + 127) / 128), dim3(128), 0, s, parents, cu, n, total, mask, words,
+  return launch_pdl(tree_mask_kernel, dim3(n), dim3(kTreeThreads), 0, s, parents, cu, n, total, mask, words,
                     status);
 }
 

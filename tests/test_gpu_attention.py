@@ -448,3 +448,31 @@ def test_binding_refusals(cuda):
     with pytest.raises(RuntimeError, match="unsupported shape"):
         A.moe_attention_cached(normal((3, 5, 64), "bf16", 73), cache, 0, seqs, cu, torch.empty((3, 5, 64), dtype=torch.bfloat16,
                                                                                               device="cuda"), ws)
+
+
+@pytest.mark.parametrize("sizes,words", [([1, 2, 33, 0, 64, 31], 2), ([256, 255], 8), ([300, 5], 11), ([7], 3)])
+def test_tree_masks(cuda, sizes, words):
+    """Ancestors' bits in every word of the rows, for trees that fit one CTA's table and one that does not; a chain
+    (the longest walk) among them."""
+    rng = np.random.RandomState(len(sizes))
+    parents = [[j - 1 for j in range(n)] if i == 0 else [int(rng.randint(-1, j)) if j else -1 for j in range(n)]
+               for i, n in enumerate(sizes)]
+    mask = torch.full((sum(sizes), words), 77, dtype=torch.int32, device="cuda")
+    A.moe_tree_mask(ints(sum(parents, [])), starts(sizes), mask)
+    got, at = mask.cpu().numpy().view(np.uint32), 0
+    for p in parents:
+        bits = OA.ancestors(p)
+        for i in range(len(p)):
+            row = [(got[at + i, j >> 5] >> (j & 31)) & 1 for j in range(32 * words)]
+            assert row[:len(p)] == bits[i].astype(int).tolist() and not any(row[len(p):]), (len(p), i)
+        at += len(p)
+    assert N.check_status() == 0
+
+
+def test_tree_mask_bad_parents_and_words(cuda):
+    mask = torch.full((5, 1), 77, dtype=torch.int32, device="cuda")
+    A.moe_tree_mask(ints([-1, 0, 2, -5, 1]), ints([0, 5]), mask)
+    assert mask[:, 0].tolist() == [1, 3, 4, 8, 19] and N.check_status() == 1
+    mask = torch.full((40, 1), 77, dtype=torch.int32, device="cuda")
+    A.moe_tree_mask(ints(list(range(-1, 33)) + [-1] * 6), ints([0, 34, 40]), mask)
+    assert mask[:, 0].tolist() == [0] * 34 + [1 << j for j in range(6)] and N.check_status() == 1
