@@ -600,29 +600,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   uint8_t* s_stage = smem + (2 + kStages) * Sz::tile;
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-  if (tid == 0) {
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(full_bar(s), maps.use ? 1 : kLoaders);
-      mbar_init(empty_bar(s), 2);  // both MMA warps
-      mbar_init(land_bar(s), 1);
-    }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(qfull_bar(w), maps.use ? 1 : kLoaders);
-      mbar_init(qempty_bar(w), 2);
-      mbar_init(sfull_bar(w), 1);
-      mbar_init(pfull_bar(w, 0), 4);  // warps
-      mbar_init(pfull_bar(w, 1), 4);
-      mbar_init(ofull_bar(w), 1);
-      mbar_init(oempty_bar(w), 8);
-    }
-    mbar_init(drain_bar, 1);
-    mbar_init(drain2_bar, 1);
-    for (int i = 0; i < kItems; ++i) {
-      mbar_init(ifull_bar(i), 1);
-      mbar_init(iempty_bar(i), kItemReaders);
-    }
-    for (int i = 0; i < kPoisoned; ++i) poisoned[i] = 0;
-    *abort_flag = 0;
+  if (warp == 0) {  // a barrier or two to a lane
+    auto arrivals = [&](int i) -> int {
+      if (i < 8) return maps.use ? 1 : kLoaders;         // full
+      if (i < 16) return 2;                              // empty: both MMA warps
+      if (i < 18) return maps.use ? 1 : kLoaders;        // query tiles full
+      if (i < 20) return 2;                              // query tiles empty
+      if (i < 22) return 1;                              // scores full
+      if (i < 24 || i == 47 || i == 48) return 4;        // weights full: warps
+      if (i < 26) return 1;                              // O full
+      if (i < 28) return 8;                              // O empty: warps
+      if (i >= 30 && i < 34) return 1;                   // items full
+      if (i >= 34 && i < 38) return kItemReaders;        // items empty
+      return 1;                                          // landed values, drains
+    };
+    for (int i = lane; i < 49; i += 32) mbar_init(bar0 + 8u * i, arrivals(i));
+    if (lane < kPoisoned) poisoned[lane] = 0;
+    if (lane == 0) *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -846,7 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           landed ^= 1u << v.slot;
           const uint32_t tile = sKV + v.slot * Sz::tile;
           const int rows = min(kTile, it.nk - (end - kTile));  // rows of this sequence
-          for (int i = rows * kChunks + lane; i < kTile * kChunks; i += 32)
+          // (the MMAs read whole steps of 16 rows)
+          for (int i = rows * kChunks + lane; i < ((rows + 15) & ~15) * kChunks; i += 32)
             *at_smem(chunk_at(tile, i / kChunks, i % kChunks)) = make_uint4(0u, 0u, 0u, 0u);
           if (edge) {
             // carries out of the exponent tell whether anything is to be cleared
@@ -965,6 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
     while (ok && next_item()) {
       const int n = __shfl_sync(~0u, it.blocks, 0), two = __shfl_sync(~0u, it.two, 0);
+      const int nk = __shfl_sync(~0u, it.nk, 0), b0 = __shfl_sync(~0u, it.b0, 0);
       if (n == 0) continue;
       const int last = two ? n - 1 : n - 1 - ((n - 1 - w) & 1);  // this warpgroup's last block; below w: none
       Place<2> q = qring;
@@ -985,6 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           if (!ok || !wait_bar(full_bar(vat.slot), vat.parity, ctl)) { ok = false; break; }
           fence_proxy_async_shared();
           const uint64_t vd = vd0 + (uint64_t)(vat.slot * (Sz::tile >> 4));
+          // 16 keys a step; steps past the sequence's end are left out
+          const int ksteps = min((nk - (b0 + pending) * kTile + 15) / 16, kTile / 16);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if (ok) ok = wait_bar(pfull_bar(w, half), steps, ctl);
@@ -993,7 +991,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             if (elect_one()) {
 #pragma unroll
               for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
-                tc_mma_ts(tO, tS + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o, !first || k != 0);
+                if (k < ksteps)
+                  tc_mma_ts(tO, tS + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o, !first || k != 0);
               if (half) {
                 tc_commit(empty_bar(vat.slot));
                 if (pending == last) tc_commit(ofull_bar(w));
@@ -1064,6 +1063,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int n = it.blocks, two = it.two;
       const int steps = two ? 2 * n : n;
       const int rows0 = min(tpt, it.tokens) * group, rows1 = two ? (it.tokens - tpt) * group : rows0;
+      // the least that any row of a tile sees
+      const int lim0 = limit_of(a, it.nk, it.nq, it.i0), lim1 = two ? limit_of(a, it.nk, it.nq, it.i0 + tpt) : lim0;
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // of the two S; m in units of the raw scores
       for (int t = 0; t < steps; ++t) {
         const int w = t & 1;
@@ -1072,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const bool live = quad * 32 < rows;             // any row of this warp's
         const int pos = (it.b0 + (two ? t >> 1 : t)) * kTile;
         // some row of the tile does not see all of the block
-        const bool edge = pos + kTile > limit_of(a, it.nk, it.nq, it.i0 + tok0);
+        const bool edge = pos + kTile > (w ? lim1 : lim0);
         uint32_t bits[2] = {0u, 0u};
         if (edge && live && r < rows) {
           const int i = it.i0 + tok0 + token, limit = limit_of(a, it.nk, it.nq, i);
