@@ -57,9 +57,14 @@ cudaError_t launch_tree_mask(const int* parents, const int* cu, int n, int total
 // ---------------------------- attention (attention.cu) ----------------------------
 // How a sequence's keys are cut into pieces that are worked on by themselves
 // (128 keys are a block). The cut goes by the sequence alone, so that its
-// results do not depend on the call's other sequences.
+// results do not depend on the call's other sequences. Many short pieces serve
+// a lone sequence, few long ones a batch: against pieces of at least 4 blocks
+// throughout, this rule takes 16.8 instead of 15.3 us for one stream over 4000
+// keys and 83 instead of 88 for 32 streams over 500..6000, 42 instead of 51 for
+// trees of 16 streams over 300..5000 (at least 8 blocks throughout: 17.7, 81, 42).
 constexpr int kSplitItems = 152;     // pieces x heads x query tiles that one sequence is cut into at most (one a SM)
-constexpr int kSplitMinBlocks = 4;   // blocks of a piece at least
+constexpr int kSplitMinBlocks = 4;   // blocks of a piece at least ...
+constexpr int kSplitFew = 6;         // ... of up to this many pieces; of more, twice as many blocks
 struct Cut {
   int pieces, blocks;                // pieces of `blocks` blocks, the last one what is left
 };
@@ -67,6 +72,8 @@ __host__ __device__ inline Cut cut_of(int blocks, int tiles_and_heads) {
   if (blocks < 2 * kSplitMinBlocks || tiles_and_heads >= kSplitItems) return {1, blocks};
   int most = blocks / kSplitMinBlocks;
   const int want = (kSplitItems + tiles_and_heads - 1) / tiles_and_heads;
+  const int few = blocks / (2 * kSplitMinBlocks) > kSplitFew ? blocks / (2 * kSplitMinBlocks) : kSplitFew;
+  if (few < most) most = few;
   if (want < most) most = want;
   const int per = (blocks + most - 1) / most;
   return {(blocks + per - 1) / per, per};
