@@ -44,6 +44,7 @@
 #include "attention_internal.h"
 #include "internal.h"
 #include "ldcg.cuh"
+#include "mbar.cuh"
 #include "pdl.cuh"
 
 namespace moe {
@@ -70,28 +71,10 @@ struct Sizes {
 };
 
 // ------------------------------- PTX helpers --------------------------------
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // One arrival for a whole warp.
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 // 16 bytes global -> shared through L2; zeros where there is no source.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
@@ -102,9 +85,6 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
 // One box of a 3-d tensor (head dimension, heads, rows) to shared memory.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
                                          uint64_t policy) {
@@ -293,14 +273,13 @@ struct Ctl {
   volatile int* abort_flag;
   int* status;
 };
-constexpr long long kBudget = 2000000000LL;  // clock cycles of one wait, about a second
 
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl c) {
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*c.abort_flag) return false;
-    if (clock64() - t0 > kBudget) {
+    if (clock64() - t0 > kWaitCycles) {
       *c.abort_flag = 1;
       atomicExch(c.status, (int)MOE_ERR_TIMEOUT);
       return false;
@@ -810,11 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int i = 0; i < kStages; ++i)
           if ((filled >> i) & 1u)
             while (!mbar_try_wait((by_land >> i) & 1u ? land_bar(i) : full_bar(i), (parity >> i) & 1u) &&
-                   clock64() - t0 < kBudget) {
+                   clock64() - t0 < kWaitCycles) {
             }
         for (int i = 0; i < 2; ++i)
           if ((qfilled >> i) & 1u)
-            while (!mbar_try_wait(qfull_bar(i), (qparity >> i) & 1u) && clock64() - t0 < kBudget) {
+            while (!mbar_try_wait(qfull_bar(i), (qparity >> i) & 1u) && clock64() - t0 < kWaitCycles) {
             }
       }
     } else if (maps.use) {
@@ -1039,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const uint32_t bar = w ? drain2_bar : drain_bar;
       if (elect_one()) tc_commit(bar);
       const long long t0 = clock64();
-      while (!mbar_try_wait(bar, 0) && clock64() - t0 < kBudget) {
+      while (!mbar_try_wait(bar, 0) && clock64() - t0 < kWaitCycles) {
       }
     }
   } else {

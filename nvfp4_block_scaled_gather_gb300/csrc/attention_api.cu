@@ -146,7 +146,9 @@ int moe_kv_compact(const moe_kv_cache_t* cache, void* workspace, size_t ws_bytes
   if (st != MOE_OK) return st;
   const KvWs ws = kv_carve(workspace, *cache);
   if ((st = workspace_status(workspace, ws_bytes, ws.bytes)) != MOE_OK) return st;
-  return status_of(launch_kv_compact(*cache, ws, stream));
+  int* word = status_ptr();
+  if (!word) return MOE_ERR_CUDA;
+  return status_of(launch_kv_compact(*cache, ws, word, stream));
 }
 
 int moe_tree_mask(const int32_t* parents, const int32_t* cu, int n, int total, int32_t* mask, int mask_words,

@@ -25,7 +25,7 @@ struct Heads {
 
 // ------------------------------ pages (kv_pages.cu) ------------------------------
 // Scratch of the upkeep calls, carved from the caller's workspace: a list of
-// page copies (src < 0: none), its count, and for compaction the new id of
+// page copies, its count, and for compaction the new id of
 // every page. keep uses new_len in the same place as src.
 struct KvWs {
   int* count;   // copies in the list
@@ -50,7 +50,7 @@ cudaError_t launch_kv_keep(const moe_kv_cache_t& c, const int* seqs, const int* 
                            const int* kept, int n, const KvWs& ws, int* status, cudaStream_t s);
 cudaError_t launch_kv_copy_pages(const moe_kv_cache_t& c, const int* src, const int* dst, int n, int* status,
                                  cudaStream_t s);
-cudaError_t launch_kv_compact(const moe_kv_cache_t& c, const KvWs& ws, cudaStream_t s);
+cudaError_t launch_kv_compact(const moe_kv_cache_t& c, const KvWs& ws, int* status, cudaStream_t s);
 cudaError_t launch_tree_mask(const int* parents, const int* cu, int n, int total, int* mask, int words, int* status,
                              cudaStream_t s);
 

@@ -3,9 +3,9 @@
 // rows, copying and compacting pages.
 //
 // What bounds these: the tables are a few KB, so the planning is latency (one
-// CTA, a handful of dependent reads), and the page data is a plain copy. So
-// the planning kernels leave a list of page copies in the workspace and one
-// copy kernel spreads the list's bytes over the whole GPU.
+// CTA, a handful of dependent reads), and the page data is a plain copy, bound
+// by memory. So the planning kernels leave a list of page copies in the
+// workspace and one copy kernel spreads the list's bytes over the whole GPU.
 //
 // Nothing read from device memory is followed as an index before it has been
 // checked against its range.
@@ -16,14 +16,17 @@
 #include "attention_internal.h"
 #include "internal.h"
 #include "ldcg.cuh"
+#include "mbar.cuh"
 #include "pdl.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPiece = 16384;      // bytes of one unit of page copying
-constexpr int kCopyThreads = 256;  // 64 bytes a thread and unit: four 16-byte loads in flight
+constexpr int kPiece = 32768;      // bytes of one unit of page copying
+constexpr int kSlots = 6;          // units that a CTA holds in shared memory
+constexpr int kAhead = 4;          // of them being read; the others are being written
+constexpr int kCopyThreads = 256;  // one warp moves the units, the others go over the tables
 
 struct Kv {
   uint8_t* pages;
@@ -54,44 +57,71 @@ Kv make_kv(const moe_kv_cache_t& c) {
 // The first thing found wrong stays until it is read.
 __device__ __forceinline__ void report(int* status, int what) { atomicCAS(status, 0, what); }
 
-__device__ __forceinline__ int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
-
-// Exclusive sum over the CTA's threads (kPlanThreads of them); total: the sum.
-__device__ int block_scan(int v, int& total) {
-  __shared__ int part[kPlanThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int p = part[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(~0u, p, o);
-      if (lane >= o) p += y;
-    }
-    part[lane] = p;
-  }
-  __syncthreads();
-  const int before = warp ? part[warp - 1] : 0;
-  total = part[kPlanThreads / 32 - 1];
-  __syncthreads();
-  return before + x - v;
+// 16-byte aligned runs of bytes to shared memory (complete on the barrier) and
+// back (one group each, of the thread that asks).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(uint8_t* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// By a whole warp, the same answer in every lane; false after kWaitCycles.
+__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
+  bool done = mbar_try_wait(bar, parity);
+  for (const long long t0 = clock64(); !done && clock64() - t0 < kWaitCycles;) done = mbar_try_wait(bar, parity);
+  return __all_sync(~0u, done);
 }
 
-// A thread's share of the pool: a run of pages of its own.
+__device__ __forceinline__ int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
+
+// Exclusive sums over the CTA's threads (kPlanThreads of them) of N values at
+// once, in place; total: the sums.
+template <int N>
+__device__ void block_scan(int (&v)[N], int (&total)[N]) {
+  __shared__ int part[N][kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kPlanThreads == 1024, "a lane for every warp's sum");
+  int x[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) x[e] = v[e];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int y = __shfl_up_sync(~0u, x[e], o);
+      if (lane >= o) x[e] += y;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int e = 0; e < N; ++e) part[e][warp] = x[e];
+  __syncthreads();
+  // every warp sums the warps' sums for itself
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int mine = part[e][lane];
+    total[e] = __reduce_add_sync(~0u, mine);
+    v[e] = x[e] - v[e] + __reduce_add_sync(~0u, lane < warp ? mine : 0);
+  }
+  __syncthreads();
+}
+
+// A warp's share of the pool: a run of pages of its own, in groups of 32.
 struct Run {
   int lo, hi;
 };
 __device__ __forceinline__ Run run_of(int n_pages) {
-  const int per = (n_pages + kPlanThreads - 1) / kPlanThreads;
-  const long long lo = (long long)per * threadIdx.x;
+  const int warps = kPlanThreads / 32, warp = threadIdx.x >> 5;
+  const long long per = ((n_pages + kPlanThreads - 1) / kPlanThreads) * 32LL, lo = per * warp;
+  static_assert(warps * 32 == kPlanThreads, "whole warps");
   return {(int)min(lo, (long long)n_pages), (int)min(lo + per, (long long)n_pages)};
+}
+// Bit l: page p + l of the run is in use. By a whole warp.
+__device__ __forceinline__ uint32_t used_of(const int* refs, const Run& run, int p) {
+  const int at = p + (threadIdx.x & 31);
+  return __ballot_sync(~0u, at < run.hi && ld_cg(refs + at) != 0);
 }
 
 // Plans the growth of up to MOE_KV_MAX_CALL sequences in one CTA.
@@ -100,33 +130,41 @@ __device__ __forceinline__ Run run_of(int n_pages) {
 // sequence with off(i) <= r < off(i + 1). A sequence is the k-th of the call to
 // share an open page: the refs it finds are those minus k (each before it has
 // left for its own copy), so it copies while more than one remain.
+//
+// Latency bounds it, a chain of dependent reads of half a microsecond each. So
+// a thread has one sequence of each 1024 (four in a row, one after the other,
+// made it 14 us for 96 sequences; so it takes 6 us), and the pool is read
+// before the sequences are compared.
+struct Growth {
+  int seq[MOE_KV_MAX_CALL];
+  int open[MOE_KV_MAX_CALL];     // the open page, or -1; then where its copy is in the list, or -1
+  int off[MOE_KV_MAX_CALL + 1];
+  int column[MOE_KV_MAX_CALL];   // of the table, where the first page wanted goes
+};
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(Kv kv, const int* seqs, const int* add, int n,
                                                                    KvWs ws, int* status) {
-  __shared__ int s_seq[MOE_KV_MAX_CALL];
-  __shared__ int s_page[MOE_KV_MAX_CALL];     // the open page, or -1
-  extern __shared__ int s_off[];              // [MOE_KV_MAX_CALL + 1]
+  extern __shared__ int s_growth[];
+  Growth& g = *reinterpret_cast<Growth*>(s_growth);
   constexpr int kPer = MOE_KV_MAX_CALL / kPlanThreads;
-  static_assert(kPer == 4, "the sum of cow[] below");
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  // thread tid plans sequences kPer * tid .. (so that the scan keeps their order)
-  int need[kPer], cow[kPer], len[kPer], more[kPer], own[kPer];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int need[kPer], refs[kPer], len[kPer], more[kPer], own[kPer];  // refs: of the open page
   bool bad = false;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int i = tid * kPer + u;
-    need[u] = cow[u] = len[u] = more[u] = own[u] = 0;
+    const int i = u * kPlanThreads + tid;
+    need[u] = refs[u] = len[u] = more[u] = own[u] = 0;
     if (i >= n) continue;
-    s_seq[i] = -1;
-    s_page[i] = -1;
+    g.seq[i] = -1;
+    g.open[i] = -1;
     const int s = ld_cg(seqs + i);
     const int a = ld_cg(add + i);
     if (s < 0 || s >= kv.max_seqs || a < 0) {
       bad = true;
       continue;
     }
-    s_seq[i] = s;
+    g.seq[i] = s;
     len[u] = ld_cg(kv.length + s);
     own[u] = ld_cg(kv.held + s);
     more[u] = a;
@@ -142,42 +180,54 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(Kv kv, const 
         bad = true;
         continue;
       }
-      s_page[i] = p;
+      g.open[i] = p;
+      refs[u] = ld_cg(kv.refs + p);
     }
   }
+  const Run run = run_of(kv.n_pages);
+  int free_pages = 0;
+#pragma unroll 4
+  for (int p = run.lo; p < run.hi; p += 32) free_pages += min(32, run.hi - p) - __popc(used_of(kv.refs, run, p));
   __syncthreads();
-  int want = 0;
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const int i = tid * kPer + u;
-    if (i >= n || bad) continue;
-    const int s = s_seq[i], p = s_page[i];
+  // a warp compares a sequence with those before it: listed twice? how many share its open page?
+  for (int i = warp; i < n; i += kPlanThreads / 32) {
+    const int s = g.seq[i], p = g.open[i];
     int before = 0;
-    for (int j = 0; j < i; ++j) {
-      bad |= s_seq[j] == s;
-      before += (p >= 0 && s_page[j] == p) ? 1 : 0;
+    for (int j = lane; j < i; j += 32) {
+      bad |= g.seq[j] == s;
+      before += g.open[j] == p ? 1 : 0;
     }
-    cow[u] = p >= 0 && ld_cg(kv.refs + p) - before > 1 ? 1 : 0;
-    want += need[u] + cow[u];
+    before = __reduce_add_sync(~0u, before);
+    if (lane == 0) g.off[i] = before;
   }
   if (tid == 0) *ws.count = 0;
   if (__syncthreads_or(bad ? 1 : 0)) {
     if (tid == 0) report(status, MOE_ERR_INVALID);
     return;
   }
-  int total, copies;
-  int off = block_scan(want, total);
-  int slot = block_scan(cow[0] + cow[1] + cow[2] + cow[3], copies);
+  int total = 0, copies = 0, all_free = 0, first = 0;  // first: rank of the run's first free page
+  int slot[kPer];                                      // in the list of copies, or -1
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    s_off[tid * kPer + u] = off;
-    off += need[u] + cow[u];
+    const int i = u * kPlanThreads + tid;
+    slot[u] = -1;
+    if (u * kPlanThreads >= n) continue;
+    const bool copy = i < n && g.open[i] >= 0 && refs[u] - g.off[i] > 1;
+    const int want = need[u] + (copy ? 1 : 0);
+    int at[3] = {want, copy ? 1 : 0, u == 0 && lane == 0 ? free_pages : 0}, sums[3];
+    block_scan(at, sums);
+    if (i < n) {
+      g.off[i] = total + at[0];
+      g.column[i] = own[u] + need[u] - want;  // with a copy the open page's, before the new ones
+    }
+    if (copy) slot[u] = copies + at[1];
+    if (u == 0) {
+      first = __shfl_sync(~0u, at[2], 0);
+      all_free = sums[2];
+    }
+    total += sums[0];
+    copies += sums[1];
   }
-  if (tid == kPlanThreads - 1) s_off[MOE_KV_MAX_CALL] = off;
-  const Run run = run_of(kv.n_pages);
-  int mine = 0, all_free;
-  for (int p = run.lo; p < run.hi; ++p) mine += ld_cg(kv.refs + p) == 0 ? 1 : 0;
-  int rank = block_scan(mine, all_free);
   if (total > all_free) {
     if (tid == 0) report(status, MOE_ERR_PAGES);
     return;
@@ -185,101 +235,138 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(Kv kv, const 
   // the lengths and the copies' sources; the sequences leave their shared open pages
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int i = tid * kPer + u;
+    const int i = u * kPlanThreads + tid;
     if (i >= n) continue;
-    const int s = s_seq[i];
+    const int s = g.seq[i], open = g.open[i];
     kv.length[s] = len[u] + more[u];
     kv.held[s] = own[u] + need[u];
-    const int open = s_page[i];
-    s_page[i] = -1;  // from here on: where sequence i's copy is in the list, or -1
-    if (cow[u]) {
-      ws.src[slot] = open;
-      ws.rows[slot] = len[u] % kv.page_size;
-      s_page[i] = slot++;
+    g.open[i] = slot[u];
+    if (slot[u] >= 0) {
+      ws.src[slot[u]] = open;
+      ws.rows[slot[u]] = len[u] % kv.page_size;
       atomicSub(kv.refs + open, 1);
     }
   }
   if (tid == 0) *ws.count = copies;
   __syncthreads();
-  // every thread gives out the free pages of its run (a page's refs here only
+  // every warp gives out the free pages of its run (a page's refs here only
   // fall from above 1 to at least 1, so a free page is still the same one)
-  for (int p = run.lo; p < run.hi && rank < total; ++p) {
-    if (ld_cg(kv.refs + p) != 0) continue;
+  for (int p0 = run.lo; p0 < run.hi && first < total; p0 += 32) {
+    const int p = p0 + lane;
+    const uint32_t free = ~used_of(kv.refs, run, p0) & (run.hi - p0 < 32 ? (1u << (run.hi - p0)) - 1u : ~0u);
+    const int rank = first + __popc(free & ((1u << lane) - 1u));
+    first += __popc(free);
+    if (!((free >> lane) & 1u) || rank >= total) continue;
     int lo = 0, hi = n;  // the last i with off(i) <= rank
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_off[mid] <= rank) lo = mid;
+      if (g.off[mid] <= rank) lo = mid;
       else hi = mid;
     }
-    const int s = s_seq[lo], q = rank - s_off[lo], wanted = s_off[lo + 1] - s_off[lo];
-    // the last columns of the grown sequence; with a copy the first page is
-    // the open one's column, which is the one before the new ones
-    const int column = ld_cg(kv.held + s) - wanted + q;
-    if (s_page[lo] >= 0 && q == 0) ws.dst[s_page[lo]] = p;
+    const int q = rank - g.off[lo];
+    if (g.open[lo] >= 0 && q == 0) ws.dst[g.open[lo]] = p;
     kv.refs[p] = 1;
-    kv.table[(long long)s * kv.max_pages + column] = p;
-    ++rank;
-  }
-}
-
-// One unit of page copying: kPiece bytes (or the rest) of `bytes` at src and dst.
-__device__ __forceinline__ void copy_piece(const uint8_t* src, uint8_t* dst, long long at, long long bytes) {
-  const long long left = min((long long)kPiece, bytes - at);
-  const uint4* from = reinterpret_cast<const uint4*>(src + at);
-  uint4* to = reinterpret_cast<uint4*>(dst + at);
-  const int count = (int)(left / 16);
-  uint4 v[kPiece / 16 / kCopyThreads];
-#pragma unroll
-  for (int j = 0; j < kPiece / 16 / kCopyThreads; ++j) {
-    const int c = threadIdx.x + j * kCopyThreads;
-    if (c < count) v[j] = ld_cg(from + c);
-  }
-#pragma unroll
-  for (int j = 0; j < kPiece / 16 / kCopyThreads; ++j) {
-    const int c = threadIdx.x + j * kCopyThreads;
-    if (c < count) to[c] = v[j];
+    kv.table[(long long)g.seq[lo] * kv.max_pages + g.column[lo] + q] = p;
   }
 }
 
 // Carries out a list of page copies in all planes. count: null (n entries) or
 // their number on the device; rows: null for whole pages. check: the list is
 // the caller's, its ids are checked here. With moved, the tables' page ids are
-// replaced as well (compaction).
+// replaced as well (compaction), by the other warps meanwhile.
+//
+// Memory bounds it: what it reads it writes once. A page goes in units of
+// kPiece bytes through shared memory, by asynchronous copies that one warp
+// issues; the warp looks up 32 units at a time, a lane each, so that the reads
+// of the list do not stand between the units. 6.2 TB/s over 700 MB of pages,
+// 55 us for the open pages of 96 forks (blocks of 256 threads that load and
+// store 16 KB: 5.7 TB/s and 74 us; units of 16 KB: 6.4 TB/s and 60 us; of 8 KB:
+// 90 us, the issuing lane is the limit).
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv kv, const int* src, const int* dst,
                                                                   const int* rows, const int* count, int n, int check,
                                                                   const int* moved, int* status) {
+  extern __shared__ __align__(128) uint8_t s_units[];  // [kSlots][kPiece]
+  __shared__ uint64_t s_full[kSlots];
+  __shared__ unsigned long long s_to[kSlots];
+  __shared__ uint32_t s_bytes[kSlots];
+  const int lane = threadIdx.x & 31;
+  const uint32_t units = smem_u32(s_units), full = smem_u32(s_full);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(full + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int entries = count ? ld_cg(count) : n;
-  const int pieces = (int)((kv.page_bytes + kPiece - 1) / kPiece);
-  const long long per = (long long)kv.planes * pieces;
-  for (long long w = blockIdx.x; w < entries * per; w += gridDim.x) {
-    const int i = (int)(w / per);
-    const int r = (int)(w - i * per);
-    const int plane = r / pieces, piece = r - plane * pieces;
-    const int a = ld_cg(src + i);
-    const int b = ld_cg(dst + i);
-    if (check && (a < 0 || a >= kv.n_pages || b < 0 || b >= kv.n_pages)) {
-      if (threadIdx.x == 0) report(status, MOE_ERR_INVALID);
-      continue;
-    }
-    const long long bytes = rows ? (long long)ld_cg(rows + i) * kv.row_bytes : kv.page_bytes;
-    const long long at = (long long)piece * kPiece;
-    if (at >= bytes || a == b) continue;
-    uint8_t* plane_at = kv.pages + plane * kv.plane_bytes;
-    copy_piece(plane_at + a * kv.page_bytes, plane_at + b * kv.page_bytes, at, bytes);
-  }
-  if (moved && entries > 0) {
+  if (threadIdx.x >= 32) {
+    if (!moved || entries <= 0) return;
     const long long cells = (long long)kv.max_seqs * kv.max_pages;
-    for (long long c = (long long)blockIdx.x * kCopyThreads + threadIdx.x; c < cells;
-         c += (long long)gridDim.x * kCopyThreads) {
+    constexpr int kOthers = kCopyThreads - 32;
+    for (long long c = (long long)blockIdx.x * kOthers + threadIdx.x - 32; c < cells; c += (long long)gridDim.x * kOthers) {
       const int p = ld_cg(kv.table + c);
       if (p >= 0 && p < kv.n_pages) {
         const int q = ld_cg(moved + p);
         if (q != p) kv.table[c] = q;
       }
     }
+    return;
   }
+  const int pieces = (int)((kv.page_bytes + kPiece - 1) / kPiece);
+  const long long per = (long long)kv.planes * pieces, all = entries * per;
+  int begun = 0, ended = 0;  // units asked for, units given back
+  bool ok = true;
+  auto end_one = [&]() {
+    const int i = ended % kSlots;
+    ok = wait_full(full + 8 * i, (ended / kSlots) & 1);
+    if (!ok) return;
+    if (lane == 0) bulk_store(reinterpret_cast<uint8_t*>(s_to[i]), units + i * kPiece, s_bytes[i]);
+    ++ended;
+  };
+  for (long long w0 = blockIdx.x; ok && w0 < all; w0 += 32LL * gridDim.x) {
+    const long long w = w0 + (long long)lane * gridDim.x;
+    unsigned long long from = 0, to = 0;
+    uint32_t bytes = 0;
+    if (w < all) {
+      const int i = (int)(w / per);
+      const int r = (int)(w - i * per);
+      const int plane = r / pieces;
+      const long long at = (long long)(r - plane * pieces) * kPiece;
+      const int a = ld_cg(src + i), b = ld_cg(dst + i);
+      const long long most = rows ? (long long)ld_cg(rows + i) * kv.row_bytes : kv.page_bytes;
+      if (check && (a < 0 || a >= kv.n_pages || b < 0 || b >= kv.n_pages)) {
+        report(status, MOE_ERR_INVALID);
+      } else if (at < most && a != b) {
+        const unsigned long long base = reinterpret_cast<unsigned long long>(kv.pages) + plane * kv.plane_bytes + at;
+        from = base + a * kv.page_bytes;
+        to = base + b * kv.page_bytes;
+        bytes = (uint32_t)min((long long)kPiece, most - at);
+      }
+    }
+    for (uint32_t left = __ballot_sync(~0u, bytes != 0); ok && left; left &= left - 1) {
+      const int l = __ffs(left) - 1, i = begun % kSlots;
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(__shfl_sync(~0u, from, l));
+      const unsigned long long q = __shfl_sync(~0u, to, l);
+      const uint32_t size = __shfl_sync(~0u, bytes, l);
+      if (lane == 0) {
+        // of the begun - kAhead writes so far all but the last few have let go
+        // of their slots: the one of unit begun - kSlots is among them
+        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kSlots - kAhead - 1) : "memory");
+        s_to[i] = q;
+        s_bytes[i] = size;
+        mbar_expect_tx(full + 8 * i, size);
+        bulk_load(units + i * kPiece, p, size, full + 8 * i);
+      }
+      if (++begun > kAhead) end_one();
+    }
+  }
+  while (ok && ended < begun) end_one();
+  if (!ok) {
+    // what is still on its way must land before the CTA may go
+    if (lane == 0) report(status, MOE_ERR_TIMEOUT);
+    for (; ended < begun; ++ended) wait_full(full + 8 * (ended % kSlots), (ended / kSlots) & 1);
+  }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Compaction's plan in one CTA: U pages in use; the k-th used page from U on
@@ -288,48 +375,85 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Kv kv, KvWs 
   pdl_wait();
   pdl_trigger();
   const Run run = run_of(kv.n_pages);
-  int used = 0, in_use, holes, movers;
-  for (int p = run.lo; p < run.hi; ++p) used += ld_cg(kv.refs + p) != 0 ? 1 : 0;
-  block_scan(used, in_use);
+  const int lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1u;
+  int used = 0;
+#pragma unroll 4
+  for (int p = run.lo; p < run.hi; p += 32) used += __popc(used_of(kv.refs, run, p));
+  int count[1] = {lane == 0 ? used : 0}, all[1];
+  block_scan(count, all);
+  const int in_use = all[0];
+  // bit l: page p + l of the run comes before page in_use
+  auto front_of = [&](int p) {
+    const int left = min(run.hi, in_use) - p;
+    return left <= 0 ? 0u : left < 32 ? (1u << left) - 1u : ~0u;
+  };
   int h = 0, m = 0;
-  for (int p = run.lo; p < run.hi; ++p) {
-    const bool busy = ld_cg(kv.refs + p) != 0;
-    h += !busy && p < in_use ? 1 : 0;
-    m += busy && p >= in_use ? 1 : 0;
-    ws.moved[p] = p;
+#pragma unroll 4
+  for (int p = run.lo; p < run.hi; p += 32) {
+    const uint32_t busy = used_of(kv.refs, run, p), front = front_of(p);
+    h += __popc(~busy & front);
+    m += __popc(busy & ~front);
+    if (p + lane < run.hi) ws.moved[p + lane] = p + lane;
   }
-  h = block_scan(h, holes);
-  m = block_scan(m, movers);
-  if (threadIdx.x == 0) *ws.count = movers;
-  for (int p = run.lo; p < run.hi && p < in_use; ++p)
-    if (ld_cg(kv.refs + p) == 0) ws.dst[h++] = p;
+  int at[2] = {lane == 0 ? h : 0, lane == 0 ? m : 0}, sums[2];
+  block_scan(at, sums);
+  h = __shfl_sync(~0u, at[0], 0);
+  m = __shfl_sync(~0u, at[1], 0);
+  if (threadIdx.x == 0) *ws.count = sums[1];
+  for (int p = run.lo; p < run.hi && p < in_use; p += 32) {
+    const uint32_t hole = ~used_of(kv.refs, run, p) & front_of(p);
+    if ((hole >> lane) & 1u) ws.dst[h + __popc(hole & below)] = p + lane;
+    h += __popc(hole);
+  }
   __syncthreads();
-  for (int p = max(run.lo, in_use); p < run.hi; ++p) {
-    const int refs = ld_cg(kv.refs + p);
-    if (refs == 0) continue;
-    const int to = ld_cg(ws.dst + m);
-    ws.src[m++] = p;
-    ws.moved[p] = to;
-    kv.refs[to] = refs;
-    kv.refs[p] = 0;
+  for (int p = run.lo; p < run.hi; p += 32) {
+    const uint32_t mover = used_of(kv.refs, run, p) & ~front_of(p);
+    if ((mover >> lane) & 1u) {
+      const int from = p + lane, k = m + __popc(mover & below);
+      const int to = ld_cg(ws.dst + k), refs = ld_cg(kv.refs + from);
+      ws.src[k] = from;
+      ws.moved[from] = to;
+      kv.refs[to] = refs;
+      kv.refs[from] = 0;
+    }
+    m += __popc(mover);
   }
 }
 
-// One warp per row: both of its planes' rows, 16 bytes a lane.
+// One warp per row: both of its planes' rows, 16 bytes a lane. A row's place is
+// found by a chain of dependent reads, so its values are asked for first, and
+// its sequence is searched for with 32 probes at a time.
 __global__ void __launch_bounds__(256) append_kernel(Kv kv, int layer, const int* seqs, const int* cu, int n, int total,
                                                      Heads k, Heads v, int heads, int head_dim, int* status) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int per_head = head_dim / 8, chunks = heads * per_head;
+  constexpr int kHeld = 4;  // chunks a lane that are asked for ahead
   for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8) {
-    if (t < ld_cg(cu) || t >= ld_cg(cu + n)) continue;
+    uint4 a[kHeld], b[kHeld];
+    auto load = [&](int c, uint4& x, uint4& y) {
+      const int head = c / per_head, e = (c - head * per_head) * 8;
+      x = ld_cg(reinterpret_cast<const uint4*>(k.p + t * k.ts + head * k.hs + e));
+      y = ld_cg(reinterpret_cast<const uint4*>(v.p + t * v.ts + head * v.hs + e));
+    };
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (lane + 32 * j < chunks) load(lane + 32 * j, a[j], b[j]);
+    const int last = ld_cg(cu + n);
     int lo = 0, hi = n;  // the last i with cu[i] <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (ld_cg(cu + mid) <= t) lo = mid;
-      else hi = mid;
+    bool inside = n > 0 && t < last;
+    while (hi > lo) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const uint32_t up_to = __ballot_sync(~0u, at < hi && ld_cg(cu + at) <= t);
+      if (!up_to) inside = false;  // before the first
+      const int i = up_to ? 31 - __clz(up_to) : 0;
+      lo += i * step;
+      hi = min(lo + step, hi);
+      if (step == 1) break;
     }
+    if (!inside) continue;
     const int s = ld_cg(seqs + lo), end = ld_cg(cu + lo + 1);
     bool ok = s >= 0 && s < kv.max_seqs && t < end;
     long long row = 0;
@@ -347,12 +471,17 @@ __global__ void __launch_bounds__(256) append_kernel(Kv kv, int layer, const int
       continue;
     }
     uint8_t* to = kv.pages + 2LL * layer * kv.plane_bytes + row * kv.row_bytes;
-    for (int c = lane; c < chunks; c += 32) {
-      const int head = c / per_head, e = (c - head * per_head) * 8;
-      const uint4 a = ld_cg(reinterpret_cast<const uint4*>(k.p + t * k.ts + head * k.hs + e));
-      const uint4 b = ld_cg(reinterpret_cast<const uint4*>(v.p + t * v.ts + head * v.hs + e));
-      reinterpret_cast<uint4*>(to)[c] = a;
-      reinterpret_cast<uint4*>(to + kv.plane_bytes)[c] = b;
+    auto store = [&](int c, const uint4& x, const uint4& y) {
+      reinterpret_cast<uint4*>(to)[c] = x;
+      reinterpret_cast<uint4*>(to + kv.plane_bytes)[c] = y;
+    };
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (lane + 32 * j < chunks) store(lane + 32 * j, a[j], b[j]);
+    for (int c = lane + 32 * kHeld; c < chunks; c += 32) {
+      uint4 x, y;
+      load(c, x, y);
+      store(c, x, y);
     }
   }
 }
@@ -433,11 +562,16 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(Kv kv, const int* se
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x, tid = threadIdx.x;
+  const int* row = keep + (long long)i * max_keep;
+  const int mine = tid < max_keep ? ld_cg(row + tid) : 0;
   const int s = ld_cg(seqs + i), m = ld_cg(drafted + i), k = ld_cg(kept + i);
   bool bad = s < 0 || s >= kv.max_seqs || m < 0 || k < 0 || k > m || k > max_keep;
   for (int j = tid; j < i; j += kKeepThreads) bad |= ld_cg(seqs + j) == s;
   int length = 0, start = 0;
-  const int* row = keep + (long long)i * max_keep;
+  auto offset = [&](int pos) -> long long {
+    const int p = ld_cg(kv.table + (long long)s * kv.max_pages + pos / kv.page_size);
+    return ((long long)p * kv.page_size + pos % kv.page_size) * kv.row_bytes;
+  };
   if (!bad) {
     length = ld_cg(kv.length + s);
     start = length - m;
@@ -445,8 +579,13 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(Kv kv, const int* se
   }
   if (!bad) {
     for (int j = tid; j < k; j += kKeepThreads) {
-      const int x = ld_cg(row + j);
-      bad |= x < 0 || x >= m || (j > 0 && ld_cg(row + j - 1) >= x);
+      const int x = j == tid ? mine : ld_cg(row + j);
+      const bool out = x < 0 || x >= m;
+      if (j == tid && !out) {  // the first rows' places (of no use if a page turns out to be bad)
+        s_src[tid] = offset(start + x);
+        s_dst[tid] = offset(start + tid);
+      }
+      bad |= out || (j > 0 && ld_cg(row + j - 1) >= x);
     }
     if (k > 0)
       for (int c = start / kv.page_size + tid; c < ceil_div(length, kv.page_size); c += kKeepThreads) {
@@ -462,18 +601,16 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(Kv kv, const int* se
   if (bad) return;
   uint8_t* plane = kv.pages + blockIdx.y * kv.plane_bytes;
   const long long byte = ((long long)blockIdx.z * kKeepThreads + tid) * 16;
-  auto offset = [&](int pos) -> long long {
-    const int p = ld_cg(kv.table + (long long)s * kv.max_pages + pos / kv.page_size);
-    return ((long long)p * kv.page_size + pos % kv.page_size) * kv.row_bytes;
-  };
   for (int j0 = 0; j0 < k; j0 += kKeepThreads) {
     const int count = min(kKeepThreads, k - j0);
-    __syncthreads();
-    if (tid < count) {
-      s_src[tid] = offset(start + ld_cg(row + j0 + tid));
-      s_dst[tid] = offset(start + j0 + tid);
+    if (j0 > 0) {
+      __syncthreads();
+      if (tid < count) {
+        s_src[tid] = offset(start + ld_cg(row + j0 + tid));
+        s_dst[tid] = offset(start + j0 + tid);
+      }
+      __syncthreads();
     }
-    __syncthreads();
     if (byte >= kv.row_bytes) continue;
     for (int j = 0; j < count; j += 4) {
       uint4 v[4];
@@ -552,10 +689,15 @@ __global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const int* pare
   }
 }
 
-int copy_grid(const Kv& kv, long long entries) {
-  const long long units = entries * kv.planes * ((kv.page_bytes + kPiece - 1) / kPiece);
-  const long long most = (long long)num_sms() * 8;
-  return (int)(units < 1 ? 1 : units < most ? units : most);
+cudaError_t launch_copy(const Kv& kv, long long entries, const int* src, const int* dst, const int* rows,
+                        const int* count, int n, int check, const int* moved, int* status, cudaStream_t s) {
+  const int smem = kSlots * kPiece;
+  const cudaError_t err = cudaFuncSetAttribute(copy_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  const long long units = entries * kv.planes * ((kv.page_bytes + kPiece - 1) / kPiece), most = num_sms();
+  const int grid = (int)(units < 1 ? 1 : units < most ? units : most);
+  return launch_pdl(copy_pages_kernel, dim3(grid), dim3(kCopyThreads), smem, s, kv, src, dst, rows, count, n, check,
+                    moved, status);
 }
 
 }  // namespace
@@ -581,13 +723,12 @@ KvWs kv_carve(void* base, const moe_kv_cache_t& c) {
 cudaError_t launch_kv_extend(const moe_kv_cache_t& c, const int* seqs, const int* add, int n, const KvWs& ws,
                              int* status, cudaStream_t s) {
   const Kv kv = make_kv(c);
-  const size_t smem = (MOE_KV_MAX_CALL + 1) * sizeof(int);
+  const size_t smem = sizeof(Growth);
   cudaError_t err = cudaFuncSetAttribute(extend_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   err = launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, kv, seqs, add, n, ws, status);
   if (err != cudaSuccess) return err;
-  return launch_pdl(copy_pages_kernel, dim3(copy_grid(kv, n)), dim3(kCopyThreads), 0, s, kv, (const int*)ws.src,
-                    (const int*)ws.dst, (const int*)ws.rows, (const int*)ws.count, 0, 0, (const int*)nullptr, status);
+  return launch_copy(kv, n, ws.src, ws.dst, ws.rows, ws.count, 0, 0, nullptr, status, s);
 }
 
 cudaError_t launch_kv_append(const moe_kv_cache_t& c, int layer, const int* seqs, const int* cu, int n, int total,
@@ -620,18 +761,14 @@ cudaError_t launch_kv_keep(const moe_kv_cache_t& c, const int* seqs, const int* 
 
 cudaError_t launch_kv_copy_pages(const moe_kv_cache_t& c, const int* src, const int* dst, int n, int* status,
                                  cudaStream_t s) {
-  const Kv kv = make_kv(c);
-  return launch_pdl(copy_pages_kernel, dim3(copy_grid(kv, n)), dim3(kCopyThreads), 0, s, kv, src, dst,
-                    (const int*)nullptr, (const int*)nullptr, n, 1, (const int*)nullptr, status);
+  return launch_copy(make_kv(c), n, src, dst, nullptr, nullptr, n, 1, nullptr, status, s);
 }
 
-cudaError_t launch_kv_compact(const moe_kv_cache_t& c, const KvWs& ws, cudaStream_t s) {
+cudaError_t launch_kv_compact(const moe_kv_cache_t& c, const KvWs& ws, int* status, cudaStream_t s) {
   const Kv kv = make_kv(c);
   const cudaError_t err = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, kv, ws);
   if (err != cudaSuccess) return err;
-  return launch_pdl(copy_pages_kernel, dim3(copy_grid(kv, c.n_pages)), dim3(kCopyThreads), 0, s, kv,
-                    (const int*)ws.src, (const int*)ws.dst, (const int*)nullptr, (const int*)ws.count, 0, 0,
-                    (const int*)ws.moved, (int*)nullptr);
+  return launch_copy(kv, c.n_pages, ws.src, ws.dst, nullptr, ws.count, 0, 0, ws.moved, status, s);
 }
 
 cudaError_t launch_tree_mask(const int* parents, const int* cu, int n, int total, int* mask, int words, int* status,
