@@ -68,13 +68,17 @@ constexpr int kSplitFew = 6;         // ... of up to this many pieces; of more, 
 struct Cut {
   int pieces, blocks;                // pieces of `blocks` blocks, the last one what is left
 };
-__host__ __device__ inline Cut cut_of(int blocks, int tiles_and_heads) {
-  if (blocks < 2 * kSplitMinBlocks || tiles_and_heads >= kSplitItems) return {1, blocks};
+// The most pieces (a limit that only rises with the blocks).
+__host__ __device__ inline int pieces_within(int blocks, int tiles_and_heads) {
   int most = blocks / kSplitMinBlocks;
   const int want = (kSplitItems + tiles_and_heads - 1) / tiles_and_heads;
   const int few = blocks / (2 * kSplitMinBlocks) > kSplitFew ? blocks / (2 * kSplitMinBlocks) : kSplitFew;
   if (few < most) most = few;
-  if (want < most) most = want;
+  return want < most ? want : most;
+}
+__host__ __device__ inline Cut cut_of(int blocks, int tiles_and_heads) {
+  if (blocks < 2 * kSplitMinBlocks || tiles_and_heads >= kSplitItems) return {1, blocks};
+  const int most = pieces_within(blocks, tiles_and_heads);
   const int per = (blocks + most - 1) / most;
   return {(blocks + per - 1) / per, per};
 }
