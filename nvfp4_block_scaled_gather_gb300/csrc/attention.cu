@@ -38,8 +38,8 @@
 //    drains its copies and MMAs, frees tensor memory and returns.
 //
 // What bounds it: of long prompts the MMAs (two of 128 x 128 x 128 a step;
-// 8192 tokens, 32 query and 8 kv heads of 128: 382 us, 1440 TFLOP/s counting
-// what the causal mask leaves, 76% of a large matrix product's rate); of decode
+// 8192 tokens, 32 query and 8 kv heads of 128: 368 us, 1490 TFLOP/s counting
+// what the causal mask leaves, 79% of a large matrix product's rate); of decode
 // batches the reads of the cache (32 streams over 500..6000 keys, 8 kv heads:
 // 83 us, 5.4 TB/s); of single short calls the chain from the plan over the
 // first loads, S, P and O to the store (12.5 us, launch and all).
@@ -168,6 +168,14 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   auto qfull_bar = [&](int s) { return bar0 + 8u * (16 + s); };
   auto qempty_bar = [&](int s) { return bar0 + 8u * (18 + s); };
   auto sfull_bar = [&](int w) { return bar0 + 8u * (20 + w); };
-  auto pfull_bar = [&](int w, int half) { return bar0 + 8u * (half ? 47 + w : 22 + w); };  // 64 keys of P each
+  auto pfull_bar = [&](int w, int part) { return bar0 + 8u * (part ? 47 + w : 22 + w); };  // 2 x 32 keys of P each
   auto ofull_bar = [&](int w) { return bar0 + 8u * (24 + w); };
   auto oempty_bar = [&](int w) { return bar0 + 8u * (26 + w); };
   const uint32_t drain_bar = bar0 + 8u * 29, drain2_bar = bar0 + 8u * 46;
@@ -595,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (i < 18) return maps.use ? 1 : kLoaders;        // query tiles full
       if (i < 20) return 2;                              // query tiles empty
       if (i < 22) return 1;                              // scores full
-      if (i < 24 || i == 47 || i == 48) return 4;        // weights full: warps
+      if (i < 24 || i == 47 || i == 48) return 8;        // weights full: warps
       if (i < 26) return 1;                              // O full
       if (i < 28) return 8;                              // O empty: warps
       if (i >= 30 && i < 34) return 1;                   // items full
@@ -972,16 +980,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           // 16 keys a step; steps past the sequence's end are left out
           const int ksteps = min((nk - (b0 + pending) * kTile + 15) / 16, kTile / 16);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (ok) ok = wait_bar(pfull_bar(w, half), steps, ctl);
+          for (int part = 0; part < 2; ++part) {
+            if (ok) ok = wait_bar(pfull_bar(w, part), steps, ctl);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
-                if (k < ksteps)
-                  tc_mma_ts(tO, tS + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o, !first || k != 0);
-              if (half) {
+              for (int i = 0; i < 4; ++i) {  // keys 0..31 and 64..95, then the others: 8 columns of P, 2048 bytes of V
+                const int k = 2 * part + (i & 1) + (i & 2) * 2;
+                if (k < ksteps) tc_mma_ts(tO, tS + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o, !first || k != 0);
+              }
+              if (part) {
                 tc_commit(empty_bar(vat.slot));
                 if (pending == last) tc_commit(ofull_bar(w));
               }
@@ -1125,18 +1134,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const float base = m == -INFINITY ? 0.0f : -m * c;
             const uint64_t c2 = pair_of(c, c), base2 = pair_of(base, base);
             uint64_t sum[2] = {0, 0};
-            uint32_t p[32];
+            // in two parts, so that the MMAs of the first run while the second is
+            // made (8192 keys: 368 us, in one part 380); each waits for all eight
+            // warps, whose rescaling of O must be over
 #pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-              const uint64_t x = fma2(pair_of(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), c2, base2);
-              float p0, p1;
-              split_pair(x, p0, p1);
-              p0 = ex2(p0);
-              p1 = ex2(p1);
-              sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair_of(p0, p1));
-              p[j / 2] = pack2<kType>(p0, p1);
+            for (int part = 0; part < 2; ++part) {
+              uint32_t p[16];
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const int e = part * 32 + j;
+                const uint64_t x = fma2(pair_of(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, base2);
+                float p0, p1;
+                split_pair(x, p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair_of(p0, p1));
+                p[j / 2] = pack2<kType>(p0, p1);
+              }
+              tc_st16(tS + half * 32 + part * 16, p);
+              if (part == 0) {
+                tc_wait_st();
+                tc_fence_before();
+                warp_arrive(pfull_bar(w, 0), lane);
+              }
             }
-            tc_st32(tS + half * 32, p);
             float a0, a1;
             split_pair(add2(sum[0], sum[1]), a0, a1);
             l += a0 + a1;
@@ -1152,8 +1173,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         ok = here;
         if (!ok) break;
+        if (!live) warp_arrive(pfull_bar(w, 0), lane);
         tc_fence_before();
-        warp_arrive(pfull_bar(w, half), lane);
+        warp_arrive(pfull_bar(w, 1), lane);
       }
       if (!ok) break;
       // ------------------------------ epilogue ------------------------------
