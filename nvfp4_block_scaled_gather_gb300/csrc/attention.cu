@@ -38,8 +38,8 @@
 //    drains its copies and MMAs, frees tensor memory and returns.
 //
 // What bounds it: of long prompts the MMAs (two of 128 x 128 x 128 a step;
-// 8192 tokens, 32 query and 8 kv heads of 128: 368 us, 1490 TFLOP/s counting
-// what the causal mask leaves, 79% of a large matrix product's rate); of decode
+// 8192 tokens, 32 query and 8 kv heads of 128: 362 us, 1520 TFLOP/s counting
+// what the causal mask leaves, 80% of a large matrix product's rate); of decode
 // batches the reads of the cache (32 streams over 500..6000 keys, 8 kv heads:
 // 83 us, 5.4 TB/s); of single short calls the chain from the plan over the
 // first loads, S, P and O to the store (12.5 us, launch and all).
@@ -112,6 +112,9 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
+}
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 // The same box back to global memory, and the waits of the lane that issued it:
 // until shared memory has been read, until all is written.
@@ -425,14 +428,14 @@ __device__ __forceinline__ Item item_of(const AttnArgs& a, const Planned* s_plan
                                         int largest, int round, int tpt) {
   const int lane = threadIdx.x & 31;
   Item x = {};
-  const long long next =
-      (long long)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  // (below 2^32: an item has a row of a tile at least, or of a partial result, and both are counted in 31 bits)
+  const uint32_t next = (uint32_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   // (a CTA's last round can miss it, but then no later one is left)
-  x.end = next >= (long long)total * a.heads_kv;
+  x.end = next >= (unsigned long long)total * a.heads_kv;
   if (x.end) return x;
-  const int kvh = (int)(next % a.heads_kv);
-  int u = (int)(next / a.heads_kv);  // item of this kv head
-  int b = 0, first = 0;              // its sequence, and where the sequence's items of this size begin
+  int u = (int)(next / (uint32_t)a.heads_kv);  // item of this kv head
+  const int kvh = (int)(next - (uint32_t)u * a.heads_kv);
+  int b = 0, first = 0;                        // its sequence, and where the sequence's items of this size begin
   Planned w;
   long long part;
   if (a.n == 1) {
@@ -616,6 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  if (warp == 8 && maps.use && lane < (maps.store ? 4 : 3))
+    tma_prefetch(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.out);
   if (warp == 10) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols)
@@ -637,10 +642,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     part += part_rows_of(a, w);
   }
   long long p = part;  // inclusive sum of the warp's partial rows (for up to kPlan sequences)
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(~0u, p, o);
-    if (lane >= o) p += y;
-  }
+  if (a.part_o)
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, p, o);
+      if (lane >= o) p += y;
+    }
   count = __reduce_add_sync(~0u, count);
   size = __reduce_max_sync(~0u, size);
   if (lane == 31) {
@@ -651,17 +657,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   __syncthreads();
   if (tid < kPlan) {
     p -= part;
-    for (int x = 0; x < warp; ++x) p += s_wpart[x];
+    if (a.part_o)
+      for (int x = 0; x < warp; ++x) p += s_wpart[x];
     s_part[tid] = p;
   }
-  if (tid == 0) {
-    int all = 0, most = 0;
-    for (int x = 0; x < kThreads / 32; ++x) {
-      all += s_wsum[x];
-      most = max(most, s_wsum[16 + x]);
+  if (warp == kThreads / 32 - 1) {
+    const bool has = lane < kThreads / 32;
+    const int all = __reduce_add_sync(~0u, has ? s_wsum[lane] : 0);
+    const int most = __reduce_max_sync(~0u, has ? s_wsum[16 + lane] : 0);
+    if (lane == 0) {
+      *s_total = all;
+      *s_largest = most;
     }
-    *s_total = all;
-    *s_largest = most;
   }
   __syncthreads();
   tc_fence_after();
