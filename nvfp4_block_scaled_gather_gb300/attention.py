@@ -11,6 +11,7 @@ the library raises RuntimeError. There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -35,7 +36,8 @@ class CacheStruct(ctypes.Structure):
                 ("refs", c_void_p), ("max_seqs", c_int), ("max_pages", c_int)]
 
 
-_CACHE, _HEADS = ctypes.POINTER(CacheStruct), ctypes.POINTER(Heads)
+_CACHE, _HEADS = ctypes.POINTER(CacheStruct), c_void_p
+_heads_bytes = struct.Struct("Pqq").pack  # a moe_heads_t, at a fifth of the time that the class takes
 
 _SIGS = {
     "moe_kv_workspace_size": (c_size_t, [_CACHE]),
@@ -91,13 +93,14 @@ def _ints(name, t, n, device: int) -> int:
 
 
 def _heads(name, t, dtype, device: int):
-    """[tokens, heads, dim] with dim contiguous, as moe_heads_t."""
+    """[tokens, heads, dim] with dim contiguous, as the bytes of a moe_heads_t, and its shape."""
+    shape = t.shape
     if t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{name} must be {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(shape)}")
     ts, hs, ds = t.stride()
-    tokens, heads, dim = t.shape
+    tokens, heads, dim = shape
     # a stride along one element says nothing
     if tokens <= 1:
         ts = 0
@@ -106,7 +109,7 @@ def _heads(name, t, dtype, device: int):
     if (ds != 1 and dim != 1) or ts % 8 or hs % 8:
         raise ValueError(f"{name}: the last dimension must be contiguous and the other strides multiples of 8 elements, "
                          f"got {t.stride()}")
-    return Heads(t.data_ptr(), ts, hs)
+    return _heads_bytes(t.data_ptr(), ts, hs), shape
 
 
 def _call(name, fn, *args):
@@ -131,7 +134,7 @@ class KVCache:
         max_seqs, max_pages = table.shape
         self.pages, self.table, self.length, self.held, self.refs = pages, table, length, held, refs
         self.layers, self.device, self.dtype = planes // 2, pages.get_device(), pages.dtype
-        self.heads_kv, self.head_dim = heads, dim
+        self.heads_kv, self.head_dim, self.row = heads, dim, (heads, dim)
         self.struct = CacheStruct(pages.data_ptr(), planes, n_pages, page_size, heads, dim, _CODES[pages.dtype],
                                   _ints("table", table, max_seqs * max_pages, self.device),
                                   _ints("length", length, max_seqs, self.device),
@@ -167,13 +170,13 @@ def moe_kv_extend(cache: KVCache, seqs, add, workspace, stream=None):
 
 
 def moe_kv_append(cache: KVCache, layer: int, seqs, cu, k, v, stream=None):
-    n, total, dev = seqs.numel(), k.shape[0], cache.device
-    shape = (total, cache.heads_kv, cache.head_dim)
-    if k.shape != shape or v.shape != shape:
-        raise ValueError(f"k and v must be {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    n, dev = seqs.numel(), cache.device
+    (hk, shape), (hv, shape_v) = _heads("k", k, cache.dtype, dev), _heads("v", v, cache.dtype, dev)
+    if shape[1:] != cache.row or shape_v != shape:
+        raise ValueError(f"k and v must be [total, {cache.heads_kv}, {cache.head_dim}], got {tuple(shape)} and "
+                         f"{tuple(shape_v)}")
     _call("moe_kv_append", load().moe_kv_append, cache._ref, layer, _ints("seqs", seqs, n, dev),
-          _ints("cu", cu, n + 1, dev), n, total, ctypes.byref(_heads("k", k, cache.dtype, dev)),
-          ctypes.byref(_heads("v", v, cache.dtype, dev)), _stream(stream, dev))
+          _ints("cu", cu, n + 1, dev), n, shape[0], hk, hv, _stream(stream, dev))
 
 
 def moe_kv_fork(cache: KVCache, src, dst, stream=None):
@@ -233,16 +236,16 @@ def moe_attention_prompt(q, k, v, cu_q, cu_k, out, lse=None, scale=None, stream=
     code = _CODES.get(dtype)
     if code is None:
         raise ValueError(f"q must be bfloat16 or float16, got {dtype}")
-    hq, ho = _heads("q", q, dtype, dev), _heads("out", out, dtype, dev)
-    hk, hv = _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
-    total_q, heads_q, dim = q.shape
-    total_k, heads_kv, dim_k = k.shape
-    if dim_k != dim or v.shape != k.shape or out.shape != q.shape:
-        raise ValueError(f"k and v must be [total_k, kv_heads, {dim}] and out like q, got {tuple(k.shape)}, "
-                         f"{tuple(v.shape)} and {tuple(out.shape)}")
-    _call("moe_attention_prompt", load().moe_attention_prompt, ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
+    (hq, shape), (ho, shape_o) = _heads("q", q, dtype, dev), _heads("out", out, dtype, dev)
+    (hk, shape_k), (hv, shape_v) = _heads("k", k, dtype, dev), _heads("v", v, dtype, dev)
+    total_q, heads_q, dim = shape
+    total_k, heads_kv, dim_k = shape_k
+    if dim_k != dim or shape_v != shape_k or shape_o != shape:
+        raise ValueError(f"k and v must be [total_k, kv_heads, {dim}] and out like q, got {tuple(shape_k)}, "
+                         f"{tuple(shape_v)} and {tuple(shape_o)}")
+    _call("moe_attention_prompt", load().moe_attention_prompt, hq, hk, hv,
           _ints("cu_q", cu_q, n + 1, dev), _ints("cu_k", cu_k, n + 1, dev), n, total_q, total_k, heads_q, heads_kv, dim,
-          code, dim ** -0.5 if scale is None else scale, ctypes.byref(ho), _lse(lse, total_q, heads_q, dev),
+          code, dim ** -0.5 if scale is None else scale, ho, _lse(lse, total_q, heads_q, dev),
           _stream(stream, dev))
 
 
@@ -258,18 +261,18 @@ def moe_attention_cached(q, cache: KVCache, layer: int, seqs, cu_q, out, workspa
     mask: None for a chain, else the tree's bits (moe_tree_mask). scale
     defaults to head_dim ** -0.5."""
     n, dev = seqs.numel(), cache.device
-    hq, ho = _heads("q", q, cache.dtype, dev), _heads("out", out, cache.dtype, dev)
-    total_q, heads_q, dim = q.shape
-    if dim != cache.head_dim or out.shape != q.shape:
-        raise ValueError(f"q and out must be [total_q, heads_q, {cache.head_dim}], got {tuple(q.shape)} and "
-                         f"{tuple(out.shape)}")
+    (hq, shape), (ho, shape_o) = _heads("q", q, cache.dtype, dev), _heads("out", out, cache.dtype, dev)
+    total_q, heads_q, dim = shape
+    if dim != cache.head_dim or shape_o != shape:
+        raise ValueError(f"q and out must be [total_q, heads_q, {cache.head_dim}], got {tuple(shape)} and "
+                         f"{tuple(shape_o)}")
     words, bits = 0, None
     if mask is not None:
         if mask.dim() != 2:
             raise ValueError("mask must be [total_q, words]")
         words = mask.shape[1]
         bits = _ints("mask", mask, total_q * words, dev)
-    _call("moe_attention_cached", load().moe_attention_cached, ctypes.byref(hq), cache._ref, layer,
+    _call("moe_attention_cached", load().moe_attention_cached, hq, cache._ref, layer,
           _ints("seqs", seqs, n, dev), _ints("cu_q", cu_q, n + 1, dev), n, total_q, heads_q, bits, words,
-          dim ** -0.5 if scale is None else scale, ctypes.byref(ho), _lse(lse, total_q, heads_q, dev),
+          dim ** -0.5 if scale is None else scale, ho, _lse(lse, total_q, heads_q, dev),
           *_scratch(workspace, dev), _stream(stream, dev))
