@@ -23,10 +23,11 @@ namespace moe {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPiece = 32768;      // bytes of one unit of page copying
-constexpr int kSlots = 6;          // units that a CTA holds in shared memory
-constexpr int kAhead = 4;          // of them being read; the others are being written
-constexpr int kCopyThreads = 256;  // one warp moves the units, the others go over the tables
+constexpr int kPiece = 16384;      // bytes of one unit of page copying
+constexpr int kMovers = 4;         // warps that move units
+constexpr int kSlots = 3;          // units that each holds in shared memory
+constexpr int kAhead = 2;          // of them being read; the others are being written
+constexpr int kCopyThreads = 256;  // the other warps go over the tables
 
 struct Kv {
   uint8_t* pages;
@@ -276,34 +277,34 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(Kv kv, const 
 // replaced as well (compaction), by the other warps meanwhile.
 //
 // Memory bounds it: what it reads it writes once. A page goes in units of
-// kPiece bytes through shared memory, by asynchronous copies that one warp
-// issues; the warp looks up 32 units at a time, a lane each, so that the reads
-// of the list do not stand between the units. 6.2 TB/s over 700 MB of pages,
-// 55 us for the open pages of 96 forks (blocks of 256 threads that load and
-// store 16 KB: 5.7 TB/s and 74 us; units of 16 KB: 6.4 TB/s and 60 us; of 8 KB:
-// 90 us, the issuing lane is the limit).
+// kPiece bytes through shared memory, by asynchronous copies; a warp looks up
+// 32 units at a time, a lane each, so that the reads of the list do not stand
+// between the units. 6.3 TB/s over 1300 MB of pages of 128 KB, 6.1 over pages
+// of 4 KB (one moving warp with units of 32 KB: 6.3 and 3.4, its issuing lane
+// is the limit; blocks of 256 threads that load and store 16 KB: 5.7 over
+// large pages).
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv kv, const int* src, const int* dst,
                                                                   const int* rows, const int* count, int n, int check,
                                                                   const int* moved, int* status) {
-  extern __shared__ __align__(128) uint8_t s_units[];  // [kSlots][kPiece]
-  __shared__ uint64_t s_full[kSlots];
-  __shared__ unsigned long long s_to[kSlots];
-  __shared__ uint32_t s_bytes[kSlots];
-  const int lane = threadIdx.x & 31;
-  const uint32_t units = smem_u32(s_units), full = smem_u32(s_full);
+  extern __shared__ __align__(128) uint8_t s_units[];  // [kMovers][kSlots][kPiece]
+  __shared__ uint64_t s_full[kMovers * kSlots];
+  __shared__ unsigned long long s_to[kMovers * kSlots];
+  __shared__ uint32_t s_bytes[kMovers * kSlots];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < kMovers * kSlots; ++i) mbar_init(smem_u32(s_full + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int entries = count ? ld_cg(count) : n;
-  if (threadIdx.x >= 32) {
+  if (warp >= kMovers) {
     if (!moved || entries <= 0) return;
     const long long cells = (long long)kv.max_seqs * kv.max_pages;
-    constexpr int kOthers = kCopyThreads - 32;
-    for (long long c = (long long)blockIdx.x * kOthers + threadIdx.x - 32; c < cells; c += (long long)gridDim.x * kOthers) {
+    constexpr int kOthers = kCopyThreads - 32 * kMovers;
+    for (long long c = (long long)blockIdx.x * kOthers + threadIdx.x - 32 * kMovers; c < cells;
+         c += (long long)gridDim.x * kOthers) {
       const int p = ld_cg(kv.table + c);
       if (p >= 0 && p < kv.n_pages) {
         const int q = ld_cg(moved + p);
@@ -313,25 +314,31 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv kv, const i
     return;
   }
   const int pieces = (int)((kv.page_bytes + kPiece - 1) / kPiece);
-  const long long per = (long long)kv.planes * pieces, all = entries * per;
+  const long long all = (long long)entries * kv.planes * pieces;
+  const uint32_t units = smem_u32(s_units) + warp * kSlots * kPiece, full = smem_u32(s_full + warp * kSlots);
+  unsigned long long* const tos = s_to + warp * kSlots;
+  uint32_t* const sizes = s_bytes + warp * kSlots;
   int begun = 0, ended = 0;  // units asked for, units given back
   bool ok = true;
   auto end_one = [&]() {
     const int i = ended % kSlots;
     ok = wait_full(full + 8 * i, (ended / kSlots) & 1);
     if (!ok) return;
-    if (lane == 0) bulk_store(reinterpret_cast<uint8_t*>(s_to[i]), units + i * kPiece, s_bytes[i]);
+    if (lane == 0) bulk_store(reinterpret_cast<uint8_t*>(tos[i]), units + i * kPiece, sizes[i]);
     ++ended;
   };
-  for (long long w0 = blockIdx.x; ok && w0 < all; w0 += 32LL * gridDim.x) {
-    const long long w = w0 + (long long)lane * gridDim.x;
+  const int movers = gridDim.x * kMovers;
+  for (long long w0 = blockIdx.x * kMovers + warp; ok && w0 < all; w0 += 32LL * movers) {
+    const long long w = w0 + (long long)lane * movers;
     unsigned long long from = 0, to = 0;
     uint32_t bytes = 0;
     if (w < all) {
-      const int i = (int)(w / per);
-      const int r = (int)(w - i * per);
-      const int plane = r / pieces;
-      const long long at = (long long)(r - plane * pieces) * kPiece;
+      // all first pieces, then all second ones: of partly filled pages the later
+      // ones are empty, and a grid that the pieces divide would give them all to
+      // the same CTAs (96 forks: 52 us that way, 50 this way)
+      const long long r = w / kv.planes;
+      const int plane = (int)(w - r * kv.planes), piece = (int)(r / entries), i = (int)(r - (long long)piece * entries);
+      const long long at = (long long)piece * kPiece;
       const int a = ld_cg(src + i), b = ld_cg(dst + i);
       const long long most = rows ? (long long)ld_cg(rows + i) * kv.row_bytes : kv.page_bytes;
       if (check && (a < 0 || a >= kv.n_pages || b < 0 || b >= kv.n_pages)) {
@@ -352,8 +359,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv kv, const i
         // of the begun - kAhead writes so far all but the last few have let go
         // of their slots: the one of unit begun - kSlots is among them
         asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kSlots - kAhead - 1) : "memory");
-        s_to[i] = q;
-        s_bytes[i] = size;
+        tos[i] = q;
+        sizes[i] = size;
         mbar_expect_tx(full + 8 * i, size);
         bulk_load(units + i * kPiece, p, size, full + 8 * i);
       }
@@ -691,10 +698,11 @@ __global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const int* pare
 
 cudaError_t launch_copy(const Kv& kv, long long entries, const int* src, const int* dst, const int* rows,
                         const int* count, int n, int check, const int* moved, int* status, cudaStream_t s) {
-  const int smem = kSlots * kPiece;
+  const int smem = kMovers * kSlots * kPiece;
   const cudaError_t err = cudaFuncSetAttribute(copy_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   const long long units = entries * kv.planes * ((kv.page_bytes + kPiece - 1) / kPiece), most = num_sms();
+  // (few units: a CTA for each, so that they are in flight all over the GPU)
   const int grid = (int)(units < 1 ? 1 : units < most ? units : most);
   return launch_pdl(copy_pages_kernel, dim3(grid), dim3(kCopyThreads), smem, s, kv, src, dst, rows, count, n, check,
                     moved, status);
