@@ -41,8 +41,8 @@
 // 8192 tokens, 32 query and 8 kv heads of 128: 362 us, 1520 TFLOP/s counting
 // what the causal mask leaves, 80% of a large matrix product's rate); of decode
 // batches the reads of the cache (32 streams over 500..6000 keys, 8 kv heads:
-// 83 us, 5.4 TB/s); of single short calls the chain from the plan over the
-// first loads, S, P and O to the store (12.5 us, launch and all).
+// 81 us, 5.5 TB/s); of single short calls the chain from the plan over the
+// first loads, S, P and O to the store (12 us, launch and all).
 #include <cstdint>
 
 #include <cuda.h>
