@@ -63,6 +63,7 @@ constexpr int kTile = 128;       // query rows of a tile, keys of a block
 constexpr int kThreads = 384;
 constexpr int kLoaders = 64;     // threads that load by cp.async
 constexpr int kPlan = 256;       // sequences whose plan is kept in shared memory, a thread each
+constexpr int kClasses = 256;    // classes that items are put in by size
 constexpr int kItems = 4;        // work items between the loader and the other roles
 constexpr int kPoisoned = 8;     // more than the items that a loader can be ahead by
 constexpr int kItemReaders = 12;  // every warp
@@ -75,8 +76,7 @@ template <int DP>
 struct Sizes {
   static constexpr int tile = kTile * DP * 2;       // bytes of 128 rows
   static constexpr int stages = DP == 128 ? 4 : 8;  // 128 KB in flight
-  static constexpr int stage = 8 * 32 * 64;         // output staging: 32 rows of 32 values for each of eight warps
-  static constexpr int smem = 2 * tile + stages * tile + stage + kHeader;
+  static constexpr int smem = 2 * tile + stages * tile + kHeader;
 };
 
 // ------------------------------- PTX helpers --------------------------------
@@ -116,16 +116,12 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-// The same box back to global memory, and the waits of the lane that issued it:
-// until shared memory has been read, until all is written.
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-               "r"(src), "r"(x), "r"(y), "r"(z)
+// 32 bytes, a whole sector.
+__device__ __forceinline__ void store32(void* to, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -367,7 +363,10 @@ __device__ __forceinline__ int items_from(const AttnArgs& a, const Planned& w, i
   if (n <= 0 || w.cut.pieces > 1 || a.mask) return w.items;
   // pair p sees the keys before nk - nq + (p + 1) * 2 * tokens_per_tile
   const int rest = (n - 1) * kTile - (w.seq.nk - w.seq.nq);
-  return w.pairs - (rest <= 0 ? 0 : min(rest / (2 * tokens_per_tile), w.pairs - 1));
+  if (rest <= 0) return w.pairs;
+  const int tokens = 2 * tokens_per_tile;
+  const int shorter = (tokens & (tokens - 1)) == 0 ? rest >> (31 - __clz(tokens)) : rest / tokens;
+  return w.pairs - min(shorter, w.pairs - 1);
 }
 
 struct __align__(16) Item {
@@ -417,21 +416,38 @@ __device__ __forceinline__ bool sees_any(const AttnArgs& a, int t, int nk, int n
   return any;
 }
 
+// What the plan leaves in shared memory.
+struct Plan {
+  union {
+    Planned seq[kPlan];                // of up to kPlan sequences
+    int group[kPlan + 1];              // of more: items before each group of 32 * per sequences
+  };
+  long long part[kPlan];               // partial rows before a sequence (or group)
+  int from[kClasses + 1];              // items of class c (2^shift blocks) and above
+  int total;                           // items for one kv head
+  int shift, classes;
+  int per;
+};
+
 // By a whole warp: this CTA's item of a round. The items stand in order of
 // falling size (number of key blocks), a kv head after the other, and are
 // dealt to the CTAs forth and back, which comes within a few per cent of the
 // best there is: 992 items of 9 ragged prompts, 992 / 152 to a CTA, end after
 // 82 steps instead of the 112 that dealing them out as they stand takes (80
-// where each CTA takes the longest that is left). With more sequences than the
-// plan holds they are dealt in the order of the call.
-__device__ __forceinline__ Item item_of(const AttnArgs& a, const Planned* s_plan, const long long* s_part, int total,
-                                        int largest, int round, int tpt) {
+// where each CTA takes the longest that is left). Counts of the sizes, made
+// once, tell the size of an item; then a pass over the sequences finds its own
+// (1600 cycles for 9 sequences, 3800 for 256; without the counts 9000, which
+// short items waited for: 256 streams over 300..1500 keys 206 us, so 179). With
+// more sequences than the plan holds the items are dealt in the order of the
+// call, and 32 sequences are read again for an item (1024 streams over
+// 300..1500 keys: 660 us, 5.9 TB/s; searched from the first one on 1870).
+__device__ __forceinline__ Item item_of(const AttnArgs& a, const Plan& plan, int round, int tpt) {
   const int lane = threadIdx.x & 31;
   Item x = {};
   // (below 2^32: an item has a row of a tile at least, or of a partial result, and both are counted in 31 bits)
   const uint32_t next = (uint32_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   // (a CTA's last round can miss it, but then no later one is left)
-  x.end = next >= (unsigned long long)total * a.heads_kv;
+  x.end = next >= (unsigned long long)plan.total * a.heads_kv;
   if (x.end) return x;
   int u = (int)(next / (uint32_t)a.heads_kv);  // item of this kv head
   const int kvh = (int)(next - (uint32_t)u * a.heads_kv);
@@ -439,53 +455,58 @@ __device__ __forceinline__ Item item_of(const AttnArgs& a, const Planned* s_plan
   Planned w;
   long long part;
   if (a.n == 1) {
-    w = s_plan[0];
+    w = plan.seq[0];
     part = 0;
   } else if (a.n <= kPlan) {
-    // the size n with (items of more than n blocks) <= u < (items of n or more)
-    auto from = [&](int n) {
-      int c = 0;
-      for (int i = lane; i < a.n; i += 32) c += items_from(a, s_plan[i], n, tpt);
-      return __reduce_add_sync(~0u, c);
-    };
-    int n = 0, above = largest + 1;
-    while (above - n > 1) {
-      const int mid = (n + above) >> 1;
-      if (from(mid) > u) n = mid;
+    // the class c with from[c + 1] <= u < from[c]
+    int c = 0, above = plan.classes;
+    while (above - c > 1) {
+      const int mid = (c + above) >> 1;
+      if (plan.from[mid] > u) c = mid;
       else above = mid;
     }
-    u -= from(n + 1);
-    // the sequence among those with items of this size
+    u -= plan.from[c + 1];
+    const int least = c << plan.shift, more_than = (c + 1) << plan.shift;
+    // the sequence among those with items of this class
     for (int i0 = 0;; i0 += 32) {
-      int more = 0, c = 0;
+      int more = 0, count = 0;
       if (i0 + lane < a.n) {
-        more = items_from(a, s_plan[i0 + lane], n + 1, tpt);
-        c = items_from(a, s_plan[i0 + lane], n, tpt) - more;
+        more = items_from(a, plan.seq[i0 + lane], more_than, tpt);
+        count = items_from(a, plan.seq[i0 + lane], least, tpt) - more;
       }
-      int sum = c;
+      const int all = __reduce_add_sync(~0u, count);
+      if (u >= all && i0 + 32 < a.n) {
+        u -= all;
+        continue;
+      }
+      int sum = count;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(~0u, sum, o);
         if (lane >= o) sum += y;
       }
       const uint32_t reach = __ballot_sync(~0u, sum > u);
-      if (reach || i0 + 32 >= a.n) {
-        const int at = reach ? __ffs(reach) - 1 : 0;
-        b = i0 + at;
-        u -= __shfl_sync(~0u, sum - c, at);
-        first = __shfl_sync(~0u, more, at);
-        break;
-      }
-      u -= __shfl_sync(~0u, sum, 31);
+      const int at = reach ? __ffs(reach) - 1 : 0;
+      b = i0 + at;
+      u -= __shfl_sync(~0u, sum - count, at);
+      first = __shfl_sync(~0u, more, at);
+      break;
     }
-    w = s_plan[b];
-    part = s_part[b];
+    w = plan.seq[b];
+    part = plan.part[b];
   } else {
-    // 32 sequences at a time
-    part = 0;
-    for (int i0 = 0;; i0 += 32) {
+    int g = 0, above = kPlan;  // the group with group[g] <= u < group[g + 1]
+    while (above - g > 1) {
+      const int mid = (g + above) >> 1;
+      if (plan.group[mid] <= u) g = mid;
+      else above = mid;
+    }
+    u -= plan.group[g];
+    part = plan.part[g];
+    // its sequences, 32 at a time
+    for (long long i0 = (long long)g * 32 * plan.per;; i0 += 32) {
       Planned mine = {};
-      if (i0 + lane < a.n) mine = plan_of(a, i0 + lane, tpt);
+      if (i0 + lane < a.n) mine = plan_of(a, (int)i0 + lane, tpt);
       int sum = mine.items;
       long long rows = part_rows_of(a, mine);
 #pragma unroll
@@ -502,7 +523,7 @@ __device__ __forceinline__ Item item_of(const AttnArgs& a, const Planned* s_plan
         const int at = reach ? __ffs(reach) - 1 : 0;
         u -= __shfl_sync(~0u, sum - mine.items, at);
         part += __shfl_sync(~0u, rows - part_rows_of(a, mine), at);
-        w = plan_of(a, i0 + at, tpt);
+        w = plan_of(a, min((int)i0 + at, a.n - 1), tpt);
         break;
       }
       u -= __shfl_sync(~0u, sum, 31);
@@ -531,12 +552,12 @@ __device__ __forceinline__ Item item_of(const AttnArgs& a, const Planned* s_plan
   return x;
 }
 
-// The tensor maps of a call (boxes of 64 columns, of the output 32).
+// The tensor maps of a call (boxes of 64 columns).
 struct Maps {
-  CUtensorMap q, k, v, out;
+  CUtensorMap q, k, v;
   int use;       // 0: the tiles are copied by cp.async
   int box;       // rows of a box of K and V
-  int store;     // query heads of a box of the output (32 rows); 0: it is not stored by TMA
+  int wide;      // the output's rows are whole sectors of 32 bytes
 };
 
 // A place in the ring of tiles and the parity of its round.
@@ -569,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     return;
   }
   const uint32_t sQ = smem_u32(smem), sKV = sQ + 2 * Sz::tile;
-  uint8_t* head = smem + (2 + kStages) * Sz::tile + Sz::stage;
+  uint8_t* head = smem + (2 + kStages) * Sz::tile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(head);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -587,16 +608,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   // after the barriers (49 of them, 392 bytes)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(head + 392);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(head + 396);
-  int* s_total = reinterpret_cast<int*>(head + 400);                       // items for one kv head
-  int* s_largest = reinterpret_cast<int*>(head + 404);                     // blocks of the largest
   volatile int* poisoned = reinterpret_cast<volatile int*>(head + 416);    // [kPoisoned]
   Item* s_item = reinterpret_cast<Item*>(head + 448);                      // [kItems]
   float* s_top = reinterpret_cast<float*>(head + 704);                     // [2][128]
-  Planned* s_plan = reinterpret_cast<Planned*>(head + 1728);               // [kPlan]
-  long long* s_part = reinterpret_cast<long long*>(head + 9920);           // [kPlan] first partial row
-  int* s_wsum = reinterpret_cast<int*>(head + 11968);                      // [warps] items, then sizes
-  long long* s_wpart = reinterpret_cast<long long*>(head + 12096);         // [warps]
-  uint8_t* s_stage = smem + (2 + kStages) * Sz::tile;
+  int* s_wsum = reinterpret_cast<int*>(head + 1728);                       // [warps] items, then sizes
+  long long* s_wpart = reinterpret_cast<long long*>(head + 1856);          // [warps]
+  Plan& plan = *reinterpret_cast<Plan*>(head + 1952);
+  static_assert(1952 % alignof(Plan) == 0 && 1952 + sizeof(Plan) <= kHeader, "the header holds it");
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   if (warp == 0) {  // a barrier or two to a lane
@@ -619,8 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 8 && maps.use && lane < (maps.store ? 4 : 3))
-    tma_prefetch(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.out);
+  if (warp == 8 && maps.use && lane < 3) tma_prefetch(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
   if (warp == 10) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols)
@@ -632,17 +649,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   pdl_trigger();
   const int group = a.group, tpt = a.tile_tokens;
   // the plan, a thread to a sequence
+  const bool kept = a.n <= kPlan;
+  const int groups = (a.n + 31) / 32, per = (groups + kPlan - 1) / kPlan;  // of more sequences
+  if (!kept) {
+    if (tid < kPlan) plan.group[tid + 1] = 0, plan.part[tid] = 0;
+    __syncthreads();
+  }
   int count = 0, size = 0;
   long long part = 0;
-  for (int b = tid; b < a.n; b += kThreads) {
-    const Planned w = plan_of(a, b, tpt);
-    if (b < kPlan) s_plan[b] = w;
+  for (int b0 = warp * 32; b0 < a.n; b0 += kThreads) {
+    Planned w = {};
+    if (b0 + lane < a.n) w = plan_of(a, b0 + lane, tpt);
+    if (kept) {
+      if (b0 + lane < a.n) plan.seq[b0 + lane] = w;
+    } else {
+      const int g = b0 / 32 / per, items = __reduce_add_sync(~0u, w.items);
+      long long rows = part_rows_of(a, w);
+      for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(~0u, rows, o);
+      if (lane == 0) {
+        atomicAdd(&plan.group[g + 1], items);
+        if (g + 1 < kPlan) atomicAdd(reinterpret_cast<unsigned long long*>(&plan.part[g + 1]), (unsigned long long)rows);
+      }
+    }
     count += w.items;
     size = max(size, w.items ? w.cut.blocks : 0);
     part += part_rows_of(a, w);
   }
-  long long p = part;  // inclusive sum of the warp's partial rows (for up to kPlan sequences)
-  if (a.part_o)
+  long long p = part;  // inclusive sum of the warp's partial rows
+  if (a.part_o && kept)
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, p, o);
       if (lane >= o) p += y;
@@ -655,22 +689,60 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     s_wpart[warp] = p;
   }
   __syncthreads();
-  if (tid < kPlan) {
-    p -= part;
-    if (a.part_o)
-      for (int x = 0; x < warp; ++x) p += s_wpart[x];
-    s_part[tid] = p;
-  }
-  if (warp == kThreads / 32 - 1) {
+  {
     const bool has = lane < kThreads / 32;
     const int all = __reduce_add_sync(~0u, has ? s_wsum[lane] : 0);
-    const int most = __reduce_max_sync(~0u, has ? s_wsum[16 + lane] : 0);
-    if (lane == 0) {
-      *s_total = all;
-      *s_largest = most;
+    const int largest = __reduce_max_sync(~0u, has ? s_wsum[16 + lane] : 0);
+    int shift = 0;
+    while ((largest >> shift) >= kClasses) ++shift;
+    if (kept && tid < kPlan) {
+      p -= part;
+      if (a.part_o)
+        for (int x = 0; x < warp; ++x) p += s_wpart[x];
+      plan.part[tid] = p;
+    }
+    const int classes = (largest >> shift) + 1;
+    if (kept && a.n > 1)  // a warp counts a class
+      for (int c = warp; c <= classes; c += kThreads / 32) {
+        int items = 0;
+        for (int i = lane; i < a.n; i += 32) items += items_from(a, plan.seq[i], c << shift, tpt);
+        items = __reduce_add_sync(~0u, items);
+        if (lane == 0) plan.from[c] = items;
+      }
+    if (tid == 0) {
+      plan.total = all;
+      plan.shift = shift;
+      plan.classes = classes;
+      plan.per = per;
+      if (!kept) plan.group[0] = 0;
     }
   }
   __syncthreads();
+  if (!kept) {
+    if (warp == (maps.use ? 9 : 8)) {  // the warp that hands out: items and rows before each group
+      int mine[kPlan / 32], sum = 0;
+      long long rows[kPlan / 32], all = 0;
+#pragma unroll
+      for (int i = 0; i < kPlan / 32; ++i) {
+        mine[i] = sum += plan.group[1 + lane * (kPlan / 32) + i];
+        rows[i] = all += plan.part[lane * (kPlan / 32) + i];
+      }
+      int before = sum;
+      long long rows_before = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, before, o);
+        const long long z = __shfl_up_sync(~0u, rows_before, o);
+        if (lane >= o) before += y, rows_before += z;
+      }
+#pragma unroll
+      for (int i = 0; i < kPlan / 32; ++i) {
+        plan.group[1 + lane * (kPlan / 32) + i] = mine[i] + before - sum;
+        plan.part[lane * (kPlan / 32) + i] = rows[i] + rows_before - all;
+      }
+    }
+    __syncwarp();
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Ctl ctl{abort_flag, a.status};
@@ -691,7 +763,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp == 8 || warp == 9) {
     // ================================ loader ================================
     const int lw = warp - 8;
-    const int largest = *s_largest;
     int round = 0;  // of items: one for each CTA
     Place<kStages> ring = {0, 0};
     Place<2> qring = {0, 0};
@@ -703,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int i = handed % kItems;
       if (!wait_bar(iempty_bar(i), ((handed / kItems) & 1) ^ 1, ctl)) return false;
       ++handed;
-      const Item x = item_of(a, s_plan, s_part, *s_total, largest, round, tpt);
+      const Item x = item_of(a, plan, round, tpt);
       if (lane == 0) {
         s_item[i] = x;
         mbar_arrive(ifull_bar(i));
@@ -822,11 +893,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
     } else if (maps.use) {
       // -------------- values that some row does not see, and tails --------------
-      // This warp also hands out the items, two ahead of the one that it cleans
-      // (never more: the ring of items would wait for this warp itself).
-      for (int i = 0; i < 2 && ok; ++i) ok = hand_out();
-      while (ok) {
-        ok = hand_out() && next_item();
+      // This warp also hands out the items, three ahead of the one that it
+      // cleans (never more: the ring of items would wait for this warp itself),
+      // the next one after the cleaning, which others wait for.
+      for (int i = 0; i < 3 && ok; ++i) ok = hand_out();
+      for (; ok; ok = ok && hand_out()) {
+        ok = next_item();
         if (!ok) break;
         const int n = it.blocks;
         if (n == 0) continue;
@@ -1239,11 +1311,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       f0 *= inv;
       f1 *= inv;
       const long long at = valid && !cut ? (long long)t_row * a.out.ts + (long long)h * a.out.hs : -1;
-      const bool by_tma = maps.store > 0 && !cut && !bad && (quad + 1) * 32 <= rows;
-      // 16-byte chunk of a row of this warp's staging rows (64-byte swizzle)
-      auto at_stage = [&](int row, int chunk) {
-        return s_stage + warp * 2048 + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-      };
       const uint32_t tO = lanes + kColO + w * 128 + c0;
 #pragma unroll 1
       for (int j = 0; j < columns; j += 32) {
@@ -1281,36 +1348,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                 __uint_as_float(o[e + 3]));
           }
-        } else if (live) {
-          // through shared memory, so that whole lines are written
-          tma_store_read();  // the last store has left the staging rows
-          __syncwarp();
+        } else if (at >= 0) {
+          uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 v;
-            v.x = pack2<kType>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
-            v.y = pack2<kType>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-            v.z = pack2<kType>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
-            v.w = pack2<kType>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
-            *reinterpret_cast<uint4*>(at_stage(lane, e / 8)) = v;
-          }
-          if (by_tma) {
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (elect_one())
-              tma_store(&maps.out, smem_u32(s_stage) + warp * 2048, column, it.kvh * group + (quad * 32) % group,
-                        it.first + w * tpt + quad * 32 / group);
+          for (int e = 0; e < 16; ++e)
+            v[e] = pack2<kType>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          // a thread has a row: 32 bytes at a time are whole sectors, and nothing
+          // is waited for (128 columns: 3350 cycles; through shared memory by TMA,
+          // 64 bytes of a row at a time, 4280; 16 rows at a time through shared
+          // memory, so that a store writes whole lines: slower too, 200 short
+          // prompts 214 instead of 204 us)
+          uint16_t* to = a.out.p + at + column;
+          if (maps.wide) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (column + e * 16 < a.head_dim) store32(to + e * 16, v + e * 8);
           } else {
-            __syncwarp();
-            const int chunk = lane & 3;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int row = y * 8 + lane / 4;
-              const long long to = __shfl_sync(~0u, at, row);
-              if (to >= 0 && column + chunk * 8 < a.head_dim)
-                *reinterpret_cast<uint4*>(a.out.p + to + column + chunk * 8) =
-                    *reinterpret_cast<const uint4*>(at_stage(row, chunk));
-            }
+            for (int e = 0; e < 4; ++e)
+              if (column + e * 8 < a.head_dim)
+                *reinterpret_cast<uint4*>(to + e * 8) = make_uint4(v[e * 4], v[e * 4 + 1], v[e * 4 + 2], v[e * 4 + 3]);
           }
         }
       }
@@ -1364,7 +1421,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       __syncwarp();
     }
-    tma_store_done();
     // Every meeting of two warps begins with pair_any. If this one gave up
     // where the other one does not know (or the other way round), that one
     // will wait in its next meeting, or here: so they meet once more.
@@ -1457,10 +1513,10 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Boxes of 64 (or 32) columns x box_heads x box_rows of [rows, heads, head_dim]. False
+// Boxes of 64 columns x box_heads x box_rows of [rows, heads, head_dim]. False
 // where a tensor map cannot describe the tensor.
 bool make_map(CUtensorMap* map, const Heads& h, int dtype, int head_dim, int heads, long long rows, int box_heads,
-              int box_rows, int columns = 64) {
+              int box_rows) {
   const EncodeTiled encode = encode_tiled();
   if (!encode || !h.p || rows <= 0) return false;
   // a stride along one element says nothing
@@ -1469,10 +1525,10 @@ bool make_map(CUtensorMap* map, const Heads& h, int dtype, int head_dim, int hea
   if (hs == 0 || ts == 0 || hs >= (1ull << 40) || ts >= (1ull << 40)) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {hs, ts};
-  const cuuint32_t box[3] = {(cuuint32_t)columns, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   const cuuint32_t steps[3] = {1, 1, 1};
   return encode(map, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, h.p,
-                dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1488,11 +1544,8 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s) {
   const int sms = num_sms();
   Maps maps = {};
   const int group = a.heads_q / a.heads_kv;
-  // a warp's 32 rows are whole tokens or a part of one token's heads
-  const int store = min(group, 32);
-  if (32 % store == 0 && group % store == 0 &&
-      make_map(&maps.out, a.out, kType, a.head_dim, a.heads_q, a.total_q, store, 32 / store, 32))
-    maps.store = store;
+  auto whole = [](long long x) { return x % 16 == 0; };
+  maps.wide = reinterpret_cast<uintptr_t>(a.out.p) % 32 == 0 && whole(a.head_dim) && whole(a.out.ts) && whole(a.out.hs);
   const long long rows = a.paged ? (long long)a.n_pages * a.page_size : a.total_k;
   maps.box = a.paged ? min(a.page_size & -a.page_size, kTile) : kTile;  // rows of a page that lie together
   maps.use = maps.box >= 8 && make_map(&maps.q, a.q, kType, a.head_dim, a.heads_q, a.total_q, group, tpt) &&

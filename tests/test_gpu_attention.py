@@ -334,6 +334,31 @@ def test_cached_poison_among_the_drafted(cuda, poison):
     assert torch.isnan(out[[i for i in range(n) if bits[i, 18]]].float()).all()
 
 
+@pytest.mark.parametrize("n", [250, 256, 257, 600])
+def test_cached_many_sequences(cuda, n):
+    """Long ones, that are cut into pieces, among short ones, for more or fewer sequences than one plan holds."""
+    rng = np.random.RandomState(n)
+    lengths = [int(rng.randint(1024, 2200)) if x < 0.1 else int(rng.randint(1, 200)) for x in rng.rand(n)]
+    draft = [int(min(length, d)) for length, d in zip(lengths, rng.randint(0, 4, n))]
+    check_cached(lengths, draft, 2, 1, 64, 16, "bf16", seed=n)
+
+
+def test_cached_sizes_of_many_classes(cuda):
+    check_cached([33100, 40, 5000, 33000, 1], [1, 2, 40, 3, 1], 2, 1, 64, 64, "bf16", seed=9)
+
+
+def test_prompt_thousands_of_sequences(cuda):
+    rng = np.random.RandomState(1)
+    nq = (rng.randint(1, 4, 8500) * (rng.rand(8500) < 0.1)).tolist()
+    check_prompt(nq, nq, 2, 1, 64, "bf16", seed=11)
+
+
+def test_prompt_sizes_of_one_call(cuda):
+    """Many classes of sizes: prompts of 1 to 2000 tokens, with and without earlier keys."""
+    nq = [1, 2000, 17, 900, 400, 400, 33, 1200, 5, 640]
+    check_prompt(nq, [n + x for n, x in zip(nq, [0, 0, 700, 0, 300, 0, 1500, 0, 5, 0])], 4, 1, 64, "bf16", seed=12)
+
+
 def test_cached_shared_pages_and_prompt_agree(cuda):
     """A prompt written into the cache (and a fork of it) gives what the packed form gives."""
     n, heads, kv, dim = 333, 8, 2, 128
