@@ -440,7 +440,7 @@ struct Plan {
 // short items waited for: 256 streams over 300..1500 keys 206 us, so 179). With
 // more sequences than the plan holds the items are dealt in the order of the
 // call, and 32 sequences are read again for an item (1024 streams over
-// 300..1500 keys: 660 us, 5.9 TB/s; searched from the first one on 1870).
+// 300..1500 keys: 660 us, 5.7 TB/s; searched from the first one on 1870).
 __device__ __forceinline__ Item item_of(const AttnArgs& a, const Plan& plan, int round, int tpt) {
   const int lane = threadIdx.x & 31;
   Item x = {};
