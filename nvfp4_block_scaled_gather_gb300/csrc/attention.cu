@@ -158,6 +158,14 @@ __device__ __forceinline__ bool elect_one() {
 // warp has to execute these together: a __syncwarp() stands before them where
 // lanes may have gone separate ways, which also keeps the compiler from pulling
 // a lane's condition out of a loop around them.
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -1313,63 +1321,60 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const long long at = valid && !cut ? (long long)t_row * a.out.ts + (long long)h * a.out.hs : -1;
       const uint32_t tO = lanes + kColO + w * 128 + c0;
 #pragma unroll 1
-      for (int j = 0; j < columns; j += 32) {
-        uint32_t o[32];
+      for (int j = 0; j < columns; j += 16) {
+        uint32_t o[16];
         __syncwarp();
         if (n > 0 && live) {
-          tc_ld32(tO + j, o);
+          tc_ld16(tO + j, o);
           tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
           if (other) {
-            uint32_t o1[32];
-            tc_ld32(tO + 128 + j, o1);
+            uint32_t o1[16];
+            tc_ld16(tO + 128 + j, o1);
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
               o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (n > 0 && j + 32 >= columns) {  // O has been read
-          tc_fence_before();
-          warp_arrive(oempty_bar(w), lane);
-          if (other) warp_arrive(oempty_bar(1), lane);
+          for (int e = 0; e < 16; ++e) o[e] = 0u;
         }
         const int column = c0 + j;
+        if (column >= a.head_dim) continue;
         if (cut) {
           if (keep) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
+            for (int e = 0; e < 16; e += 4)
               if (column + e < a.head_dim)
                 *reinterpret_cast<float4*>(part_o + (column + e) * eight) =
                     make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                 __uint_as_float(o[e + 3]));
           }
         } else if (at >= 0) {
-          uint32_t v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            v[e] = pack2<kType>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
           // a thread has a row: 32 bytes at a time are whole sectors, and nothing
-          // is waited for (128 columns: 3350 cycles; through shared memory by TMA,
-          // 64 bytes of a row at a time, 4280; 16 rows at a time through shared
-          // memory, so that a store writes whole lines: slower too, 200 short
-          // prompts 214 instead of 204 us)
+          // is waited for. 200 short prompts take 197 us so; with 32 columns of
+          // the loop at a time (more code to fetch for every item) 205, by TMA
+          // from shared memory about 210, and through shared memory, so that a
+          // store writes whole lines, 208 to 214.
+          uint32_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = pack2<kType>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
           uint16_t* to = a.out.p + at + column;
           if (maps.wide) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (column + e * 16 < a.head_dim) store32(to + e * 16, v + e * 8);
+            store32(to, v);
           } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (column + e * 8 < a.head_dim)
-                *reinterpret_cast<uint4*>(to + e * 8) = make_uint4(v[e * 4], v[e * 4 + 1], v[e * 4 + 2], v[e * 4 + 3]);
+            *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+            if (column + 8 < a.head_dim) *reinterpret_cast<uint4*>(to + 8) = make_uint4(v[4], v[5], v[6], v[7]);
           }
         }
+      }
+      if (n > 0) {  // O has been read
+        tc_fence_before();
+        warp_arrive(oempty_bar(w), lane);
+        if (other) warp_arrive(oempty_bar(1), lane);
       }
       __syncwarp();
       if (n > 0) {
