@@ -132,6 +132,22 @@ def test_forks_share_pages_until_they_grow(cuda):
     assert not any(b.model.refs)
 
 
+@pytest.mark.parametrize("page,kv,dim", [(64, 8, 128), (37, 3, 120), (5, 16, 128)])
+def test_copies_of_large_pages(cuda, page, kv, dim):
+    """Pages of several units of copying (128 KB), of one and a half, and of a little more than one; part of them in use."""
+    b = Both(90, page, 40, 8, kv=kv, dim=dim)
+    b.grow([0, 30], [2 * page + page // 2, page + 1])
+    b.fork([0] * 20, list(range(1, 21)))
+    b.grow(list(range(1, 21)), [1 + i % 3 for i in range(20)])
+    b.fork([30, 30], [31, 32])
+    b.grow([32, 30, 31], [page, 1, 2])
+    b.truncate([0, 3, 7, 30], [0, 0, page + 1, 0])
+    b.compact()
+    b.keep([5, 31], [2, 1], [[1], []])
+    b.truncate(list(range(1, 21)), [0] * 20)
+    b.compact()
+
+
 def test_forks_of_empty_and_whole_page_sequences(cuda):
     b = Both(20, 4, 6, 5)
     b.grow([0], [8])
