@@ -18,7 +18,9 @@
  * heads_kv)):
  *   s_ij = scale * sum_d q[i, d] k[j, d]       over the keys j that i sees
  *   out[i] = sum_j exp(s_ij - lse_i) v[j],     lse_i = log sum_j exp(s_ij)
- * A query that sees no key gives out = 0 and lse = -inf. Keys and values that
+ * A query that sees no key gives out = 0 and lse = -inf; so do all queries of
+ * a sequence whose id, length (past max_pages pages) or a page id within its
+ * length is out of range (MOE_ERR_INVALID). Keys and values that
  * a query does not see have no influence on it, NaN and infinities included.
  * Scores, the running maximum and sum, and the sum over the values are held
  * in fp32.

@@ -34,6 +34,9 @@
 //    values there that are not finite are zeroed before the MMA (0 * NaN would
 //    reach rows that do not see them); the rows that do see them get them
 //    added at the end.
+//  * Pages whose id is out of range are not loaded: their rows of a tile hold
+//    what was there before, and every item that meets one gives its rows no
+//    result (0 and -inf; so do the other pieces of a cut sequence, by the join).
 //  * Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT,
 //    drains its copies and MMAs, frees tensor memory and returns.
 //
@@ -66,11 +69,13 @@ constexpr int kPlan = 256;       // sequences whose plan is kept in shared memor
 constexpr int kClasses = 256;    // classes that items are put in by size
 constexpr int kItems = 4;        // work items between the loader and the other roles
 constexpr int kPoisoned = 8;     // more than the items that a loader can be ahead by
+constexpr int kNoKey = -1, kNoPage = -2;  // for a key's row: past the sequence's end, in no page of the pool
 constexpr int kItemReaders = 12;  // every warp
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // the two S (P goes over it) and the two O, 128 columns each
 constexpr int kHeader = 16384;
 constexpr float kLazy = 8.0f;    // powers of two that a score may exceed the running maximum by
+constexpr float kUndone = -1.0f;  // in place of a piece's sum: the sequence has a bad page
 
 template <int DP>
 struct Sizes {
@@ -560,6 +565,19 @@ __device__ __forceinline__ Item item_of(const AttnArgs& a, const Plan& plan, int
   return x;
 }
 
+// By a whole warp: whether any of the page ids first .. last of a row of the
+// table is out of range. Rarely needed, and kept out of line: within the
+// loader's code it made decode_one 13.8 us instead of 12.6 and trees of 16
+// streams 48.7 instead of 41.2, where it never runs.
+__device__ __noinline__ bool any_bad(const int* row, int first, int last, int n_pages) {
+  bool bad = false;
+  for (int at = first + (threadIdx.x & 31); at <= last; at += 32) {
+    const int p = ld_cg(row + at);
+    bad |= p < 0 || p >= n_pages;
+  }
+  return __any_sync(~0u, bad);
+}
+
 // The tensor maps of a call (boxes of 64 columns).
 struct Maps {
   CUtensorMap q, k, v;
@@ -621,8 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   float* s_top = reinterpret_cast<float*>(head + 704);                     // [2][128]
   int* s_wsum = reinterpret_cast<int*>(head + 1728);                       // [warps] items, then sizes
   long long* s_wpart = reinterpret_cast<long long*>(head + 1856);          // [warps]
-  Plan& plan = *reinterpret_cast<Plan*>(head + 1952);
-  static_assert(1952 % alignof(Plan) == 0 && 1952 + sizeof(Plan) <= kHeader, "the header holds it");
+  volatile int* undone = reinterpret_cast<volatile int*>(head + 1952);     // [kPoisoned]
+  Plan& plan = *reinterpret_cast<Plan*>(head + 1984);
+  static_assert(1984 % alignof(Plan) == 0 && 1984 + sizeof(Plan) <= kHeader, "the header holds it");
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   if (warp == 0) {  // a barrier or two to a lane
@@ -640,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       return 1;                                          // landed values, drains
     };
     for (int i = lane; i < 49; i += 32) mbar_init(bar0 + 8u * i, arrivals(i));
-    if (lane < kPoisoned) poisoned[lane] = 0;
+    if (lane < kPoisoned) poisoned[lane] = undone[lane] = 0;
     if (lane == 0) *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -790,18 +809,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       ++round;
       return true;
     };
-    // Row of the packed keys or of the cache's planes that holds key `pos`, or
-    // -1 (no such key, or a page id out of range).
+    // Row of the packed keys or of the cache's planes that holds key `pos`, or kNoKey or kNoPage.
     auto row_of = [&](int pos) -> int {
-      if (pos >= it.nk) return -1;
+      if (pos >= it.nk) return kNoKey;
       if (!a.paged) return it.k0 + pos;
       const int at = pos / a.page_size;
       const int p = ld_cg(a.table + (long long)it.k0 * a.max_pages + at);
       if (p < 0 || p >= a.n_pages) {
         report(a.status, MOE_ERR_INVALID);
-        return -1;
+        return kNoPage;
       }
       return p * a.page_size + (pos - at * a.page_size);
+    };
+    // Pages that none of the item's rows sees (a chain: its earlier rows do not
+    // see the last pages). The piece that has the last key that the rows see
+    // looks at the pages behind it before its first block, so that all rows of a
+    // sequence agree on its pages.
+    auto check_unseen_pages = [&]() {
+      const int end = (it.b0 + it.blocks) * kTile;
+      if (a.paged && !a.mask && end < it.nk && limit_of(a, it.nk, it.nq, it.i0 + it.tokens - 1) <= end &&
+          any_bad(a.table + (long long)it.k0 * a.max_pages, end / a.page_size, (it.nk - 1) / a.page_size, a.n_pages)) {
+        if (lane == 0) {
+          report(a.status, MOE_ERR_INVALID);
+          undone[(seq_no - 1) % kPoisoned] = seq_no;
+        }
+        __syncwarp();
+      }
     };
     // 16-byte chunk c of row r of a tile.
     auto chunk_at = [](uint32_t tile, int r, int c) -> uint32_t {
@@ -828,14 +861,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       while (ok) {
         ok = next_item();
         if (!ok) break;
-        const int n = __shfl_sync(~0u, it.blocks, 0);
+        const int n = __shfl_sync(~0u, it.blocks, 0), item_no = seq_no - 1;
         if (n == 0) continue;
         const int lim = limit_of(a, it.nk, it.nq, it.i0);  // the least that any row of the pair sees
         // keys that no other item reads leave L2 first (to partial results, for one)
         const uint64_t policy = it.nq <= 2 * tpt ? once : normal;
         // lane i: row of box i of the block
         const int first = it.b0 * kTile + lane * maps.box;
-        int row = lane < boxes ? row_of(first) : -1;
+        int row = lane < boxes ? row_of(first) : kNoKey;
         for (int q = 0; q < 1 + it.two && ok; ++q) {
           ok = wait_bar(qempty_bar(qring.slot), qring.parity ^ 1, ctl);
           if (ok && elect_one()) {
@@ -852,10 +885,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
           qring.step(1);
         }
+        check_unseen_pages();
         for (int b = 0; b < n && ok; ++b) {
           const int end = (it.b0 + b + 1) * kTile;
           const uint32_t there = __ballot_sync(~0u, row >= 0);
-          const int nrow = lane < boxes && b + 1 < n ? row_of(first + (b + 1) * kTile) : -1;
+          if (__any_sync(~0u, row == kNoPage)) {
+            if (lane == 0) undone[item_no % kPoisoned] = item_no + 1;
+            __syncwarp();
+          }
+          const int nrow = lane < boxes && b + 1 < n ? row_of(first + (b + 1) * kTile) : kNoKey;
           const uint32_t bytes = (uint32_t)__popc(there) * box_bytes * (DP / 64);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
@@ -985,11 +1023,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const int lim = limit_of(a, it.nk, it.nq, it.i0);
         auto rows_of = [&](int block) {
           const int pos = (it.b0 + block) * kTile + lw * 64 + lane;
-          return block < n ? make_int2(row_of(pos), row_of(pos + 32)) : make_int2(-1, -1);
+          return block < n ? make_int2(row_of(pos), row_of(pos + 32)) : make_int2(kNoKey, kNoKey);
         };
         int2 rows = rows_of(0);
+        if (lw == 0) check_unseen_pages();
         for (int b = 0; b < n && ok; ++b) {
           const int2 later = rows_of(b + 1);
+          if (rows.x == kNoPage || rows.y == kNoPage) {
+            undone[item_no % kPoisoned] = item_no + 1;
+            __threadfence_block();  // before this thread's arrival, which the copies make
+          }
           const bool edge = (it.b0 + b + 1) * kTile > lim && lim < it.nk;
           for (int v = 0; v < 2; ++v) {
             const Heads& x = v ? a.v : a.k;
@@ -1298,8 +1341,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (!ok) break;
         tc_fence_after();
       }
-      // (O is complete, so every block's values have been through the cleaning)
-      const bool bad = n > 0 && poisoned[(seq_no - 1) % kPoisoned] == seq_no;
+      // (O is complete, so every block has been through the loads and the cleaning)
+      const bool gone = n > 0 && undone[(seq_no - 1) % kPoisoned] == seq_no;  // a page of the sequence's is bad
+      const bool bad = n > 0 && !gone && poisoned[(seq_no - 1) % kPoisoned] == seq_no;
+      if (gone) l = 0.0f;
       const int h = it.kvh * group + head_in;
       const int i = it.i0 + w * tpt + token, t_row = it.first + w * tpt + token;
       // rows of a cut sequence are kept a kv head after the other; eight of a
@@ -1314,7 +1359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       float inv = 1.0f;
       if (!cut) {
         inv = rcp_approx(l);
-        if (l == 0.0f) inv = valid && sees_any(a, t_row, it.nk, it.nq, limit_of(a, it.nk, it.nq, i)) ? NAN : 0.0f;
+        if (l == 0.0f) inv = valid && !gone && sees_any(a, t_row, it.nk, it.nq, limit_of(a, it.nk, it.nq, i)) ? NAN : 0.0f;
       }
       f0 *= inv;
       f1 *= inv;
@@ -1324,7 +1369,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int j = 0; j < columns; j += 16) {
         uint32_t o[16];
         __syncwarp();
-        if (n > 0 && live) {
+        if (n > 0 && live && !gone) {
           tc_ld16(tO + j, o);
           tc_wait_ld();
 #pragma unroll
@@ -1412,7 +1457,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (valid && (two || half == 0)) {
         const int row = t_row * a.heads_q + h;
         if (cut) {
-          if (keep) a.part_ml[part + r] = make_float2(m * c, l);
+          if (keep) a.part_ml[part + r] = make_float2(m * c, gone ? kUndone : l);
           else report(a.status, MOE_ERR_INVALID);
           if (it.piece == 0) {
             const bool any = sees_any(a, t_row, it.nk, it.nq, limit_of(a, it.nk, it.nq, i));
@@ -1470,6 +1515,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
   const float* from = a.part_o + ((long long)of.x + (r & ~7)) * a.head_dim + (r & 7) * 4 + q * 4 * eight;
   const float2* ml = a.part_ml + of.x + r;
   float top = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  bool undone = false;
 #pragma unroll 1
   for (int i0 = 0; i0 < pieces; i0 += kSplitFew) {
     float4 v[kSplitFew];
@@ -1483,6 +1529,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
 #pragma unroll
     for (int u = 0; u < kSplitFew; ++u) {
       const float m = __uint_as_float(x[u].x), sum = __uint_as_float(x[u].y);
+      undone |= sum == kUndone;
       if (i0 + u < pieces && sum != 0.0f) {  // a sum of 0: the piece saw nothing
         const float now = fmaxf(top, m);
         const float keep = now == top ? 1.0f : ex2(top - now), f = now == m || m == -INFINITY ? 1.0f : ex2(m - now);
@@ -1495,7 +1542,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
       }
     }
   }
-  const float inv = l != 0.0f ? rcp_approx(l) : ((of.y >> 16) & 1 ? NAN : 0.0f);
+  if (undone) l = o[0] = o[1] = o[2] = o[3] = 0.0f;
+  const float inv = undone ? 0.0f : l != 0.0f ? rcp_approx(l) : ((of.y >> 16) & 1 ? NAN : 0.0f);
   const int t = of.w / a.heads_q, h = of.w - t * a.heads_q;
   *reinterpret_cast<uint2*>(a.out.p + (long long)t * a.out.ts + (long long)h * a.out.hs + q * 4) =
       make_uint2(pack2<kType>(o[0] * inv, o[1] * inv), pack2<kType>(o[2] * inv, o[3] * inv));
