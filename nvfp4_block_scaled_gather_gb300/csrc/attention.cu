@@ -326,10 +326,15 @@ struct Seq {
   int k0, nk;      // keys: first packed row or row of the table, count
 };
 
+// Rows first .. end - 1 within total: how many (0 where they run backwards; no
+// difference of offsets that could pass 32 bits is taken).
+__device__ __forceinline__ int rows_between(int first, int end, int total) {
+  return max(min(end, total), first) - first;
+}
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   Seq s;
   s.first = max(ld_cg(a.cu_q + b), 0);
-  s.nq = max(min(ld_cg(a.cu_q + b + 1), a.total_q) - s.first, 0);
+  s.nq = rows_between(s.first, ld_cg(a.cu_q + b + 1), a.total_q);
   s.nk = 0;
   if (a.paged) {
     s.k0 = ld_cg(a.seqs + b);
@@ -345,7 +350,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
     }
   } else {
     s.k0 = max(ld_cg(a.cu_k + b), 0);
-    s.nk = max(min(ld_cg(a.cu_k + b + 1), a.total_k) - s.k0, 0);
+    s.nk = rows_between(s.k0, ld_cg(a.cu_k + b + 1), a.total_k);
   }
   return s;
 }

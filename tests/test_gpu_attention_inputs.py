@@ -5,10 +5,13 @@ import pytest
 import torch
 
 from nvfp4_block_scaled_gather_gb300 import _native as N
-from tests.test_gpu_attention import ints, make_cache, normal, run_cached, starts
+from nvfp4_block_scaled_gather_gb300 import attention as A
+from oracle import attention as OA
+from tests.test_gpu_attention import hold, ints, make_cache, normal, run_cached, starts
 
 pytestmark = pytest.mark.gpu
 INVALID = 1
+LEAST, MOST = -2 ** 31, 2 ** 31 - 1
 
 
 # (length, drafted): one tile, pieces that are joined, several pairs of tiles, and pairs that do not see the last pieces
@@ -54,3 +57,51 @@ def test_cached_bad_page_ids_under_a_mask(cuda, page):
         assert N.check_status() == INVALID
         assert (out[7:] == 0).all() and (lse[7:] == -np.inf).all() and torch.equal(out[:7], good[:7])
         cache.table[1, at] = page_id
+
+
+def guarded(q, k, v, cu_q, cu_k):
+    """Prompt attention into the middle of larger tensors: results, after the rows around them were found untouched."""
+    n, heads, dim = q.shape
+    out = torch.full((n + 64, heads, dim), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((n + 64, heads), 7.0, dtype=torch.float32, device="cuda")
+    A.moe_attention_prompt(q, k, v, ints(cu_q), ints(cu_k), out[32:32 + n], lse=lse[32:32 + n])
+    torch.cuda.synchronize()
+    assert N.check_status() == 0
+    for x in (out, lse):
+        assert (x[:32] == 7).all() and (x[32 + n:] == 7).all()
+    return out[32:32 + n], lse[32:32 + n]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_offsets_are_cut_to_the_tensors(cuda, dim):
+    """(rows, keys) of each sequence, from offsets that lie outside the tensors, run backwards or differ by more than
+    32 bits hold. Rows of no sequence are left alone."""
+    q, k, v = normal((40, 2, dim), "bf16", 33), normal((40, 2, dim), "bf16", 34), normal((40, 2, dim), "bf16", 35)
+    none = (0, 0)
+    for cu_q, cu_k, want in (
+            ([-5, 10, 1000], [0, 20, 30], [((0, 10), (0, 20)), ((10, 40), (20, 30))]),
+            ([0, 20, 1000], [0, 500, 30], [((0, 20), (0, 40)), ((20, 40), none)]),
+            ([5, LEAST], [0, 40], []),
+            ([MOST, LEAST], [0, 40], []),
+            ([MOST, 12], [0, 40], []),
+            ([30, 4, 4], [0, 10, 40], []),
+            ([0, 40], [7, LEAST], [((0, 40), none)]),
+            ([0, 40], [MOST, LEAST], [((0, 40), none)]),
+            ([0, 15, 40], [MOST, 7, LEAST], [((0, 15), none), ((15, 40), none)]),
+            ([LEAST, MOST], [LEAST, MOST], [((0, 40), (0, 40))])):
+        out, lse = guarded(q, k, v, cu_q, cu_k)
+        mine = torch.zeros(40, dtype=torch.bool, device="cuda")
+        for (a, b), (c, d) in want:
+            mine[a:b] = True
+            hold(out[a:b], lse[a:b], q[a:b], k[c:d], v[c:d], OA.chain(b - a, d - c), dim ** -0.5, "bf16")
+        assert (out[~mine] == 7).all() and (lse[~mine] == 7).all()
+
+
+def test_cached_offsets_are_cut_to_the_tensors(cuda):
+    cache = make_cache([2000, 300], 2, 64, 16, "bf16", 36)
+    q = normal((30, 4, 64), "bf16", 37)
+    whole, whole_lse = run_cached(q, cache, 0, ints([0]), ints([0, 30]))
+    for cu, rows in (([5, LEAST], 0), ([MOST, LEAST], 0), ([LEAST, MOST], 30), ([-1, 31], 30)):
+        out, lse = run_cached(q, cache, 0, ints([0]), ints(cu))
+        assert torch.equal(out[:rows], whole[:rows]) and torch.equal(lse[:rows], whole_lse[:rows])
+        assert (out[rows:] == 7).all() and (lse[rows:] == 7).all() and N.check_status() == 0
