@@ -645,11 +645,12 @@ __global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const int* pare
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  const int first = ld_cg(cu + blockIdx.x), end = min(ld_cg(cu + blockIdx.x + 1), total), m = end - first;
-  if (first < 0 || m <= 0) {
+  const int first = ld_cg(cu + blockIdx.x), end = min(ld_cg(cu + blockIdx.x + 1), total);
+  if (first < 0 || end <= first) {
     if (first < 0 && tid == 0) report(status, MOE_ERR_INVALID);
     return;
   }
+  const int m = end - first;
   const int* from = parents + first;
   int* rows = mask + (long long)first * words;
   if (m > 32LL * words) {

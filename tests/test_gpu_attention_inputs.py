@@ -105,3 +105,13 @@ def test_cached_offsets_are_cut_to_the_tensors(cuda):
         out, lse = run_cached(q, cache, 0, ints([0]), ints(cu))
         assert torch.equal(out[:rows], whole[:rows]) and torch.equal(lse[:rows], whole_lse[:rows])
         assert (out[rows:] == 7).all() and (lse[rows:] == 7).all() and N.check_status() == 0
+
+
+@pytest.mark.parametrize("cu,status", [([3, LEAST], 0), ([MOST, LEAST], 0), ([MOST, 2], 0), ([6, 2], 0), ([LEAST, 6], INVALID),
+                                       ([LEAST, MOST], INVALID)])
+def test_tree_mask_offsets_that_hold_no_tokens(cuda, cu, status):
+    parents = torch.full((64 + 6 + 64,), -1, dtype=torch.int32, device="cuda")[64:70]
+    mask = torch.full((64 + 6 + 64, 1), 77, dtype=torch.int32, device="cuda")
+    A.moe_tree_mask(parents, ints(cu), mask[64:70])
+    torch.cuda.synchronize()
+    assert N.check_status() == status and (mask == 77).all()
