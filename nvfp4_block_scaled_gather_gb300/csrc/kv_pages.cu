@@ -536,12 +536,16 @@ __global__ void __launch_bounds__(128) truncate_kernel(Kv kv, const int* seqs, c
   const int s = ld_cg(seqs + i), to = ld_cg(new_len + i);
   bool bad = s < 0 || s >= kv.max_seqs || to < 0;
   for (int j = threadIdx.x; j < i; j += 128) bad |= ld_cg(seqs + j) == s;  // repeats: the first one counts
+  int length = 0, held = 0;
+  if (!bad) {
+    length = min(ld_cg(kv.length + s), to);
+    held = min(ld_cg(kv.held + s), kv.max_pages);
+    bad = length < 0 || held < 0;  // of no sequence: its columns would lie before the table's row
+  }
   if (__syncthreads_or(bad ? 1 : 0)) {
     if (threadIdx.x == 0) report(status, MOE_ERR_INVALID);
     return;
   }
-  const int length = min(ld_cg(kv.length + s), to);
-  const int held = min(ld_cg(kv.held + s), kv.max_pages);
   const int stay = min(ceil_div(length, kv.page_size), held);
   for (int c = stay + threadIdx.x; c < held; c += 128) {
     int* cell = kv.table + (long long)s * kv.max_pages + c;
@@ -581,8 +585,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(Kv kv, const int* se
   };
   if (!bad) {
     length = ld_cg(kv.length + s);
-    start = length - m;
-    bad = start < 0 || ceil_div(length, kv.page_size) > kv.max_pages;
+    bad = length < m || ceil_div(length, kv.page_size) > kv.max_pages;  // (m >= 0, so no length below 0 passes)
+    start = bad ? 0 : length - m;
   }
   if (!bad) {
     for (int j = tid; j < k; j += kKeepThreads) {

@@ -1,0 +1,40 @@
+"""Upkeep of the paged cache at its limits: state that only the device can see
+to be wrong, requests that no pool can serve, long lists."""
+import pytest
+import torch
+
+from nvfp4_block_scaled_gather_gb300 import _native as N
+from nvfp4_block_scaled_gather_gb300 import attention as A
+
+pytestmark = pytest.mark.gpu
+INVALID = 1
+LEAST = -2 ** 31
+
+
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("length,held", [(-1, 2), (-100, 2), (LEAST, 2), (LEAST, LEAST), (20, -1), (-3, -3)])
+def test_counts_below_zero_are_reported_and_not_followed(cuda, length, held):
+    """A sequence whose counts are of no sequence is left alone by all upkeep, and so is what lies around its rows."""
+    cache = A.KVCache.empty(1, 12, 16, 1, 8, 4, 3)
+    ws = A.pages_workspace(cache)
+    A.moe_kv_extend(cache, ints([0, 1, 2, 3]), ints([40, 20, 33, 5]), ws)
+    cache.pages.copy_(torch.randn_like(cache.pages))
+    assert N.check_status() == 0
+    cache.length[1], cache.held[1] = length, held
+    state = (cache.table, cache.length, cache.held, cache.refs, cache.pages)
+    before = [t.clone() for t in state]
+    one, rows = ints([1]), torch.randn((1, 1, 8), device="cuda").bfloat16()
+    for name, call in (("truncate", lambda: A.moe_kv_truncate(cache, one, ints([0]))),
+                       ("cut", lambda: A.moe_kv_truncate(cache, one, ints([7]))),
+                       ("keep", lambda: A.moe_kv_keep(cache, one, ints([1]), ints([[0]]), ints([1]), ws)),
+                       ("keep none", lambda: A.moe_kv_keep(cache, one, ints([2]), ints([[0]]), ints([0]), ws)),
+                       ("append", lambda: A.moe_kv_append(cache, 0, one, ints([0, 1]), rows, rows)),
+                       ("extend", lambda: A.moe_kv_extend(cache, one, ints([1]), ws))):
+        if name.startswith(("append", "keep")) and length >= 0:
+            continue  # these go by the length and the table alone
+        call()
+        assert N.check_status() == INVALID, name
+        assert all(torch.equal(a, b) for a, b in zip(state, before)), name
