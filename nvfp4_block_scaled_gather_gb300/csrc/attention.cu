@@ -462,7 +462,8 @@ struct Plan {
 __device__ __forceinline__ Item item_of(const AttnArgs& a, const Plan& plan, int round, int tpt) {
   const int lane = threadIdx.x & 31;
   Item x = {};
-  // (below 2^32: an item has a row of a tile at least, or of a partial result, and both are counted in 31 bits)
+  // (below 2^32: an item has a row of a tile at least, or of a partial result, and both are counted in 31 bits; up to
+  // kPlan sequences may share rows: each has less than 2^23 items)
   const uint32_t next = (uint32_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   // (a CTA's last round can miss it, but then no later one is left)
   x.end = next >= (unsigned long long)plan.total * a.heads_kv;
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   Item* s_item = reinterpret_cast<Item*>(head + 448);                      // [kItems]
   float* s_top = reinterpret_cast<float*>(head + 704);                     // [2][128]
   int* s_wsum = reinterpret_cast<int*>(head + 1728);                       // [warps] items, then sizes
-  long long* s_wpart = reinterpret_cast<long long*>(head + 1856);          // [warps]
+  long long* s_wpart = reinterpret_cast<long long*>(head + 1856);          // [warps] partial rows; of many sequences, queries
   volatile int* undone = reinterpret_cast<volatile int*>(head + 1952);     // [kPoisoned]
   Plan& plan = *reinterpret_cast<Plan*>(head + 1984);
   static_assert(1984 % alignof(Plan) == 0 && 1984 + sizeof(Plan) <= kHeader, "the header holds it");
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __syncthreads();
   }
   int count = 0, size = 0;
-  long long part = 0;
+  long long part = 0, many = 0;
   for (int b0 = warp * 32; b0 < a.n; b0 += kThreads) {
     Planned w = {};
     if (b0 + lane < a.n) w = plan_of(a, b0 + lane, tpt);
@@ -696,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (b0 + lane < a.n) plan.seq[b0 + lane] = w;
     } else {
       const int g = b0 / 32 / per, items = __reduce_add_sync(~0u, w.items);
+      many += w.seq.nq;
       long long rows = part_rows_of(a, w);
       for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(~0u, rows, o);
       if (lane == 0) {
@@ -713,17 +715,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const long long y = __shfl_up_sync(~0u, p, o);
       if (lane >= o) p += y;
     }
+  if (!kept)
+    for (int o = 16; o > 0; o >>= 1) many += __shfl_xor_sync(~0u, many, o);
   count = __reduce_add_sync(~0u, count);
   size = __reduce_max_sync(~0u, size);
   if (lane == 31) {
     s_wsum[warp] = count;
     s_wsum[16 + warp] = size;
-    s_wpart[warp] = p;
+    s_wpart[warp] = kept ? p : many;
   }
   __syncthreads();
   {
     const bool has = lane < kThreads / 32;
-    const int all = __reduce_add_sync(~0u, has ? s_wsum[lane] : 0);
+    int all = __reduce_add_sync(~0u, has ? s_wsum[lane] : 0);
+    if (!kept) {
+      // Offsets that go back and forth give a row to several sequences, and of
+      // thousands of sequences that can make more items than 32 bits count:
+      // where the sequences have more queries than there are, nothing is done.
+      long long queries = 0;
+      for (int x = 0; x < kThreads / 32; ++x) queries += s_wpart[x];
+      if (queries > a.total_q) {
+        all = 0;
+        if (tid == 0) report(a.status, MOE_ERR_INVALID);
+        if (a.part_of)  // the join finds no rows
+          for (long long i = (long long)blockIdx.x * kThreads + tid; i < (long long)a.total_q * a.heads_q;
+               i += (long long)gridDim.x * kThreads)
+            a.part_of[i] = make_int4(-1, 0, 0, 0);
+      }
+    }
     const int largest = __reduce_max_sync(~0u, has ? s_wsum[16 + lane] : 0);
     int shift = 0;
     while ((largest >> shift) >= kClasses) ++shift;

@@ -115,3 +115,24 @@ def test_tree_mask_offsets_that_hold_no_tokens(cuda, cu, status):
     A.moe_tree_mask(parents, ints(cu), mask[64:70])
     torch.cuda.synchronize()
     assert N.check_status() == status and (mask == 77).all()
+
+
+def test_offsets_that_give_every_row_to_thousands_of_sequences(cuda):
+    """2^19 pairs of one-token tiles for each of 10000 sequences: more items than 32 bits count. Nothing is done."""
+    total, n = 1 << 20, 20001
+    x = torch.zeros((total, 128, 8), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(x, 7.0)
+    cu = torch.zeros(n, dtype=torch.int32, device="cuda")
+    cu[1::2] = total
+    A.moe_attention_prompt(x, x[:64, :1], x[:64, :1], cu, torch.zeros_like(cu), out)
+    torch.cuda.synchronize()
+    assert N.check_status() == INVALID and (out == 7).all()
+    q, few = normal((300, 2, 64), "bf16", 39), [0] * 300 + [200, 100, 300]  # 100 queries twice, 303 offsets
+    less = torch.full_like(q, 7.0)
+    A.moe_attention_prompt(q, q, q, ints(few), ints(few), less)
+    assert N.check_status() == INVALID and (less == 7).all()
+    cache = make_cache([2000], 1, 8, 16, "bf16", 38)
+    ws = A.cached_workspace(cache, n - 1, total, 128).zero_()
+    A.moe_attention_cached(x, cache, 0, torch.zeros(n - 1, dtype=torch.int32, device="cuda"), cu, out, ws)
+    torch.cuda.synchronize()
+    assert N.check_status() == INVALID and (out == 7).all()
