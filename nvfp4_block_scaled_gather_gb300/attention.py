@@ -4,9 +4,10 @@ that reads it, and attention over whole prompts.
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Tensors are torch CUDA tensors; calls are enqueued on the current torch
-stream (or `stream`). What torch can see of an argument (type, shape,
-strides, device) is checked here and raises ValueError; a nonzero status of
-the library raises RuntimeError. There is no fallback.
+stream (or `stream`), on the current device, whose the tensors have to be.
+What torch can see of an argument (type, shape, strides, device) is checked
+here and raises ValueError; a nonzero status of the library raises
+RuntimeError. There is no fallback.
 """
 from __future__ import annotations
 
@@ -80,8 +81,15 @@ _CODES = {torch.bfloat16: BF16, torch.float16: FP16}
 
 
 def _stream(stream, device: int) -> int:
-    """The stream's handle: the given one, or the device's current one."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    """The stream's handle: the given one, or the device's current one. The library launches on the current device, so
+    that has to be the tensors' (the default stream's handle is the same on every device and would not tell)."""
+    if torch._C._cuda_getDevice() != device:
+        raise ValueError(f"tensors are on cuda:{device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError(f"tensors are on cuda:{device}, but the stream's device is {stream.device}")
+    return stream.cuda_stream
 
 
 def _ints(name, t, n, device: int) -> int:

@@ -136,3 +136,38 @@ def test_offsets_that_give_every_row_to_thousands_of_sequences(cuda):
     A.moe_attention_cached(x, cache, 0, torch.zeros(n - 1, dtype=torch.int32, device="cuda"), cu, out, ws)
     torch.cuda.synchronize()
     assert N.check_status() == INVALID and (out == 7).all()
+
+
+def test_other_devices_are_refused(cuda, monkeypatch):
+    """Tensors of a device that is not the current one, and streams of another: nothing is launched."""
+    q, cu = normal((3, 4, 64), "bf16", 84), ints([0, 3])
+    kv, out = normal((3, 2, 64), "bf16", 85), torch.full((3, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    cache = A.KVCache.empty(1, 4, 16, 2, 64, 2, 4)
+    ws, seqs, three = A.pages_workspace(cache), ints([0]), ints([3])
+    attn_ws, mask, places = A.cached_workspace(cache, 1, 3, 4), ints([[0]] * 3), ints([[0]])
+
+    class Elsewhere:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    def calls(**stream):
+        return (lambda: A.moe_attention_prompt(q, kv, kv, cu, cu, out, **stream),
+                lambda: A.moe_attention_cached(q, cache, 0, seqs, cu, out, attn_ws, **stream),
+                lambda: A.moe_kv_extend(cache, seqs, three, ws, **stream),
+                lambda: A.moe_kv_append(cache, 0, seqs, cu, kv, kv, **stream),
+                lambda: A.moe_kv_fork(cache, seqs, ints([1]), **stream),
+                lambda: A.moe_kv_truncate(cache, seqs, three, **stream),
+                lambda: A.moe_kv_keep(cache, seqs, three, places, seqs, ws, **stream),
+                lambda: A.moe_kv_copy_pages(cache, seqs, three, **stream),
+                lambda: A.moe_kv_compact(cache, ws, **stream),
+                lambda: A.moe_tree_mask(ints([-1, 0, 1]), cu, mask, **stream))
+
+    for call in calls(stream=Elsewhere()):
+        with pytest.raises(ValueError, match="device"):
+            call()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in calls():
+        with pytest.raises(ValueError, match="device"):
+            call()
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert (out == 7).all() and not cache.refs.any() and not cache.length.any() and N.check_status() == 0
