@@ -79,7 +79,7 @@ __device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
 
 // Exclusive sums over the CTA's threads (kPlanThreads of them) of N values at
-// once, in place; total: the sums.
+// once, in place; total: the sums. Modulo 2^32.
 template <int N>
 __device__ void block_scan(int (&v)[N], int (&total)[N]) {
   __shared__ int part[N][kPlanThreads / 32];
@@ -93,7 +93,7 @@ __device__ void block_scan(int (&v)[N], int (&total)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const int y = __shfl_up_sync(~0u, x[e], o);
-      if (lane >= o) x[e] += y;
+      if (lane >= o) x[e] = (int)((uint32_t)x[e] + (uint32_t)y);
     }
   if (lane == 31)
 #pragma unroll
@@ -102,9 +102,9 @@ __device__ void block_scan(int (&v)[N], int (&total)[N]) {
   // every warp sums the warps' sums for itself
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const int mine = part[e][lane];
-    total[e] = __reduce_add_sync(~0u, mine);
-    v[e] = x[e] - v[e] + __reduce_add_sync(~0u, lane < warp ? mine : 0);
+    const uint32_t mine = (uint32_t)part[e][lane];
+    total[e] = (int)__reduce_add_sync(~0u, mine);
+    v[e] = (int)((uint32_t)x[e] - (uint32_t)v[e] + __reduce_add_sync(~0u, lane < warp ? mine : 0u));
   }
   __syncthreads();
 }
@@ -206,7 +206,11 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(Kv kv, const 
     if (tid == 0) report(status, MOE_ERR_INVALID);
     return;
   }
-  int total = 0, copies = 0, all_free = 0, first = 0;  // first: rank of the run's first free page
+  // The pages wanted can pass 32 bits (thousands of sequences of up to 2^30
+  // each), so their multiples of 4096 are summed too: more of these than the
+  // free pages have is more pages than there are, and with no more of them the
+  // sum itself is below 2^30 + 2^24.
+  int total = 0, copies = 0, high = 0, all_free = 0, first = 0;  // first: rank of the run's first free page
   int slot[kPer];                                      // in the list of copies, or -1
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
@@ -215,10 +219,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(Kv kv, const 
     if (u * kPlanThreads >= n) continue;
     const bool copy = i < n && g.open[i] >= 0 && refs[u] - g.off[i] > 1;
     const int want = need[u] + (copy ? 1 : 0);
-    int at[3] = {want, copy ? 1 : 0, u == 0 && lane == 0 ? free_pages : 0}, sums[3];
+    int at[4] = {want, copy ? 1 : 0, u == 0 && lane == 0 ? free_pages : 0, want >> 12}, sums[4];
     block_scan(at, sums);
     if (i < n) {
-      g.off[i] = total + at[0];
+      g.off[i] = (int)((uint32_t)total + (uint32_t)at[0]);
       g.column[i] = own[u] + need[u] - want;  // with a copy the open page's, before the new ones
     }
     if (copy) slot[u] = copies + at[1];
@@ -226,10 +230,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(Kv kv, const 
       first = __shfl_sync(~0u, at[2], 0);
       all_free = sums[2];
     }
+    high += sums[3];
+    if (high > all_free >> 12) break;  // (the same in every thread)
     total += sums[0];
     copies += sums[1];
   }
-  if (total > all_free) {
+  if (high > all_free >> 12 || total > all_free) {
     if (tid == 0) report(status, MOE_ERR_PAGES);
     return;
   }

@@ -7,7 +7,7 @@ from nvfp4_block_scaled_gather_gb300 import _native as N
 from nvfp4_block_scaled_gather_gb300 import attention as A
 
 pytestmark = pytest.mark.gpu
-INVALID = 1
+INVALID, OUT_OF_PAGES = 1, 6
 LEAST = -2 ** 31
 
 
@@ -38,3 +38,26 @@ def test_counts_below_zero_are_reported_and_not_followed(cuda, length, held):
         call()
         assert N.check_status() == INVALID, name
         assert all(torch.equal(a, b) for a, b in zip(state, before)), name
+
+
+def wide_cache(n_pages, max_seqs, max_pages):
+    """A fresh cache of one-token pages whose table is not filled (nothing of it is read where a sequence is empty)."""
+    zeros = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    return A.KVCache(torch.zeros((2, n_pages, 1, 1, 8), dtype=torch.bfloat16, device="cuda"),
+                     torch.empty((max_seqs, max_pages), dtype=torch.int32, device="cuda"), zeros(max_seqs), zeros(max_seqs),
+                     zeros(n_pages))
+
+
+@pytest.mark.parametrize("n,each", [(2, 1 << 30), (1500, 1 << 21), (1024, (1 << 21) + 1)])
+def test_wants_that_pass_32_bits_are_out_of_pages(cuda, n, each):
+    """Together 2^31 and more pages, in one pass of the plan's threads and in two: all or nothing."""
+    cache = wide_cache(5, n, each)
+    ws = A.pages_workspace(cache)
+    assert N.check_status() == 0
+    A.moe_kv_extend(cache, ints(list(range(n))), ints([each] * n), ws)
+    assert N.check_status() == OUT_OF_PAGES
+    assert not cache.length.any() and not cache.held.any() and not cache.refs.any()
+    A.moe_kv_extend(cache, ints([0, 1]), ints([2, 3]), ws)
+    assert N.check_status() == 0
+    assert cache.length[:3].tolist()[:2] == [2, 3] and cache.refs.tolist() == [1] * 5
+    assert cache.table[0, :2].tolist() == [0, 1] and cache.table[1, :3].tolist() == [2, 3, 4]
