@@ -61,7 +61,7 @@ typedef struct {
   int max_seqs, max_pages;
 } moe_kv_cache_t;
 
-#define MOE_KV_MAX_CALL 4096 /* sequences of one upkeep call */
+#define MOE_KV_MAX_CALL 4096 /* sequences of one upkeep call at most (else MOE_ERR_INVALID) */
 
 /* Device scratch of moe_kv_extend, moe_kv_keep and moe_kv_compact on this
  * cache: bytes (256-byte aligned, any contents). 0 for an invalid cache. */
@@ -104,7 +104,8 @@ int moe_kv_keep(const moe_kv_cache_t* cache, const int32_t* seqs, const int32_t*
                 int max_keep, const int32_t* kept, int n, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Copies page src[i] to page dst[i] in all planes; tables and counts stay.
- * The dst must be distinct and none of them a src. */
+ * The dst must be distinct and none of them a src (of another pair); any
+ * number of pairs. */
 int moe_kv_copy_pages(const moe_kv_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
                       cudaStream_t stream);
 

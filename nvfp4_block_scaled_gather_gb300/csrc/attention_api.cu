@@ -133,8 +133,10 @@ int moe_kv_keep(const moe_kv_cache_t* cache, const int32_t* seqs, const int32_t*
 
 int moe_kv_copy_pages(const moe_kv_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
                       cudaStream_t stream) {
-  const int st = upkeep_status(cache, n);
-  if (st != MOE_OK || n == 0) return st;
+  const int st = cache_status(cache);
+  if (st != MOE_OK) return st;
+  if (n < 0) return MOE_ERR_INVALID;  // (pages, not sequences: MOE_KV_MAX_CALL does not bound them)
+  if (n == 0) return MOE_OK;
   if (!src || !dst) return MOE_ERR_INVALID;
   int* word = status_ptr();
   if (!word) return MOE_ERR_CUDA;

@@ -61,3 +61,13 @@ def test_wants_that_pass_32_bits_are_out_of_pages(cuda, n, each):
     assert N.check_status() == 0
     assert cache.length[:3].tolist()[:2] == [2, 3] and cache.refs.tolist() == [1] * 5
     assert cache.table[0, :2].tolist() == [0, 1] and cache.table[1, :3].tolist() == [2, 3, 4]
+
+
+def test_copies_of_more_pages_than_a_call_has_sequences(cuda):
+    n = 5000
+    cache = A.KVCache.empty(1, 2 * n, 2, 1, 8, 1, 1)
+    cache.pages.copy_(torch.randn_like(cache.pages))
+    want = cache.pages[:, :n].flip(1).clone()
+    A.moe_kv_copy_pages(cache, torch.arange(n, dtype=torch.int32, device="cuda"),
+                        torch.arange(2 * n - 1, n - 1, -1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache.pages[:, n:], want) and N.check_status() == 0
