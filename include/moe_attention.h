@@ -23,7 +23,9 @@
  * length is out of range (MOE_ERR_INVALID). Keys and values that
  * a query does not see have no influence on it, NaN and infinities included.
  * Scores, the running maximum and sum, and the sum over the values are held
- * in fp32.
+ * in fp32; the weights exp(s_ij - lse_i) are rounded to the tensors' type for
+ * the product with the values (in fp16 those below 2^-32 of a row's largest
+ * are 0 there).
  */
 #ifndef MOE_ATTENTION_H
 #define MOE_ATTENTION_H

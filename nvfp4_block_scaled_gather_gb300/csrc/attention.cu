@@ -6,7 +6,11 @@
 //   O = O 2^(c m - c m') + P V    (tensor cores, P in 16 bits from tensor memory)
 // and at the end out = O / l. One pass over the keys; S and P never leave the
 // SM. P is rounded to 16 bits because the tensor cores take it so: its error
-// is that of the output's own rounding. m follows the running maximum lazily:
+// is that of the output's own rounding, 2^-8 or 2^-11 of it at most. l sums the
+// unrounded ones. fp16 ends at 2^-24, where bf16 has fp32's range: there all of
+// P and l are 2^7 larger (the factor cancels in O / l; P <= 2^15), so that
+// weights down to 2^-21 of the largest keep their 11 bits and none above 2^-32
+// is lost (a million such are 2^-12 of the row). m follows the running maximum lazily:
 // as long as no score of the row exceeds m by 8 powers of two, P <= 256 is
 // held against the old m (exact: the factor cancels in O / l) and O is not
 // touched.
@@ -75,6 +79,8 @@ constexpr int kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // the two S (P goes over it) and the two O, 128 columns each
 constexpr int kHeader = 16384;
 constexpr float kLazy = 8.0f;    // powers of two that a score may exceed the running maximum by
+template <int kType>
+constexpr float kRaise = kType == MOE_FP16 ? 7.0f : 0.0f;  // powers of two that P and l are held larger by
 constexpr float kUndone = -1.0f;  // in place of a piece's sum: the sequence has a bad page
 
 template <int DP>
@@ -1285,7 +1291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             if (move) m = top;
           }
           if (here) {
-            const float base = m == -INFINITY ? 0.0f : -m * c;
+            const float base = m == -INFINITY ? 0.0f : fmaf(-m, c, kRaise<kType>);
             const uint64_t c2 = pair_of(c, c), base2 = pair_of(base, base);
             uint64_t sum[2] = {0, 0};
             // in two parts, so that the MMAs of the first run while the second is
@@ -1490,7 +1496,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           }
         } else {
           if (a.part_of) a.part_of[(long long)(it.first - it.i0) * a.heads_q + row0 + r] = make_int4(-1, 0, 0, 0);
-          if (a.lse) a.lse[row] = l != 0.0f ? (m * c + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (a.lse) a.lse[row] = l != 0.0f ? (m * c + (__log2f(l) - kRaise<kType>)) * 0.6931471805599453f : -INFINITY;
         }
       }
       __syncwarp();
@@ -1571,7 +1577,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
   const int t = of.w / a.heads_q, h = of.w - t * a.heads_q;
   *reinterpret_cast<uint2*>(a.out.p + (long long)t * a.out.ts + (long long)h * a.out.hs + q * 4) =
       make_uint2(pack2<kType>(o[0] * inv, o[1] * inv), pack2<kType>(o[2] * inv, o[3] * inv));
-  if (a.lse && q == 0) a.lse[of.w] = l != 0.0f ? (top + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (a.lse && q == 0) a.lse[of.w] = l != 0.0f ? (top + (__log2f(l) - kRaise<kType>)) * 0.6931471805599453f : -INFINITY;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -7,7 +7,7 @@ import torch
 from nvfp4_block_scaled_gather_gb300 import _native as N
 from nvfp4_block_scaled_gather_gb300 import attention as A
 from oracle import attention as OA
-from tests.test_gpu_attention import hold, ints, make_cache, normal, run_cached, starts
+from tests.test_gpu_attention import f64, hold, ints, make_cache, normal, run_cached, starts
 
 pytestmark = pytest.mark.gpu
 INVALID = 1
@@ -171,3 +171,32 @@ def test_other_devices_are_refused(cuda, monkeypatch):
     monkeypatch.undo()
     torch.cuda.synchronize()
     assert (out == 7).all() and not cache.refs.any() and not cache.length.any() and N.check_status() == 0
+
+
+@pytest.mark.parametrize("call", ["prompt", "cached"])
+@pytest.mark.parametrize("n", [2000, 40000])
+def test_small_weights_of_fp16_count(cuda, call, n):
+    """One key of weight 1 whose value is 0, and n - 1 of weight 2^-26 with values of 1. In fp16 half of the least
+    number above 0 is 2^-25, so weights that are held as they are would leave nothing of them. Each is a power of two
+    and has no rounding error of its own; the scores' is 2^-20 (a product of 64 terms below 2^5 in fp32: 72 * 2^-22 * 2^5
+    is 2^-10.8 of a weight), the output's 2^-11 and, below fp16's normal numbers, 2^-25."""
+    dim = 64
+    q, k, v = (torch.zeros((m, 1, dim)) for m in (1, n, n))
+    q[:] = 1.0
+    k[n // 3, 0, 0] = 26.0            # in powers of two, by the scale
+    v[:] = 1.0
+    v[n // 3] = 0.0
+    q, k, v = (x.half().cuda() for x in (q, k, v))
+    scale = float(np.log(2.0))
+    if call == "prompt":
+        out, lse = torch.empty_like(q), torch.empty((1, 1), device="cuda")
+        A.moe_attention_prompt(q, k, v, ints([0, 1]), ints([0, n]), out, lse=lse, scale=scale)
+    else:
+        cache = A.KVCache.empty(1, -(-n // 64), 64, 1, dim, 1, -(-n // 64), dtype=torch.float16)
+        A.moe_kv_extend(cache, ints([0]), ints([n]), A.pages_workspace(cache))
+        A.moe_kv_append(cache, 0, ints([0]), ints([0, n]), k, v)
+        out, lse = run_cached(q, cache, 0, ints([0]), ints([0, 1]), scale=scale)
+    rest = (n - 1) * 2.0 ** -26
+    want = rest / (1.0 + rest)
+    assert np.abs(f64(out) - want).max() <= want * (2.0 ** -10.8 + 2.0 ** -11) + 2.0 ** -25
+    assert abs(float(lse) - (26.0 * np.log(2.0) + np.log1p(rest))) <= 2.0 ** -10.8 + 2.0 ** -20 * 20
