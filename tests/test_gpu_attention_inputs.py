@@ -200,3 +200,25 @@ def test_small_weights_of_fp16_count(cuda, call, n):
     want = rest / (1.0 + rest)
     assert np.abs(f64(out) - want).max() <= want * (2.0 ** -10.8 + 2.0 ** -11) + 2.0 ** -25
     assert abs(float(lse) - (26.0 * np.log(2.0) + np.log1p(rest))) <= 2.0 ** -10.8 + 2.0 ** -20 * 20
+
+
+@pytest.mark.parametrize("context", [0, 3000])
+def test_values_that_are_not_finite_in_a_mask_of_thousands_of_tokens(cuda, context):
+    """They reach the rows that see them, whichever those are, and the call ends in time."""
+    n, dim, page = 16000, 128, 64
+    cache = make_cache([context + n], 1, dim, page, "bf16", 40, layers=1)
+    g = torch.Generator(device="cuda").manual_seed(41)
+    mask = torch.randint(LEAST, MOST, (n, n // 32), dtype=torch.int32, device="cuda", generator=g)
+    places = {5: float("inf"), n // 2: float("nan"), n - 2: -float("inf"), n - 1: float("inf")}
+    columns = {5: 3, n // 2: 100, n - 2: 64, n - 1: 64}
+    for j, value in places.items():
+        at = context + j
+        cache.pages[1, int(cache.table[0, at // page]), at % page, 0, columns[j]] = value
+    out, lse = run_cached(normal((n, 1, dim), "bf16", 42), cache, 0, ints([0]), ints([0, n]), mask)
+    assert N.check_status() == 0 and torch.isfinite(lse).all()
+    sees = {j: (mask[:, j // 32] >> (j % 32) & 1) != 0 for j in places}
+    want = torch.zeros((n, dim), device="cuda")
+    for j, value in places.items():
+        want[:, columns[j]] += torch.where(sees[j], value, 0.0)
+    got = torch.where(torch.isfinite(out[:, 0].float()), 0.0, out[:, 0].float())
+    assert torch.equal(torch.nan_to_num(got, 1.0, 2.0, 3.0), torch.nan_to_num(want, 1.0, 2.0, 3.0))
