@@ -77,6 +77,7 @@ def exported_symbols():
 
 
 _INT32, _FLOAT32 = torch.int32, torch.float32
+_MOST = 2 ** 31 - 1  # that an int of the library holds (ctypes would pass the low 32 bits on)
 _CODES = {torch.bfloat16: BF16, torch.float16: FP16}
 
 
@@ -109,6 +110,8 @@ def _heads(name, t, dtype, device: int):
         raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(shape)}")
     ts, hs, ds = t.stride()
     tokens, heads, dim = shape
+    if tokens > _MOST or heads > _MOST:
+        raise ValueError(f"{name} must have less than 2**31 tokens and heads, got {tuple(shape)}")
     # a stride along one element says nothing
     if tokens <= 1:
         ts = 0
@@ -140,6 +143,9 @@ class KVCache:
             raise ValueError("table must be [max_seqs, max_pages]")
         planes, n_pages, page_size, heads, dim = pages.shape
         max_seqs, max_pages = table.shape
+        if max(*pages.shape, *table.shape) > _MOST:
+            raise ValueError(f"pages and table must have less than 2**31 of each, got {tuple(pages.shape)} and "
+                             f"{tuple(table.shape)}")
         self.pages, self.table, self.length, self.held, self.refs = pages, table, length, held, refs
         self.layers, self.device, self.dtype = planes // 2, pages.get_device(), pages.dtype
         self.heads_kv, self.head_dim, self.row = heads, dim, (heads, dim)

@@ -1,0 +1,15 @@
+"""Sizes at the ends of what 32 bits count, without a GPU: refused before any
+launch."""
+import pytest
+import torch
+
+from nvfp4_block_scaled_gather_gb300 import attention as A
+
+@pytest.mark.parametrize("tokens,heads", [(2 ** 31, 1), (2 ** 32 + 5, 1), (2, 2 ** 31)])
+def test_tensors_of_more_tokens_than_an_int_holds(tokens, heads):
+    """Their low 32 bits would be another size. (Broadcast rows: no memory is needed.)"""
+    rows = torch.zeros((1, 1, 8), dtype=torch.bfloat16).expand(tokens, heads, 8)
+    with pytest.raises(ValueError, match="less than 2"):
+        A._heads("q", rows, torch.bfloat16, -1)
+    _, shape = A._heads("q", rows[:2, :1], torch.bfloat16, -1)
+    assert tuple(shape) == (2, 1, 8)
