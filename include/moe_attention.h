@@ -132,11 +132,12 @@ int moe_tree_mask(const int32_t* parents, const int32_t* cu, int n, int total, i
  * nq queries and nk keys sees its keys 0 .. a + nk - nq (the queries are the
  * last nq tokens). out [total_q, heads_q] rows of heads, lse [total_q,
  * heads_q] fp32 or null. head_dim % 8 == 0, head_dim <= 128, heads_q a
- * multiple of heads_kv with at most 128 query heads per kv head (else
- * MOE_ERR_SHAPE); scale finite and > 0. Rows past cu_q[n] are left alone.
- * Offsets outside the tensors are cut to them; a sequence whose offsets run
- * backwards is empty. Where more than 256 sequences have more queries together
- * than total_q the call is left undone (MOE_ERR_INVALID). */
+ * multiple of heads_kv with at most 128 query heads per kv head, total_q *
+ * heads_q <= 2^30, total_k <= 2^31 - 128 (else MOE_ERR_SHAPE); scale finite and
+ * > 0. Rows past cu_q[n] are left alone. Offsets outside the tensors are cut to
+ * them; a sequence whose offsets run backwards is empty. Where more than 256
+ * sequences have more queries together than total_q the call is left undone
+ * (MOE_ERR_INVALID). */
 int moe_attention_prompt(const moe_heads_t* q, const moe_heads_t* k, const moe_heads_t* v, const int32_t* cu_q,
                          const int32_t* cu_k, int n, int total_q, int total_k, int heads_q, int heads_kv,
                          int head_dim, int dtype, float scale, const moe_heads_t* out, float* lse,

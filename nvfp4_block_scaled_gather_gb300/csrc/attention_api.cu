@@ -169,6 +169,7 @@ int moe_attention_prompt(const moe_heads_t* q, const moe_heads_t* k, const moe_h
   const int st = attention_status(n, total_q, heads_q, heads_kv, head_dim, scale);
   if (st != MOE_OK) return st;
   if (total_k < 0 || !dtype_ok(dtype)) return MOE_ERR_INVALID;
+  if (total_k > kMaxKeys) return MOE_ERR_SHAPE;
   if (n == 0 || total_q == 0) return MOE_OK;
   if (!heads_ok(q) || !heads_ok(out) || !cu_q || !cu_k) return MOE_ERR_INVALID;
   if (total_k > 0 && (!heads_ok(k) || !heads_ok(v))) return MOE_ERR_INVALID;

@@ -16,6 +16,7 @@ int* status_ptr();
 
 constexpr int kMaxGroup = 128;   // query heads per kv head
 constexpr int kMaxHeadDim = 128;
+constexpr int kMaxKeys = 0x7fffffff - 127;  // a place in the last block of 128 keys is still counted in 31 bits
 
 // Rows of heads, 16-bit elements.
 struct Heads {

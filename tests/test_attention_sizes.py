@@ -1,9 +1,24 @@
 """Sizes at the ends of what 32 bits count, without a GPU: refused before any
 launch."""
+import ctypes
+
 import pytest
 import torch
 
 from nvfp4_block_scaled_gather_gb300 import attention as A
+
+SHAPE = 2
+
+
+def heads():
+    return ctypes.byref(A.Heads(4096, 256, 64))
+
+
+@pytest.mark.parametrize("total_k", [2 ** 31 - 1, 2 ** 31 - 127])
+def test_keys_whose_last_block_passes_31_bits(native, total_k):
+    assert A.load().moe_attention_prompt(heads(), heads(), heads(), 16, 16, 1, 4, total_k, 4, 2, 64, 0, 0.1, heads(), None,
+                                         None) == SHAPE
+
 
 @pytest.mark.parametrize("tokens,heads", [(2 ** 31, 1), (2 ** 32 + 5, 1), (2, 2 ** 31)])
 def test_tensors_of_more_tokens_than_an_int_holds(tokens, heads):
