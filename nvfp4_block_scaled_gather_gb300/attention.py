@@ -286,6 +286,8 @@ def moe_attention_cached(q, cache: KVCache, layer: int, seqs, cu_q, out, workspa
             raise ValueError("mask must be [total_q, words]")
         words = mask.shape[1]
         bits = _ints("mask", mask, total_q * words, dev)
+        if words == 0 and total_q:  # (no address: the library would take it for a chain)
+            raise ValueError("mask must have a word at least")
     _call("moe_attention_cached", load().moe_attention_cached, hq, cache._ref, layer,
           _ints("seqs", seqs, n, dev), _ints("cu_q", cu_q, n + 1, dev), n, total_q, heads_q, bits, words,
           dim ** -0.5 if scale is None else scale, ho, _lse(lse, total_q, heads_q, dev),

@@ -222,3 +222,14 @@ def test_values_that_are_not_finite_in_a_mask_of_thousands_of_tokens(cuda, conte
         want[:, columns[j]] += torch.where(sees[j], value, 0.0)
     got = torch.where(torch.isfinite(out[:, 0].float()), 0.0, out[:, 0].float())
     assert torch.equal(torch.nan_to_num(got, 1.0, 2.0, 3.0), torch.nan_to_num(want, 1.0, 2.0, 3.0))
+
+
+def test_masks_without_words_are_refused(cuda):
+    """They have no address, and without one a call is a chain, whose tokens see those before them."""
+    cache = make_cache([20], 1, 64, 16, "bf16", 43)
+    q = normal((4, 2, 64), "bf16", 44)
+    out, ws = torch.empty_like(q), A.cached_workspace(cache, 1, 4, 2)
+    with pytest.raises(ValueError, match="word"):
+        A.moe_attention_cached(q, cache, 0, ints([0]), ints([0, 4]), out, ws, mask=torch.empty((4, 0), dtype=torch.int32, device="cuda"))
+    A.moe_attention_cached(q[:0], cache, 0, ints([0]), ints([0, 0]), out[:0], ws,
+                           mask=torch.empty((0, 0), dtype=torch.int32, device="cuda"))
