@@ -44,12 +44,15 @@
 //  * Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT,
 //    drains its copies and MMAs, frees tensor memory and returns.
 //
-// What bounds it: of long prompts the MMAs (two of 128 x 128 x 128 a step;
-// 8192 tokens, 32 query and 8 kv heads of 128: 362 us, 1520 TFLOP/s counting
-// what the causal mask leaves, 80% of a large matrix product's rate); of decode
-// batches the reads of the cache (32 streams over 500..6000 keys, 8 kv heads:
-// 81 us, 5.5 TB/s); of single short calls the chain from the plan over the
-// first loads, S, P and O to the store (12 us, launch and all).
+// What bounds it: of long prompts the MMAs (two of 128 x 128 x 128 a step) and
+// the way from a step's weights to the next scores: 8192 tokens, 32 query and 8
+// kv heads of 128, take 362 us over the same inputs again and 383 to 400 over
+// new ones, 1520 and 1376 to 1436 TFLOP/s counting what the causal mask leaves,
+// 80% and 72 to 75% of a large matrix product's rate (heads of 64: 354 us, for
+// half the products). Of decode batches the reads of the cache (32 streams over
+// 500..6000 keys, 8 kv heads: 82 us, 5.5 TB/s); of single short calls the chain
+// from the plan over the first loads, S, P and O to the store (12 us, launch
+// and all).
 #include <cstdint>
 
 #include <cuda.h>
@@ -894,7 +897,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const int n = __shfl_sync(~0u, it.blocks, 0), item_no = seq_no - 1;
         if (n == 0) continue;
         const int lim = limit_of(a, it.nk, it.nq, it.i0);  // the least that any row of the pair sees
-        // keys that no other item reads leave L2 first (to partial results, for one)
+        // keys that no other item of the sequence reads leave L2 first (to partial
+        // results, for one): 4 trees over 24,000..40,000 keys 121 us so, 131
+        // otherwise; 32 decode streams 83 and 86. Pages that forks share are not
+        // told apart: 64 forks of 8000 keys 264 and 253, 16 forks 76 both ways
         const uint64_t policy = it.nq <= 2 * tpt ? once : normal;
         // lane i: row of box i of the block
         const int first = it.b0 * kTile + lane * maps.box;
@@ -1536,8 +1542,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 // bytes), a thread one quad of one row, the values of as many pieces in flight
 // as middling sequences have. Bound by the latency of its reads where the
 // pieces are few and small, so nothing is read before the values that could be
-// read with them (16 trees over 300..5000 keys: 40.9 us in all; four pieces in
-// flight 41.7).
+// read with them (16 trees over 300..5000 keys: 41 us in all; four pieces in
+// flight 0.8 more).
 constexpr int kJoinThreads = 256;
 template <int kType>
 __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_constant__ AttnArgs a) {

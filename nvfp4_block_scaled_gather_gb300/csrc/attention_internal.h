@@ -63,7 +63,8 @@ cudaError_t launch_tree_mask(const int* parents, const int* cu, int n, int total
 // throughout, this rule takes 16.8 instead of 15.3 us for one stream over 4000
 // keys and 83 instead of 88 for 32 streams over 500..6000, 42 instead of 51 for
 // trees of 16 streams over 300..5000 (at least 8 blocks throughout: 17.7, 81, 42).
-constexpr int kSplitItems = 152;     // pieces x heads x query tiles that one sequence is cut into at most (one a SM)
+// pieces x heads x query tiles that one sequence is cut for: one a SM (the quotient is rounded up: fewer than twice as many)
+constexpr int kSplitItems = 152;
 constexpr int kSplitMinBlocks = 4;   // blocks of a piece at least ...
 constexpr int kSplitFew = 6;         // ... of up to this many pieces; of more, twice as many blocks
 struct Cut {

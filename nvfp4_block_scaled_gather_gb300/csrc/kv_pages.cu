@@ -135,7 +135,10 @@ __device__ __forceinline__ uint32_t used_of(const int* refs, const Run& run, int
 // Latency bounds it, a chain of dependent reads of half a microsecond each. So
 // a thread has one sequence of each 1024 (four in a row, one after the other,
 // made it 14 us for 96 sequences; so it takes 6 us), and the pool is read
-// before the sequences are compared.
+// before the sequences are compared. One CTA goes over the counts of the whole
+// pool (twice if it is full) and compares the sequences pairwise: 6 us with a
+// nearly full pool of 300 pages, 22 with 48,000 and 70 with 190,000 (32
+// sequences); 16 us for 256 sequences, 38 for 1024 and 300 for 4096.
 struct Growth {
   int seq[MOE_KV_MAX_CALL];
   int open[MOE_KV_MAX_CALL];     // the open page, or -1; then where its copy is in the list, or -1
@@ -383,7 +386,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv kv, const i
 }
 
 // Compaction's plan in one CTA: U pages in use; the k-th used page from U on
-// goes to the k-th free page before U (as many of the one as of the other).
+// goes to the k-th free page before U (as many of the one as of the other). It
+// goes over the pool's counts several times: with nothing to move the call takes 6
+// us for 300 pages, 39 for 48,000 and 133 for 190,000.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Kv kv, KvWs ws) {
   pdl_wait();
   pdl_trigger();
