@@ -112,7 +112,9 @@ def _heads(name, t, dtype, device: int):
     tokens, heads, dim = shape
     if tokens > _MOST or heads > _MOST:
         raise ValueError(f"{name} must have less than 2**31 tokens and heads, got {tuple(shape)}")
-    # a stride along one element says nothing
+    # a stride along one element says nothing, and without tokens none does
+    if tokens == 0:
+        ts, hs, ds = 0, 0, 1
     if tokens <= 1:
         ts = 0
     if heads <= 1:

@@ -28,3 +28,12 @@ def test_tensors_of_more_tokens_than_an_int_holds(tokens, heads):
         A._heads("q", rows, torch.bfloat16, -1)
     _, shape = A._heads("q", rows[:2, :1], torch.bfloat16, -1)
     assert tuple(shape) == (2, 1, 8)
+
+
+@pytest.mark.parametrize("shape", [(0, 2, 8), (0, 1, 64)])
+def test_strides_of_tensors_without_tokens_say_nothing(shape):
+    """A step in which no sequence grows: torch gives empty tensors any strides."""
+    rows = torch.zeros(0, dtype=torch.bfloat16)[:, None, None].expand(shape)
+    assert rows.is_contiguous() and rows.stride(2) == 0
+    _, got = A._heads("k", rows, torch.bfloat16, -1)
+    assert tuple(got) == shape
