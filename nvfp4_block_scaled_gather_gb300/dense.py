@@ -1,0 +1,278 @@
+"""ctypes binding of the dense operators of libmoe_nvfp4.so
+(include/moe_dense.h): the residual stream's step between two blocks with its
+norms, rows in 8-bit floating point, and their product.
+
+Argument marshalling only, as in attention.py: tensors are torch CUDA tensors
+on the current device, calls are enqueued on the current torch stream (or
+`stream`), what torch can see of an argument is checked here and raises
+ValueError, a nonzero status of the library raises RuntimeError. There is no
+fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import _native
+from .attention import BF16, FP16, _heads, _scratch, _stream
+from ._native import _check
+
+c_int, c_size_t, c_void_p, c_longlong, c_float = (ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong,
+                                                  ctypes.c_float)
+
+FP32 = 2  # MOE_FP32
+
+
+class Fp8RowsStruct(ctypes.Structure):
+    """moe_fp8_rows_t"""
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("row_stride", c_longlong), ("scale_stride", c_longlong)]
+
+
+class Gate(ctypes.Structure):
+    """moe_gate_t"""
+    _fields_ = [("data", c_void_p), ("token_stride", c_longlong), ("head_stride", c_longlong), ("dim_stride", c_int)]
+
+
+# the structs as bytes, at a fifth of the time that the classes take
+_rows_bytes = struct.Struct("PPqq").pack
+_gate_bytes = struct.Struct("PqqiI").pack   # (padded to 8 bytes)
+_norm_head = struct.Struct("iiii").pack     # tokens, heads, dim, dtype
+_norm_mid = struct.Struct("ffiIPP").pack    # residual_scale, eps, post_norm, padding, post_weight, pre_weight
+_NO_HEADS, _NO_GATE, _NO_ROWS = bytes(24), bytes(32), bytes(32)
+
+_SIGS = {
+    "moe_residual_norm": (c_int, [c_void_p, c_void_p]),
+    "moe_fp8_quantize_rows": (c_int, [c_void_p, c_longlong, c_int, c_int, c_int, c_void_p, c_void_p]),
+    "moe_fp8_gemm": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_void_p, c_longlong, c_int, c_void_p]),
+    "moe_fp8_linear_workspace_size": (c_size_t, [c_int, c_int]),
+    "moe_fp8_linear": (c_int, [c_void_p, c_longlong, c_int, c_int, c_int, c_void_p, c_int, c_void_p, c_longlong, c_int,
+                               c_void_p, c_size_t, c_void_p]),
+}
+_LIB = None
+
+
+def load():
+    """The library with this header's signatures (built if stale)."""
+    global _LIB
+    if _LIB is None:
+        lib = _native.load()
+        for name, (res, args) in _SIGS.items():
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = res, args
+        _LIB = lib
+    return _LIB
+
+
+def exported_symbols():
+    return list(_SIGS)
+
+
+_FLOAT32 = torch.float32
+_CODES = {torch.bfloat16: BF16, torch.float16: FP16}
+_OUT_CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+_MOST = 2 ** 31 - 1  # that an int of the library holds (ctypes would pass the low 32 bits on)
+
+
+def _call(name, fn, *args):
+    status = fn(*args)
+    if status:
+        _check(name, status)
+
+
+class Fp8Rows:
+    """8-bit rows (moe_fp8_rows_t) whose memory is the caller's: codes [rows, k], float8_e4m3fn or uint8, and scales
+    [rows, at least 4 * ceil(k / 512)] uint8 (e8m0: 2 ** (byte - 127)), one for each 128 values; both contiguous along
+    their rows. `rows(n)` is a handle over the first n."""
+
+    def __init__(self, codes, scales):
+        if codes.dim() != 2 or codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or not codes.is_cuda:
+            raise ValueError("codes must be a float8_e4m3fn or uint8 CUDA tensor [rows, k]")
+        rows, k = codes.shape
+        if max(rows, k) > _MOST:
+            raise ValueError(f"codes must have less than 2**31 rows and columns, got {tuple(codes.shape)}")
+        if k and codes.stride(1) != 1 or rows > 1 and (codes.stride(0) % 16 or codes.stride(0) < k):
+            raise ValueError(f"codes' rows must be contiguous, apart, and a multiple of 16 bytes from each other, got "
+                             f"strides {codes.stride()}")
+        if scales.dtype is not torch.uint8 or scales.dim() != 2 or scales.get_device() != codes.get_device():
+            raise ValueError(f"scales must be a uint8 tensor [rows, scales] on {codes.device}")
+        words = 4 * -(-k // 512)
+        if scales.shape[0] != rows or scales.shape[1] < words:
+            raise ValueError(f"scales must be [{rows}, {words} or more], got {tuple(scales.shape)}")
+        if scales.shape[1] and scales.stride(1) != 1 or rows > 1 and (scales.stride(0) % 4 or scales.stride(0) < words):
+            raise ValueError(f"scales' rows must be contiguous, apart, and a multiple of 4 bytes from each other, got "
+                             f"strides {scales.stride()}")
+        self.codes, self.scales, self.n, self.k, self.device = codes, scales, rows, k, codes.get_device()
+        self.bytes = _rows_bytes(codes.data_ptr(), scales.data_ptr(), codes.stride(0) if rows > 1 else 0,
+                                 scales.stride(0) if rows > 1 else 0)
+
+    @classmethod
+    def empty(cls, rows, k, device="cuda"):
+        return cls(torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty((rows, 4 * -(-k // 512)), dtype=torch.uint8, device=device))
+
+    def rows(self, n):
+        return self if n == self.n else Fp8Rows(self.codes[:n], self.scales[:n])
+
+    def dequantized(self):
+        """The values that the rows stand for, fp32 (for checks: elementary torch operations)."""
+        power = torch.ldexp(torch.ones((), device=self.codes.device), self.scales.int() - 127)
+        power = torch.where(self.scales == 255, torch.full_like(power, float("nan")), power)
+        codes = self.codes.view(torch.float8_e4m3fn).float()
+        return codes * power.repeat_interleave(128, dim=1)[:, :self.k]
+
+
+def _matrix(name, t, dtype, device: int):
+    """[rows, k] with k contiguous: address, row stride in elements, shape."""
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(shape)}")
+    rows, k = shape
+    if rows > _MOST or k > _MOST:
+        raise ValueError(f"{name} must have less than 2**31 rows and columns, got {tuple(shape)}")
+    rs, ks = t.stride()
+    if rows == 0:
+        rs, ks = 0, 1
+    elif rows == 1:
+        rs = 0
+    if ks != 1 and k > 1:
+        raise ValueError(f"{name}: rows must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), rs, rows, k
+
+
+def _input16(name, t, device: int):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    p, rs, rows, k = _matrix(name, t, t.dtype, device)
+    if rs % 8:
+        raise ValueError(f"{name}: the row stride must be a multiple of 8 elements, got {t.stride()}")
+    return p, rs, rows, k, code
+
+
+def _rows_of(name, r, device: int):
+    if not isinstance(r, Fp8Rows):
+        raise ValueError(f"{name} must be Fp8Rows")
+    if r.device != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {r.codes.device}")
+    return r.bytes
+
+
+def _output(y, rows, n, device: int):
+    code = _OUT_CODES.get(y.dtype)
+    if code is None:
+        raise ValueError(f"y must be bfloat16, float16 or float32, got {y.dtype}")
+    p, rs, rows_y, n_y = _matrix("y", y, y.dtype, device)
+    if rows_y != rows or n_y != n:
+        raise ValueError(f"y must be [{rows}, {n}], got {tuple(y.shape)}")
+    return p, rs, code
+
+
+def moe_fp8_quantize_rows(x, out: Fp8Rows, stream=None):
+    """x [rows, k], bfloat16 or float16, as 8-bit rows."""
+    dev = out.device
+    p, rs, rows, k, code = _input16("x", x, dev)
+    if (rows, k) != (out.n, out.k):
+        raise ValueError(f"out must have {rows} rows of {k}, got {out.n} of {out.k}")
+    _call("moe_fp8_quantize_rows", load().moe_fp8_quantize_rows, p, rs, rows, k, code, _rows_of("out", out, dev),
+          _stream(stream, dev))
+
+
+def moe_fp8_gemm(x: Fp8Rows, w: Fp8Rows, y, stream=None):
+    """y [x's rows, w's rows] = x w^T over dequantized values, bfloat16, float16 or float32."""
+    dev = w.device
+    if x.k != w.k:
+        raise ValueError(f"x and w must have rows of one length, got {x.k} and {w.k}")
+    p, rs, code = _output(y, x.n, w.n, dev)
+    _call("moe_fp8_gemm", load().moe_fp8_gemm, _rows_of("x", x, dev), x.n, _rows_of("w", w, dev), w.n, w.k, p, rs, code,
+          _stream(stream, dev))
+
+
+def linear_workspace(tokens: int, k: int, device="cuda"):
+    """The scratch of moe_fp8_linear for calls of up to `tokens` rows of k."""
+    size = load().moe_fp8_linear_workspace_size(tokens, k)
+    if size == 0:
+        raise ValueError(f"no product of {tokens} rows of {k}: k must be a positive multiple of 16, both within limits")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def moe_fp8_linear(x, w: Fp8Rows, y, workspace, stream=None):
+    """y = x w^T with x [rows, k], bfloat16 or float16, quantized on the way: moe_fp8_quantize_rows, then
+    moe_fp8_gemm."""
+    dev = w.device
+    p, rs, rows, k, code = _input16("x", x, dev)
+    if k != w.k:
+        raise ValueError(f"x and w must have rows of one length, got {k} and {w.k}")
+    py, rsy, code_y = _output(y, rows, w.n, dev)
+    _call("moe_fp8_linear", load().moe_fp8_linear, p, rs, rows, k, code, w.bytes, w.n, py, rsy, code_y,
+          *_scratch(workspace, dev), _stream(stream, dev))
+
+
+def _three(t):
+    """[tokens, dim] as rows of one head."""
+    return t.unsqueeze(1) if t.dim() == 2 else t
+
+
+def _norm_weight(name, w, dim, device: int):
+    if w is None:
+        return 0
+    if w.dtype is not _FLOAT32 or w.shape != (dim,) or not w.is_contiguous() or w.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous float32 tensor {(dim,)} on cuda:{device}")
+    return w.data_ptr()
+
+
+def _gate(g, dtype, shape, device: int):
+    """A factor for each element, by broadcasting: sizes of 1 are held along."""
+    if g.dim() == 2 and shape[1] == 1:
+        g = g.unsqueeze(1)
+    if g.dtype is not dtype or g.get_device() != device:
+        raise ValueError(f"gate must be {dtype} on cuda:{device}, got {g.dtype} on {g.device}")
+    if g.dim() != 3 or any(a != b and a != 1 for a, b in zip(g.shape, shape)):
+        raise ValueError(f"gate must broadcast to {tuple(shape)}, got {tuple(g.shape)}")
+    ts, hs, ds = (0 if n == 1 else s for n, s in zip(g.shape, g.stride()))
+    if ds not in (0, 1) or ds == 1 and (ts % 8 or hs % 8):
+        raise ValueError(f"gate: the last dimension must be contiguous (or 1) and the other strides multiples of 8 "
+                         f"elements, got {g.stride()}")
+    return _gate_bytes(g.data_ptr(), ts, hs, ds, 0)
+
+
+def moe_residual_norm(x, block=None, *, y=None, normed=None, quantized: Fp8Rows = None, pre_weight=None,
+                      post_norm=False, post_weight=None, gate=None, residual_scale=1.0, eps=1e-6, stream=None):
+    """The residual stream takes up a block's output and is normed for the next one (moe_residual_norm_t):
+
+      b      = norm(block) * post_weight if post_norm else block
+      y      = x + residual_scale * gate * b        (x without a block)
+      normed = norm(y) * pre_weight                 (quantized: the same as 8-bit rows)
+
+    x, block, y and normed [tokens, dim], or [tokens, heads, dim] with every head normed by itself; outputs that are
+    None are not written. gate broadcasts to x's shape."""
+    x = _three(x)
+    dtype, dev = x.dtype, x.get_device()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"x must be bfloat16 or float16, got {dtype}")
+    hx, shape = _heads("x", x, dtype, dev)
+    tokens, heads, dim = shape
+
+    def part(name, t):
+        if t is None:
+            return _NO_HEADS
+        packed, got = _heads(name, _three(t), dtype, dev)
+        if got != shape:
+            raise ValueError(f"{name} must be like x {tuple(shape)}, got {tuple(got)}")
+        return packed
+
+    rows = _NO_ROWS
+    if quantized is not None:
+        rows = _rows_of("quantized", quantized, dev)
+        if (quantized.n, quantized.k) != (tokens, dim):
+            raise ValueError(f"quantized must have {tokens} rows of {dim}, got {quantized.n} of {quantized.k}")
+    args = (_norm_head(tokens, heads, dim, code) + hx + part("block", block)
+            + (_NO_GATE if gate is None else _gate(gate, dtype, shape, dev))
+            + _norm_mid(residual_scale, eps, 1 if post_norm else 0, 0, _norm_weight("post_weight", post_weight, dim, dev),
+                        _norm_weight("pre_weight", pre_weight, dim, dev))
+            + part("y", y) + part("normed", normed) + rows)
+    _call("moe_residual_norm", load().moe_residual_norm, args, _stream(stream, dev))
