@@ -65,6 +65,7 @@
 #include "ldcg.cuh"
 #include "mbar.cuh"
 #include "pdl.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 namespace {
@@ -1597,22 +1598,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_cons
   *reinterpret_cast<uint2*>(a.out.p + (long long)t * a.out.ts + (long long)h * a.out.hs + q * 4) =
       make_uint2(pack2<kType>(o[0] * inv, o[1] * inv), pack2<kType>(o[2] * inv, o[3] * inv));
   if (a.lse && q == 0) a.lse[of.w] = l != 0.0f ? (top + (__log2f(l) - kRaise<kType>)) * 0.6931471805599453f : -INFINITY;
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
 }
 
 // Boxes of 64 columns x box_heads x box_rows of [rows, heads, head_dim]. False
