@@ -44,16 +44,22 @@ constexpr int kHeader = 1024;
 constexpr int kMaxStages = 12;
 constexpr int kMaxTokens = 240;    // of a tile: two accumulators and the scales fill tensor memory
 
-// kCols: tokens of a tile at most.
-template <int kCols>
+// kCols: tokens of a tile at most. kPair: two CTAs share a tile of 256 rows of
+// w, one MMA over both; each loads its own rows and half of the tokens.
+template <int kCols, bool kPair>
 struct Shape {
   static constexpr bool wide = kCols > 64;
+  static constexpr int ctas = kPair ? 2 : 1;
+  static constexpr int tile_rows = kRows * ctas;
   static constexpr int groups = wide ? 2 : 1;                  // of four warps that read accumulators
   static constexpr int acc = kCols / groups;                   // sums of a thread
   static constexpr int warps = 4 + 4 * groups + (wide ? 4 : 2);
   static constexpr int threads = 32 * warps;
   static constexpr int load_warp = 4 + 4 * groups, mma_warp = load_warp + 1;
   static constexpr int per_sm = wide ? 1 : 2;
+  static constexpr int asked = wide ? 32 : 16;                 // columns that are read from tensor memory together
+  // registers a thread of the two warpgroups that hold sums and of the other two: 256 x 184 + 256 x 72 of the launch's 512 x 128
+  static constexpr int many = wide ? 184 : 0, few = wide ? 72 : 0;
   static constexpr int smem = wide ? 232448 : 115712;          // 227 KB; half an SM's 228 KB less 1 KB each
   static constexpr int acc_cols = kCols;                       // of one accumulator
   static constexpr int scale_bufs = wide ? 2 : 4;
@@ -70,7 +76,7 @@ struct Args {
   int y_dtype;
   int T, N, K;
   int tn;                 // tokens of a tile, a multiple of 16
-  int tiles_t;
+  int tiles_n, tiles_t;
   long long tiles;        // of w rows x tokens
   int split;              // CTAs of a cluster that share a tile
   int piece, pieces;      // values of K of a piece; pieces
@@ -79,12 +85,21 @@ struct Args {
 };
 
 // ------------------------------- PTX helpers --------------------------------
+// (of a pair: `bar` may be the other CTA's)
+template <bool kPair>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
@@ -94,25 +109,67 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on the barrier (of a pair: on both CTAs') once this thread's MMAs are done.
+template <bool kPair>
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+template <bool kPair>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                        uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void tc_alloc(uint32_t slot, uint32_t cols) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tc_dealloc(uint32_t tmem, uint32_t cols) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-__device__ __forceinline__ void tc_st1(uint32_t taddr, uint32_t v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+__device__ __forceinline__ void tc_st1(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0]) : "memory");
+}
+__device__ __forceinline__ void tc_st2(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tc_st4(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -121,6 +178,15 @@ __device__ __forceinline__ void tc_st4(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// This warpgroup's registers a thread, up or down from the launch's 128.
+template <int kRegs>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -139,6 +205,22 @@ __device__ __forceinline__ void st_peer(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// An arrival that may be on another CTA's barrier, and a wait for such ones.
+__device__ __forceinline__ void arrive_peer(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Shared-memory descriptor, K-major operand in the 128-byte swizzle: rows of
 // 128 bytes, 8-row groups 1024 bytes apart, descriptor version 1, mode 2.
 __device__ __forceinline__ uint64_t desc_kmajor(uint32_t saddr) {
@@ -146,12 +228,19 @@ __device__ __forceinline__ uint64_t desc_kmajor(uint32_t saddr) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 // Instruction descriptor, kind::mxf8f6f4: A and B e4m3 (format 0), K-major,
-// e8m0 scales, M = 128, N = n; `byte` of each scale word is used.
-__device__ __forceinline__ uint32_t idesc_mxf8(int n) {
-  return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kRows >> 4) << 24);
+// e8m0 scales, M = m, N = n; `byte` of each scale word is used.
+__device__ __forceinline__ uint32_t idesc_mxf8(int m, int n) {
+  return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int byte) {
   return idesc | ((uint32_t)byte << 4) | ((uint32_t)byte << 29);
+}
+
+// True in one lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
 }
 
 // ------------------------------- bounded waits -------------------------------
@@ -159,10 +248,16 @@ struct Ctl {
   volatile int* abort_flag;
   int* status;
 };
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Ctl& c) {
+template <bool kCluster>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  if constexpr (kCluster) return try_wait_cluster(bar, parity);
+  return mbar_try_wait(bar, parity);
+}
+template <bool kCluster>
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Ctl& c) {
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait<kCluster>(bar, parity)) return true;
     if (*c.abort_flag) return false;
     if (clock64() - t0 > kWaitCycles) {
       *c.abort_flag = 1;
@@ -171,13 +266,22 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Ctl&
     }
   }
 }
-// By one thread.
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, const Ctl& c) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, c);
-}
-// By a whole warp, the same answer in every lane.
+// By a whole warp, the same answer in every lane; kCluster: for arrivals of the other CTA too.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Ctl& c) {
-  return __all_sync(~0u, wait_one(bar, parity, c));
+  return __all_sync(~0u, try_wait<kCluster>(bar, parity) || wait_slow<kCluster>(bar, parity, c));
+}
+
+// Tile i's place. Tiles that run at one time are eight rows of tiles of w high, so that both operands come from L2.
+struct Place {
+  int n, t;
+};
+__device__ __forceinline__ Place place_of(long long i, const Args& a) {
+  constexpr int kHigh = 8;
+  const long long full = (long long)kHigh * a.tiles_t;
+  const int group = (int)(i / full), in = (int)(i - group * full);
+  const int high = min(kHigh, a.tiles_n - group * kHigh);
+  return {group * kHigh + in % high, in / high};
 }
 
 __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
@@ -189,11 +293,11 @@ __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
         (uint16_t)(a.y_dtype == MOE_BF16 ? pack16x2<MOE_BF16>(v, 0.0f) : pack16x2<MOE_FP16>(v, 0.0f));
 }
 
-template <int kCols>
-__global__ void __launch_bounds__(Shape<kCols>::threads, Shape<kCols>::per_sm)
+template <int kCols, bool kPair>
+__global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPair>::per_sm)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ Args a) {
-  using S = Shape<kCols>;
+  using S = Shape<kCols, kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(smem);
@@ -207,24 +311,25 @@ __global__ void __launch_bounds__(Shape<kCols>::threads, Shape<kCols>::per_sm)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 516);
   const uint32_t s_w = base + kHeader, s_x = s_w + (uint32_t)a.stages * kWBytes;
-  const uint32_t x_bytes = (uint32_t)a.tn * kStageK;
+  const uint32_t x_bytes = (uint32_t)(a.tn / S::ctas) * kStageK;  // a stage's tokens in this CTA
   // the sums that this CTA's rows get from its cluster: [pieces][tokens][128 / split]
   const uint32_t recv_off = kHeader + (uint32_t)a.stages * (kWBytes + x_bytes);
   float* recv = reinterpret_cast<float*>(smem + recv_off);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (known to be the same over a warp: tensor-core and copy instructions take their operands from uniform registers)
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int i = 0; i < S::scale_bufs; ++i) {
-      mbar_init(sfull_bar(i), 4);
+      mbar_init(sfull_bar(i), 4 * S::ctas);
       mbar_init(sempty_bar(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(afull_bar(i), 1);
-      mbar_init(aempty_bar(i), 4 * S::groups);
+      mbar_init(aempty_bar(i), 4 * S::groups * S::ctas);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -232,16 +337,15 @@ __global__ void __launch_bounds__(Shape<kCols>::threads, Shape<kCols>::per_sm)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (warp == S::mma_warp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(S::tmem)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_alloc<kPair>(smem_u32(tmem_slot), S::tmem);
     tc_fence_before();
   }
-  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
-  const long long first = blockIdx.x / a.split, step = gridDim.x / a.split;
+  const int ctas = kPair ? 2 : a.split;  // of a cluster
+  const int rank = ctas > 1 ? (int)cluster_rank() : 0;
+  const long long first = blockIdx.x / ctas, step = gridDim.x / ctas;
   const int per = (a.pieces + a.split - 1) / a.split;
-  const int p0 = min(a.pieces, rank * per), p1 = min(a.pieces, p0 + per);
+  const int p0 = kPair ? 0 : min(a.pieces, rank * per), p1 = kPair ? a.pieces : min(a.pieces, p0 + per);
+  const int half = kPair ? rank : 0;  // which of a pair
   // blocks of 128 values of K: all of them, and this CTA's
   const int blocks = (a.K + kStageK - 1) / kStageK, per_piece = a.piece / kStageK;
   const int b0 = min(blocks, p0 * per_piece), b1 = min(blocks, p1 * per_piece);
@@ -251,69 +355,99 @@ __global__ void __launch_bounds__(Shape<kCols>::threads, Shape<kCols>::per_sm)
     // the rows of w may be those that the kernel before this one writes: they are asked for in L2 only
     if (first < a.tiles)
       for (int b = b0; b < b1 && b < b0 + a.stages; ++b)
-        tma_prefetch_l2(&wmap, b * kStageK, (int)(first / a.tiles_t) * kRows);
+        tma_prefetch_l2(&wmap, b * kStageK, place_of(first, a).n * S::tile_rows + half * kRows);
   }
   __syncthreads();
   tc_fence_after();
   __syncwarp();
-  if (a.split > 1) cluster_sync();  // a CTA's sums go to peers that have begun
+  if (ctas > 1) cluster_sync();  // peers have begun, their barriers are set up
   const uint32_t tmem = *tmem_slot;
   const Ctl ctl{abort_flag, a.status};
   pdl_wait();
   pdl_trigger();
 
   if (warp < 4) {
+    if constexpr (S::wide) give_registers<S::few>();
     // ============================ scales to tensor memory ============================
-    // Lane l of each warp has rows l, 32 + l, ...: column c of its quarter takes row 32 c + l's word.
-    uint32_t n = 0;
-    bool ok = true;
-    for (long long i = first; i < a.tiles && ok; i += step) {
-      const int n0 = (int)(i / a.tiles_t) * kRows, t0 = (int)(i % a.tiles_t) * a.tn;
-      for (int b = b0; b < b1 && ok; b += 4, ++n) {
-        uint32_t w[4], x[S::xs_words];
+    // Lane l of each warp has rows l, 32 + l, ...: column c of its quarter takes row 32 c + l's word. The next words
+    // are asked for before the present ones wait for their buffer.
+    struct Words {
+      uint32_t w[4], x[S::xs_words];
+    };
+    auto load = [&](long long i, int b) {
+      Words r;
+      const Place at = place_of(i, a);
+      const int n0 = at.n * S::tile_rows + half * kRows + lane, t0 = at.t * a.tn + lane;
+      const uint8_t *w = a.ws + n0 * a.ws_stride + b, *x = a.xs + t0 * a.xs_stride + b;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int r = n0 + 32 * c + lane;
-          w[c] = r < a.N ? ld_cg(reinterpret_cast<const uint32_t*>(a.ws + r * a.ws_stride + b)) : 0u;
-        }
+      for (int c = 0; c < 4; ++c, w += 32 * a.ws_stride)
+        r.w[c] = n0 + 32 * c < a.N ? ld_cg(reinterpret_cast<const uint32_t*>(w)) : 0u;
 #pragma unroll
-        for (int c = 0; c < S::xs_words; ++c) {
-          const int r = t0 + 32 * c + lane;
-          x[c] = 32 * c < a.tn && r < a.T ? ld_cg(reinterpret_cast<const uint32_t*>(a.xs + r * a.xs_stride + b)) : 0u;
+      for (int c = 0; c < S::xs_words; ++c, x += 32 * a.xs_stride)
+        r.x[c] = 32 * c < a.tn && t0 + 32 * c < a.T ? ld_cg(reinterpret_cast<const uint32_t*>(x)) : 0u;
+      return r;
+    };
+    if (first < a.tiles && b0 < b1) {
+      Words now = load(first, b0);
+      long long i = first;
+      int b = b0;
+      for (uint32_t n = 0;; ++n) {
+        b += 4;
+        if (b >= b1) {
+          b = b0;
+          i += step;
         }
+        Words next = now;
+        if (i < a.tiles) next = load(i, b);
         const int buf = n % S::scale_bufs;
-        ok = wait_warp(sempty_bar(buf), ((n / S::scale_bufs) & 1) ^ 1u, ctl);
-        if (!ok) break;
+        if (!wait_warp(sempty_bar(buf), ((n / S::scale_bufs) & 1) ^ 1u, ctl)) break;
         tc_fence_after();
         const uint32_t col = tmem + ((uint32_t)(warp * 32) << 16) + 2 * S::acc_cols + buf * S::scale_cols;
-        tc_st4(col + 8, w);
-#pragma unroll
-        for (int c = 0; c < S::xs_words; ++c) tc_st1(col + c, x[c]);
+        tc_st4(col + 8, now.w);
+        if constexpr (S::xs_words == 8) tc_st8(col, now.x);
+        else if constexpr (S::xs_words == 2) tc_st2(col, now.x);
+        else tc_st1(col, now.x);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sfull_bar(buf));
+        if (lane == 0) {
+          if constexpr (kPair) arrive_peer(peer(sfull_bar(buf), 0));
+          else mbar_arrive(sfull_bar(buf));
+        }
+        if (i >= a.tiles) break;
+        now = next;
       }
     }
-  } else if (warp == S::load_warp) {
-    // ================================ tiles by TMA ================================
-    if (lane == 0) {
+  } else if (warp >= S::load_warp) {
+    if constexpr (S::wide) give_registers<S::few>();
+    if (warp == S::load_warp) {
+      // ================================ tiles by TMA ================================
+      // (This warp and the next go through their loops whole, one lane issues: under a lane's own branch each
+      // instruction would be a loop over the lanes that may be in it.)
       uint32_t n = 0;
       bool ok = true;
       int stage = 0;
       uint32_t phase = 0;
       for (long long i = first; i < a.tiles && ok; i += step) {
-        const int n0 = (int)(i / a.tiles_t) * kRows, t0 = (int)(i % a.tiles_t) * a.tn;
+        const Place at = place_of(i, a);
+        const int n0 = at.n * S::tile_rows + half * kRows, t0 = at.t * a.tn + half * (a.tn / 2);
         for (int b = b0; b < b1; ++b, ++n) {
-          ok = wait_one(empty_bar(stage), phase ^ 1u, ctl);
+          ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
           if (!ok) break;
-          mbar_expect_tx(full_bar(stage), kWBytes + x_bytes);
-          tma_load(s_w + stage * kWBytes, &wmap, b * kStageK, n0, full_bar(stage));
-          tma_load(s_x + stage * x_bytes, &xmap, b * kStageK, t0, full_bar(stage));
+          if (elect_one()) {
+            // a pair's loads are all counted by the first CTA, whose MMAs read both CTAs' stages
+            const uint32_t bar = kPair ? peer(full_bar(stage), 0) : full_bar(stage);
+            if (half == 0) mbar_expect_tx(full_bar(stage), S::ctas * (kWBytes + x_bytes));
+            tma_load<kPair>(s_w + stage * kWBytes, &wmap, b * kStageK, n0, bar);
+            tma_load<kPair>(s_x + stage * x_bytes, &xmap, b * kStageK, t0, bar);
+          }
+          __syncwarp();
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok || *abort_flag) {  // nothing of ours may be in flight at exit: the last loads of every stage
+      // nothing of ours may be in flight at exit: the last loads of every stage (a pair's by the first CTA, before the
+      // cluster's last barrier)
+      if (half == 0 && (!ok || *abort_flag)) {
         const uint32_t s = (uint32_t)a.stages;
         for (uint32_t j = n > s ? n - s : 0; j < n; ++j) {
           const long long t = clock64();
@@ -321,88 +455,106 @@ __global__ void __launch_bounds__(Shape<kCols>::threads, Shape<kCols>::per_sm)
           }
         }
       }
-    }
-  } else if (warp == S::mma_warp) {
-    // ==================================== MMAs ====================================
-    if (lane == 0) {
-      const uint32_t idesc = idesc_mxf8(a.tn);
+    } else if (warp == S::mma_warp && half == 0) {
+      // ==================================== MMAs ====================================
+      const uint32_t idesc = idesc_mxf8(S::tile_rows, a.tn);
       int stage = 0;
       uint32_t phase = 0, ns = 0, na = 0;
       bool ok = true;
       for (long long i = first; i < a.tiles && ok; i += step) {
         for (int p = p0; p < p1 && ok; ++p, ++na) {
-          ok = wait_one(aempty_bar(na & 1), ((na >> 1) & 1) ^ 1u, ctl);
+          ok = wait_warp<kPair>(aempty_bar(na & 1), ((na >> 1) & 1) ^ 1u, ctl);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + (na & 1) * S::acc_cols;
-          const int end = min(b1, (p + 1) * per_piece);
-          for (int b = p * per_piece; b < end; ++b) {
+          const int begin = p * per_piece, end = min(b1, begin + per_piece);
+          for (int b = begin; b < end; ++b) {
             const int buf = ns % S::scale_bufs;
             if ((b & 3) == 0) {
-              ok = wait_one(sfull_bar(buf), (ns / S::scale_bufs) & 1, ctl);
+              ok = wait_warp<kPair>(sfull_bar(buf), (ns / S::scale_bufs) & 1, ctl);
               if (!ok) break;
             }
-            ok = wait_one(full_bar(stage), phase, ctl);
+            ok = wait_warp<kPair>(full_bar(stage), phase, ctl);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t col = tmem + 2 * S::acc_cols + buf * S::scale_cols;
-            const uint64_t wd = desc_kmajor(s_w + stage * kWBytes), xd = desc_kmajor(s_x + stage * x_bytes);
-            const uint32_t id = with_byte(idesc, b & 3);
-            const int steps = min(4, (a.K - b * kStageK + 31) / 32);
-            for (int j = 0; j < steps; ++j)  // 32 bytes on: 2 in a descriptor's address
-              tc_mma(d, wd + 2 * j, xd + 2 * j, id, col + 8, col, b > p * per_piece || j > 0);
-            tc_commit(empty_bar(stage));
-            if ((b & 3) == 3 || b + 1 == end) {
-              tc_commit(sempty_bar(buf));
-              ++ns;
+            const bool word_done = (b & 3) == 3 || b + 1 == end;
+            if (elect_one()) {
+              const uint32_t col = tmem + 2 * S::acc_cols + buf * S::scale_cols;
+              const uint64_t wd = desc_kmajor(s_w + stage * kWBytes), xd = desc_kmajor(s_x + stage * x_bytes);
+              const uint32_t id = with_byte(idesc, b & 3);
+              const int left = a.K - b * kStageK;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)  // 32 bytes on: 2 in a descriptor's address
+                if (32 * j < left) tc_mma<kPair>(d, wd + 2 * j, xd + 2 * j, id, col + 8, col, b > begin || j > 0);
+              tc_commit<kPair>(empty_bar(stage));
+              if (word_done) tc_commit<kPair>(sempty_bar(buf));
+              if (b + 1 == end) tc_commit<kPair>(afull_bar(na & 1));
             }
+            __syncwarp();
+            if (word_done) ++ns;
             if (++stage == a.stages) { stage = 0; phase ^= 1u; }
           }
-          if (ok) tc_commit(afull_bar(na & 1));
         }
       }
       if (!ok || *abort_flag) {
-        tc_commit(drain_bar);
+        if (elect_one()) tc_commit<kPair>(drain_bar);
+        __syncwarp();
         const long long t = clock64();
         while (!mbar_try_wait(drain_bar, 0) && clock64() - t < kWaitCycles) {
         }
       }
     }
-  } else if (warp < 4 + 4 * S::groups) {
+  } else {
+    if constexpr (S::wide) take_registers<S::many>();
     // ============================ sums of pieces, and y ============================
     const int quad = warp & 3, group = (warp - 4) >> 2;
     const int mine = a.tn / S::groups, c0 = group * mine;  // this group's columns: a multiple of 8
     const int slice = kRows / a.split, row = quad * 32 + lane;
+    const uint32_t freed = kPair ? peer(aempty_bar(0), 0) : aempty_bar(0);
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + c0;
     uint32_t na = 0;
     bool ok = true;
     for (long long i = first; i < a.tiles && ok; i += step) {
-      const int n = (int)(i / a.tiles_t) * kRows + row, t0 = (int)(i % a.tiles_t) * a.tn + c0;
+      const Place at = place_of(i, a);
+      const int n = at.n * S::tile_rows + half * kRows + row, t0 = at.t * a.tn + c0;
       float sum[S::acc];
+#pragma unroll
+      for (int c = 0; c < S::acc; ++c) sum[c] = 0.0f;
       for (int p = p0; p < p1; ++p, ++na) {
         ok = wait_warp(afull_bar(na & 1), (na >> 1) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
         const uint32_t from = taddr + (na & 1) * S::acc_cols;
-        const uint32_t to = a.split > 1 ? peer(base + recv_off, row / slice) + 4u * ((uint32_t)(p * a.tn) * slice + row % slice) : 0;
+        uint32_t v[S::asked];
+        if (S::wide || a.split == 1) {
 #pragma unroll
-        for (int c = 0; c < S::acc; c += 8) {
-          if (c < mine) {
-            uint32_t v[8];
+          for (int c = 0; c < S::acc; c += S::asked) {
+            if (c >= mine) break;
+            // (columns past the tile's are read and added too: nobody looks at their sums)
+#pragma unroll
+            for (int j = 0; j < S::asked; j += 8)
+              if (c + j < S::acc) tc_ld8(from + c + j, v + j);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < S::asked; ++j)
+              if (c + j < S::acc) sum[c + j] += __uint_as_float(v[j]);
+          }
+        } else {
+          const uint32_t to =
+              peer(base + recv_off, row / slice) + 4u * (uint32_t)(p * a.tn * slice + row % slice);
+          for (int c = 0; c < mine; c += 8) {
             tc_ld8(from + c, v);
             tc_wait_ld();
-            if (a.split > 1) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) st_peer(to + 4u * (uint32_t)((c + j) * slice), __uint_as_float(v[j]));
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) sum[c + j] = p == p0 ? __uint_as_float(v[j]) : sum[c + j] + __uint_as_float(v[j]);
-            }
+            for (int j = 0; j < 8; ++j) st_peer(to + 4u * (uint32_t)((c + j) * slice), __uint_as_float(v[j]));
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(aempty_bar(na & 1));
+        if (lane == 0) {
+          if constexpr (kPair) arrive_peer(freed + 8u * (na & 1));
+          else mbar_arrive(freed + 8u * (na & 1));
+        }
       }
       if (ok && a.split == 1 && n < a.N) {
 #pragma unroll
@@ -414,16 +566,19 @@ __global__ void __launch_bounds__(Shape<kCols>::threads, Shape<kCols>::per_sm)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (kPair || a.split > 1) {
+    __syncwarp();
+    cluster_sync();  // a pair's MMAs are done in both CTAs; a cluster's sums have arrived
+  }
   if (warp == S::mma_warp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::tmem) : "memory");
+    tc_dealloc<kPair>(tmem, S::tmem);
   }
   if (a.split > 1) {
-    __syncwarp();
-    cluster_sync();
     if (*abort_flag) return;
     const int slice = kRows / a.split;
-    const int n0 = (int)(first / a.tiles_t) * kRows + rank * slice, t0 = (int)(first % a.tiles_t) * a.tn;
+    const Place at = place_of(first, a);
+    const int n0 = at.n * kRows + rank * slice, t0 = at.t * a.tn;
     for (int i = threadIdx.x; i < slice * a.tn; i += S::threads) {
       const int n = n0 + i % slice, t = t0 + i / slice;
       if (n >= a.N || t >= a.T) continue;
@@ -447,29 +602,72 @@ bool make_map(CUtensorMap* map, const moe_fp8_rows_t& m, int rows, int K, int bo
          CUDA_SUCCESS;
 }
 
+// Pairs of CTAs that run at one time on the current device (a GPC with an odd number of SMs leaves one out).
 template <int kCols>
+int pairs_at_once() {
+  static int known[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (known[dev] == 0) {
+    using S = Shape<kCols, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * num_sms());
+    cfg.blockDim = dim3(S::threads);
+    cfg.dynamicSmemBytes = S::smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<kCols, true>, &cfg) != cudaSuccess || n < 1) return 0;
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
+template <int kCols, bool kPair>
 cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
-  using S = Shape<kCols>;
-  const long long slots = (long long)num_sms() * S::per_sm;
-  const int tiles_n = (g.N + kRows - 1) / kRows;
-  a.tiles_t = (g.T + kCols - 1) / kCols;
-  a.tn = ((g.T + a.tiles_t - 1) / a.tiles_t + 15) / 16 * 16;
+  using S = Shape<kCols, kPair>;
+  cudaError_t err =
+      cudaFuncSetAttribute(fp8_gemm_kernel<kCols, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
+  if (err != cudaSuccess) return err;
+  long long slots = (long long)num_sms() * S::per_sm;
+  if constexpr (kPair) slots = pairs_at_once<kCols>();
+  if (slots < 1) return cudaErrorInvalidConfiguration;
+  a.tiles_n = (g.N + S::tile_rows - 1) / S::tile_rows;
+  auto width = [&](int tiles_t) { return ((g.T + tiles_t - 1) / tiles_t + 15) / 16 * 16; };
+  const int least = (g.T + kCols - 1) / kCols;
+  int best = least;
+  if (S::wide) {
+    // the number of rounds of tiles times a tile's time: a few narrower tiles may fill the last round
+    long long cost = 0;
+    for (int n = least; n <= 2 * least + 2; ++n) {
+      const int tn = width(n), tiles_t = (g.T + tn - 1) / tn;
+      const long long c = ((long long)a.tiles_n * tiles_t + slots - 1) / slots * (tn + 16);
+      if (n == least || c < cost) {
+        cost = c;
+        best = n;
+      }
+    }
+  }
+  a.tn = width(best);
   a.tiles_t = (g.T + a.tn - 1) / a.tn;
-  a.tiles = (long long)tiles_n * a.tiles_t;
+  a.tiles = (long long)a.tiles_n * a.tiles_t;
   a.split = 1;
   // a cluster's CTAs share a tile where there are too few tiles; what they send each other is held in 32 KB
   if (!S::wide)
     while (a.split < 8 && a.split < a.pieces && a.tiles * a.split * 2 <= slots) a.split *= 2;
   if (a.split > 1 && a.tn > 8 * a.split) a.split = 1;
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
-  const int room = (S::smem - 1024 - kHeader - recv) / (kWBytes + a.tn * kStageK);
+  const int room = (S::smem - 1024 - kHeader - recv) / (kWBytes + a.tn / S::ctas * kStageK);
   a.stages = room < kMaxStages ? room : kMaxStages;
   CUtensorMap wmap, xmap;
-  if (!make_map(&wmap, g.w, g.N, g.K, kRows) || !make_map(&xmap, g.x, g.T, g.K, a.tn)) return cudaErrorInvalidValue;
-  const cudaError_t err =
-      cudaFuncSetAttribute(fp8_gemm_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
-  if (err != cudaSuccess) return err;
-  const long long grid = a.split > 1 ? a.tiles * a.split : a.tiles < slots ? a.tiles : slots;
+  if (!make_map(&wmap, g.w, g.N, g.K, kRows) || !make_map(&xmap, g.x, g.T, g.K, a.tn / S::ctas))
+    return cudaErrorInvalidValue;
+  const int ctas = kPair ? 2 : a.split;
+  const long long grid = a.split > 1 ? a.tiles * a.split : (a.tiles < slots ? a.tiles : slots) * ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(S::threads);
@@ -479,11 +677,11 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.split;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<kCols>, wmap, xmap, a);
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<kCols, kPair>, wmap, xmap, a);
 }
 
 }  // namespace
@@ -503,10 +701,10 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   a.piece = fp8_piece(g.K);
   a.pieces = (g.K + a.piece - 1) / a.piece;
   a.status = g.status;
-  if (g.T <= 16) return launch<16>(g, a, s);
-  if (g.T <= 32) return launch<32>(g, a, s);
-  if (g.T <= 64) return launch<64>(g, a, s);
-  return launch<kMaxTokens>(g, a, s);
+  if (g.T <= 16) return launch<16, false>(g, a, s);
+  if (g.T <= 32) return launch<32, false>(g, a, s);
+  if (g.T <= 64 || g.N <= kRows) return launch<64, false>(g, a, s);
+  return launch<kMaxTokens, true>(g, a, s);
 }
 
 }  // namespace moe
