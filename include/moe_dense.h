@@ -98,7 +98,7 @@ int moe_fp8_quantize_rows(const uint16_t* x, long long x_stride, int rows, int K
  * y_stride (elements, at least N; y aligned to its elements). The sum runs over up to eight pieces of K (512
  * ceil(K / 4096) values each), each in fp32 on the tensor cores, the pieces added in fp32 in
  * ascending order: the bits of a row of y depend on that row of x and on w
- * alone. K % 16 == 0, K <= 2^20, T and N < 2^24 (else MOE_ERR_SHAPE). */
+ * alone. K % 16 == 0, K <= 2^20, T and N < 2^24, T * N <= 2^38 (else MOE_ERR_SHAPE). */
 int moe_fp8_gemm(const moe_fp8_rows_t* x, int T, const moe_fp8_rows_t* w, int N, int K, void* y, long long y_stride,
                  int y_dtype, cudaStream_t stream);
 

@@ -83,7 +83,7 @@ int product_status(int T, const moe_fp8_rows_t* w, int N, int K, const void* y, 
   if (T < 0 || N < 0 || (!dtype_ok(y_dtype) && y_dtype != MOE_FP32)) return MOE_ERR_INVALID;
   const int st = k_status(K);
   if (st != MOE_OK) return st;
-  if (T > kFp8MaxRows || N > kFp8MaxRows) return MOE_ERR_SHAPE;
+  if (T > kFp8MaxRows || N > kFp8MaxRows || (long long)T * N > kFp8MaxResults) return MOE_ERR_SHAPE;
   if (T == 0 || N == 0) return MOE_OK;
   if (!rows_ok(w, N, K) || !y || misaligned(y, y_dtype == MOE_FP32 ? 4 : 2) || y_stride < 0 || (T > 1 && y_stride < N)) return MOE_ERR_INVALID;
   return MOE_OK;

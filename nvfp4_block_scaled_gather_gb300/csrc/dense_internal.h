@@ -15,6 +15,7 @@ constexpr int kFp8Block = 128;      // values that share a scale
 constexpr int kMaxNormDim = 16384;
 constexpr int kFp8MaxK = 1 << 20;
 constexpr int kFp8MaxRows = (1 << 24) - 1;
+constexpr long long kFp8MaxResults = 1LL << 38;  // tiles and the scale words of one CTA are counted in 32 bits
 
 // Bytes that the scales of a row of K values take: four scales a word.
 inline long long fp8_scale_bytes(long long K) { return 4 * ((K + 511) / 512); }

@@ -38,9 +38,10 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128;         // rows of w of a CTA's tile
-constexpr int kStageK = 128;       // values (bytes) of K of a stage: one scale block
-constexpr int kWBytes = kRows * kStageK;
-constexpr int kHeader = 1024;
+constexpr int kBlockK = 128;       // values (bytes) of K that share a scale: a row of a swizzled tile
+constexpr int kWBytes = kRows * kBlockK;
+constexpr int kScaleSlots = 4;     // words of scales on their way
+constexpr int kHeader = 1024 + kScaleSlots * 1536;
 constexpr int kMaxStages = 12;
 constexpr int kMaxTokens = 240;    // of a tile: two accumulators and the scales fill tensor memory
 
@@ -57,15 +58,19 @@ struct Shape {
   static constexpr int threads = 32 * warps;
   static constexpr int load_warp = 4 + 4 * groups, mma_warp = load_warp + 1;
   static constexpr int per_sm = wide ? 1 : 2;
+  // blocks of 128 values of K of a stage: a stage's waits and arrivals cost the issuing warp as much as four MMAs, so
+  // that with one block it could not keep the tensor cores busy (8192 x 10240 x 4096: 384 us)
+  static constexpr int deep = wide ? 2 : 1;
   static constexpr int asked = wide ? 32 : 16;                 // columns that are read from tensor memory together
   // registers a thread of the two warpgroups that hold sums and of the other two: 256 x 184 + 256 x 72 of the launch's 512 x 128
   static constexpr int many = wide ? 184 : 0, few = wide ? 72 : 0;
   static constexpr int smem = wide ? 232448 : 115712;          // 227 KB; half an SM's 228 KB less 1 KB each
   static constexpr int acc_cols = kCols;                       // of one accumulator
-  static constexpr int scale_bufs = wide ? 2 : 4;
-  static constexpr int xs_words = (kCols + 31) / 32;           // columns that the tokens' scales take
-  static constexpr int scale_cols = 16;                        // tokens' scales, then (at 8) those of w
-  static constexpr int tmem = wide ? 512 : 2 * acc_cols + scale_bufs * scale_cols <= 128 ? 128 : 256;
+  // a word of scales of 32 rows: a column of tensor memory; 128 rows: an atom of 512 bytes in shared memory
+  static constexpr int xs_words = (kCols + 31) / 32, xs_atoms = (xs_words + 3) / 4;
+  static constexpr int slot_bytes = (1 + xs_atoms) * 512;      // w's atom, then the tokens'
+  static constexpr int scale_cols = 16;                        // tokens' scales, then (at 8) those of w; two such
+  static constexpr int tmem = wide ? 512 : 2 * acc_cols + 2 * scale_cols <= 128 ? 128 : 256;
 };
 
 struct Args {
@@ -77,7 +82,7 @@ struct Args {
   int T, N, K;
   int tn;                 // tokens of a tile, a multiple of 16
   int tiles_n, tiles_t;
-  long long tiles;        // of w rows x tokens
+  int tiles;              // of w rows x tokens
   int split;              // CTAs of a cluster that share a tile
   int piece, pieces;      // values of K of a piece; pieces
   int stages;
@@ -120,23 +125,38 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// D (tensor memory) += A B over a block of 128 values of K, or its first 32 `steps`: 32 bytes of the tiles' rows, 2 in a
+// descriptor's address, each. The first step overwrites D where `accumulate` is 0.
+#define MOE_MMA_BLOCK(GROUP)                                                                                          \
+  if (steps == 4) {                                                                                                   \
+    asm volatile(                                                                                                     \
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"                                                                \
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"                                                          \
+        "tcgen05.mma.cta_group::" GROUP ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t" \
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"                                                                 \
+        "tcgen05.mma.cta_group::" GROUP ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%5], [%6], q;\n\t" \
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"                                                                 \
+        "tcgen05.mma.cta_group::" GROUP ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%5], [%6], q;\n\t" \
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"                                                                 \
+        "tcgen05.mma.cta_group::" GROUP ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%5], [%6], q;\n\t}\n" ::"r"(d), \
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)                                       \
+        : "memory");                                                                                                  \
+  } else {                                                                                                            \
+    for (int j = 0; j < steps; ++j, adesc += 2, bdesc += 2, accumulate = 1)                                           \
+      asm volatile(                                                                                                   \
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                                          \
+          "tcgen05.mma.cta_group::" GROUP ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d), \
+          "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)                                     \
+          : "memory");                                                                                                \
+  }
 template <bool kPair>
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                       uint32_t sfb, uint32_t accumulate) {
-  if constexpr (kPair)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
-        : "memory");
+__device__ __forceinline__ void tc_mma_block(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate, int steps) {
+  if constexpr (kPair) {
+    MOE_MMA_BLOCK("2")
+  } else {
+    MOE_MMA_BLOCK("1")
+  }
 }
 template <bool kPair>
 __device__ __forceinline__ void tc_alloc(uint32_t slot, uint32_t cols) {
@@ -160,24 +180,15 @@ __device__ __forceinline__ void tc_ld8(uint32_t taddr, uint32_t* r) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-__device__ __forceinline__ void tc_st1(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0]) : "memory");
-}
-__device__ __forceinline__ void tc_st2(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
-}
-__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ void tc_st4(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
+// An atom of 128 rows' scale words to four columns of tensor memory, all lane quarters alike (of a pair: in both CTAs).
+template <bool kPair>
+__device__ __forceinline__ void tc_copy_atom(uint32_t taddr, uint64_t desc) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // This warpgroup's registers a thread, up or down from the launch's 128.
 template <int kRegs>
 __device__ __forceinline__ void take_registers() {
@@ -205,20 +216,11 @@ __device__ __forceinline__ void st_peer(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// An arrival that may be on another CTA's barrier, and a wait for such ones.
+// An arrival that may be on another CTA's barrier. (What it tells of is in tensor memory, or in shared memory that the
+// other CTA's MMAs read through the async proxy: fences of those have come before it. With cluster scope it would wait
+// for all of the warp's loads and stores.)
 __device__ __forceinline__ void arrive_peer(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Shared-memory descriptor, K-major operand in the 128-byte swizzle: rows of
@@ -226,6 +228,11 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
 __device__ __forceinline__ uint64_t desc_kmajor(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Descriptor of an atom of scale words: 32 rows of 16 bytes (row r: those of rows r, 32 + r, 64 + r, 96 + r), no
+// swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_atom(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
 // Instruction descriptor, kind::mxf8f6f4: A and B e4m3 (format 0), K-major,
 // e8m0 scales, M = m, N = n; `byte` of each scale word is used.
@@ -248,16 +255,10 @@ struct Ctl {
   volatile int* abort_flag;
   int* status;
 };
-template <bool kCluster>
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
-  if constexpr (kCluster) return try_wait_cluster(bar, parity);
-  return mbar_try_wait(bar, parity);
-}
-template <bool kCluster>
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Ctl& c) {
   const long long t0 = clock64();
   while (true) {
-    if (try_wait<kCluster>(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*c.abort_flag) return false;
     if (clock64() - t0 > kWaitCycles) {
       *c.abort_flag = 1;
@@ -266,22 +267,29 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, const C
     }
   }
 }
-// By a whole warp, the same answer in every lane; kCluster: for arrivals of the other CTA too.
-template <bool kCluster = false>
+// By a whole warp, which goes on where the wait gave up (the flag is up then, and no later wait waits).
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, const Ctl& c) {
+  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, c);
+  __syncwarp();
+}
+// By a whole warp, the same answer in every lane. (Inlined: a kernel that moves registers between its warps makes no
+// calls. The other CTA's arrivals need no wider scope: what they tell of is in tensor memory, ordered by tcgen05
+// fences; a wait with cluster scope took 500 cycles when it had nothing to wait for.)
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Ctl& c) {
-  return __all_sync(~0u, try_wait<kCluster>(bar, parity) || wait_slow<kCluster>(bar, parity, c));
+  return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_slow(bar, parity, c));
 }
 
 // Tile i's place. Tiles that run at one time are eight rows of tiles of w high, so that both operands come from L2.
 struct Place {
   int n, t;
 };
-__device__ __forceinline__ Place place_of(long long i, const Args& a) {
+__device__ __forceinline__ Place place_of(int i, const Args& a) {
   constexpr int kHigh = 8;
-  const long long full = (long long)kHigh * a.tiles_t;
-  const int group = (int)(i / full), in = (int)(i - group * full);
-  const int high = min(kHigh, a.tiles_n - group * kHigh);
-  return {group * kHigh + in % high, in / high};
+  if (a.tiles_n <= kHigh) return {i % a.tiles_n, i / a.tiles_n};
+  const int full = kHigh * a.tiles_t;
+  const int group = i / full, in = i - group * full;
+  const int high = min(kHigh, a.tiles_n - group * kHigh), t = in / high;
+  return {group * kHigh + in - t * high, t};
 }
 
 __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
@@ -291,6 +299,24 @@ __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
   else
     static_cast<uint16_t*>(a.y)[at] =
         (uint16_t)(a.y_dtype == MOE_BF16 ? pack16x2<MOE_BF16>(v, 0.0f) : pack16x2<MOE_FP16>(v, 0.0f));
+}
+
+// One row of w's results for `there` tokens, a warp's lanes next to each other.
+template <int kAcc, typename To, typename Round>
+__device__ __forceinline__ void store_column(To* y, long long stride, const float (&sum)[kAcc], int there, Round round) {
+#pragma unroll
+  for (int c = 0; c < kAcc; c += 8) {
+    if (c >= there) break;
+    if (c + 8 <= there) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j * stride] = round(sum[c + j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < there) y[j * stride] = round(sum[c + j]);
+    }
+    y += 8 * stride;
+  }
 }
 
 template <int kCols, bool kPair>
@@ -310,10 +336,10 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   const uint32_t drain_bar = base + 8u * (2 * kMaxStages + 12);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 516);
-  const uint32_t s_w = base + kHeader, s_x = s_w + (uint32_t)a.stages * kWBytes;
-  const uint32_t x_bytes = (uint32_t)(a.tn / S::ctas) * kStageK;  // a stage's tokens in this CTA
+  const uint32_t s_scales = base + 1024, s_w = base + kHeader, s_x = s_w + (uint32_t)a.stages * S::deep * kWBytes;
+  const uint32_t x_bytes = (uint32_t)(a.tn / S::ctas) * kBlockK;  // a block's tokens in this CTA
   // the sums that this CTA's rows get from its cluster: [pieces][tokens][128 / split]
-  const uint32_t recv_off = kHeader + (uint32_t)a.stages * (kWBytes + x_bytes);
+  const uint32_t recv_off = kHeader + (uint32_t)a.stages * S::deep * (kWBytes + x_bytes);
   float* recv = reinterpret_cast<float*>(smem + recv_off);
 
   // (known to be the same over a warp: tensor-core and copy instructions take their operands from uniform registers)
@@ -323,7 +349,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int i = 0; i < S::scale_bufs; ++i) {
+    for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(sfull_bar(i), 4 * S::ctas);
       mbar_init(sempty_bar(i), 1);
     }
@@ -342,80 +368,88 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   }
   const int ctas = kPair ? 2 : a.split;  // of a cluster
   const int rank = ctas > 1 ? (int)cluster_rank() : 0;
-  const long long first = blockIdx.x / ctas, step = gridDim.x / ctas;
+  const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
   const int per = (a.pieces + a.split - 1) / a.split;
   const int p0 = kPair ? 0 : min(a.pieces, rank * per), p1 = kPair ? a.pieces : min(a.pieces, p0 + per);
   const int half = kPair ? rank : 0;  // which of a pair
   // blocks of 128 values of K: all of them, and this CTA's
-  const int blocks = (a.K + kStageK - 1) / kStageK, per_piece = a.piece / kStageK;
+  const int blocks = (a.K + kBlockK - 1) / kBlockK, per_piece = a.piece / kBlockK;
   const int b0 = min(blocks, p0 * per_piece), b1 = min(blocks, p1 * per_piece);
   if (warp == S::load_warp && lane == 0) {
     tma_prefetch_map(&wmap);
     tma_prefetch_map(&xmap);
     // the rows of w may be those that the kernel before this one writes: they are asked for in L2 only
     if (first < a.tiles)
-      for (int b = b0; b < b1 && b < b0 + a.stages; ++b)
-        tma_prefetch_l2(&wmap, b * kStageK, place_of(first, a).n * S::tile_rows + half * kRows);
+      for (int b = b0; b < b1 && b < b0 + a.stages * S::deep; ++b)
+        tma_prefetch_l2(&wmap, b * kBlockK, place_of(first, a).n * S::tile_rows + half * kRows);
   }
   __syncthreads();
   tc_fence_after();
   __syncwarp();
   if (ctas > 1) cluster_sync();  // peers have begun, their barriers are set up
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(~0u, *tmem_slot, 0);
   const Ctl ctl{abort_flag, a.status};
   pdl_wait();
   pdl_trigger();
 
   if (warp < 4) {
     if constexpr (S::wide) give_registers<S::few>();
-    // ============================ scales to tensor memory ============================
-    // Lane l of each warp has rows l, 32 + l, ...: column c of its quarter takes row 32 c + l's word. The next words
-    // are asked for before the present ones wait for their buffer.
+    // ================================ scale words ================================
+    // Group g of 32 rows is warp g % 4's: w's rows, then the tokens'. A lane has a row's word, in its place of the atom
+    // that the MMA warp copies to tensor memory. (Stores from here to tensor memory wait for the MMAs that are queued.)
+    // Words are asked for kAhead ahead, each set in registers of its own (moving them would wait for them).
+    constexpr int kMine = (4 + S::xs_words + 3) / 4;
     struct Words {
-      uint32_t w[4], x[S::xs_words];
+      uint32_t v[kMine];
     };
-    auto load = [&](long long i, int b) {
-      Words r;
+    constexpr int kAhead = 4;
+    Words q[kAhead];
+    int i = b0 < b1 ? first : a.tiles, b = b0;  // of the next words to ask for
+    const uint8_t* from[kMine];                 // this lane's rows' scales, or none
+    auto enter = [&] {
       const Place at = place_of(i, a);
-      const int n0 = at.n * S::tile_rows + half * kRows + lane, t0 = at.t * a.tn + lane;
-      const uint8_t *w = a.ws + n0 * a.ws_stride + b, *x = a.xs + t0 * a.xs_stride + b;
+      const int n = at.n * S::tile_rows + half * kRows + 32 * warp + lane;
+      from[0] = n < a.N ? a.ws + n * a.ws_stride : nullptr;
 #pragma unroll
-      for (int c = 0; c < 4; ++c, w += 32 * a.ws_stride)
-        r.w[c] = n0 + 32 * c < a.N ? ld_cg(reinterpret_cast<const uint32_t*>(w)) : 0u;
-#pragma unroll
-      for (int c = 0; c < S::xs_words; ++c, x += 32 * a.xs_stride)
-        r.x[c] = 32 * c < a.tn && t0 + 32 * c < a.T ? ld_cg(reinterpret_cast<const uint32_t*>(x)) : 0u;
-      return r;
+      for (int c = 1; c < kMine; ++c) {
+        const int first_row = 32 * (warp + 4 * (c - 1)), t = at.t * a.tn + first_row + lane;
+        from[c] = first_row < a.tn && t < a.T ? a.xs + t * a.xs_stride : nullptr;
+      }
     };
-    if (first < a.tiles && b0 < b1) {
-      Words now = load(first, b0);
-      long long i = first;
-      int b = b0;
-      for (uint32_t n = 0;; ++n) {
-        b += 4;
-        if (b >= b1) {
-          b = b0;
-          i += step;
-        }
-        Words next = now;
-        if (i < a.tiles) next = load(i, b);
-        const int buf = n % S::scale_bufs;
-        if (!wait_warp(sempty_bar(buf), ((n / S::scale_bufs) & 1) ^ 1u, ctl)) break;
-        tc_fence_after();
-        const uint32_t col = tmem + ((uint32_t)(warp * 32) << 16) + 2 * S::acc_cols + buf * S::scale_cols;
-        tc_st4(col + 8, now.w);
-        if constexpr (S::xs_words == 8) tc_st8(col, now.x);
-        else if constexpr (S::xs_words == 2) tc_st2(col, now.x);
-        else tc_st1(col, now.x);
-        tc_wait_st();
-        tc_fence_before();
+    auto ask = [&](Words& r) {
+      if (i >= a.tiles) return;
+#pragma unroll
+      for (int c = 0; c < kMine; ++c) r.v[c] = from[c] ? ld_cg(reinterpret_cast<const uint32_t*>(from[c] + b)) : 0u;
+      b += 4;
+      if (b >= b1) {
+        b = b0;
+        i += step;
+        if (i < a.tiles) enter();
+      }
+    };
+    if (i < a.tiles) enter();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) ask(q[u]);
+    const int words = (b1 - b0 + 3) / 4;
+    const uint32_t mine = first < a.tiles ? (uint32_t)((a.tiles - first + step - 1) / step * words) : 0u;
+    bool ok = true;
+    for (uint32_t n = 0; n < mine && ok;) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u, ++n) {
+        if (n >= mine) break;
+        const int slot = n % kScaleSlots;
+        ok = wait_warp(sempty_bar(slot), ((n / kScaleSlots) & 1) ^ 1u, ctl);
+        if (!ok) break;
+        uint8_t* atoms = smem + 1024 + slot * S::slot_bytes + lane * 16 + warp * 4;
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint32_t*>(atoms + c * 512) = q[u].v[c];
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          if constexpr (kPair) arrive_peer(peer(sfull_bar(buf), 0));
-          else mbar_arrive(sfull_bar(buf));
+          if constexpr (kPair) arrive_peer(peer(sfull_bar(slot), 0));
+          else mbar_arrive(sfull_bar(slot));
         }
-        if (i >= a.tiles) break;
-        now = next;
+        ask(q[u]);
       }
     }
   } else if (warp >= S::load_warp) {
@@ -428,18 +462,23 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
       bool ok = true;
       int stage = 0;
       uint32_t phase = 0;
-      for (long long i = first; i < a.tiles && ok; i += step) {
+      for (int i = first; i < a.tiles && ok; i += step) {
         const Place at = place_of(i, a);
         const int n0 = at.n * S::tile_rows + half * kRows, t0 = at.t * a.tn + half * (a.tn / 2);
-        for (int b = b0; b < b1; ++b, ++n) {
+        for (int b = b0; b < b1; b += S::deep, ++n) {
           ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
           if (!ok) break;
           if (elect_one()) {
+            const int here = min(S::deep, b1 - b);
             // a pair's loads are all counted by the first CTA, whose MMAs read both CTAs' stages
             const uint32_t bar = kPair ? peer(full_bar(stage), 0) : full_bar(stage);
-            if (half == 0) mbar_expect_tx(full_bar(stage), S::ctas * (kWBytes + x_bytes));
-            tma_load<kPair>(s_w + stage * kWBytes, &wmap, b * kStageK, n0, bar);
-            tma_load<kPair>(s_x + stage * x_bytes, &xmap, b * kStageK, t0, bar);
+            if (half == 0) mbar_expect_tx(full_bar(stage), S::ctas * here * (kWBytes + x_bytes));
+#pragma unroll
+            for (int h = 0; h < S::deep; ++h) {
+              if (h >= here) break;
+              tma_load<kPair>(s_w + (stage * S::deep + h) * kWBytes, &wmap, (b + h) * kBlockK, n0, bar);
+              tma_load<kPair>(s_x + (stage * S::deep + h) * x_bytes, &xmap, (b + h) * kBlockK, t0, bar);
+            }
           }
           __syncwarp();
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
@@ -458,37 +497,48 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
     } else if (warp == S::mma_warp && half == 0) {
       // ==================================== MMAs ====================================
       const uint32_t idesc = idesc_mxf8(S::tile_rows, a.tn);
+      const uint64_t w_desc = desc_kmajor(s_w), x_desc = desc_kmajor(s_x), atom_desc = desc_atom(s_scales);
       int stage = 0;
       uint32_t phase = 0, ns = 0, na = 0;
       bool ok = true;
-      for (long long i = first; i < a.tiles && ok; i += step) {
+      for (int i = first; i < a.tiles && ok; i += step) {
         for (int p = p0; p < p1 && ok; ++p, ++na) {
-          ok = wait_warp<kPair>(aempty_bar(na & 1), ((na >> 1) & 1) ^ 1u, ctl);
+          ok = wait_warp(aempty_bar(na & 1), ((na >> 1) & 1) ^ 1u, ctl);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + (na & 1) * S::acc_cols;
           const int begin = p * per_piece, end = min(b1, begin + per_piece);
-          for (int b = begin; b < end; ++b) {
-            const int buf = ns % S::scale_bufs;
+          for (int b = begin; b < end; b += S::deep) {
+            const int slot = ns % kScaleSlots;
+            const uint32_t col = tmem + 2 * S::acc_cols + (ns & 1) * S::scale_cols;
             if ((b & 3) == 0) {
-              ok = wait_warp<kPair>(sfull_bar(buf), (ns / S::scale_bufs) & 1, ctl);
-              if (!ok) break;
-            }
-            ok = wait_warp<kPair>(full_bar(stage), phase, ctl);
-            if (!ok) break;
-            tc_fence_after();
-            const bool word_done = (b & 3) == 3 || b + 1 == end;
-            if (elect_one()) {
-              const uint32_t col = tmem + 2 * S::acc_cols + buf * S::scale_cols;
-              const uint64_t wd = desc_kmajor(s_w + stage * kWBytes), xd = desc_kmajor(s_x + stage * x_bytes);
-              const uint32_t id = with_byte(idesc, b & 3);
-              const int left = a.K - b * kStageK;
+              // the word before the last one was in these columns
+              if (ns >= 2) wait_on(sempty_bar((ns - 2) % kScaleSlots), ((ns - 2) / kScaleSlots) & 1, ctl);
+              wait_on(sfull_bar(slot), (ns / kScaleSlots) & 1, ctl);
+              if (elect_one()) {
+                const uint64_t from = atom_desc + (uint64_t)(slot * (S::slot_bytes >> 4));
+                tc_copy_atom<kPair>(col + 8, from);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)  // 32 bytes on: 2 in a descriptor's address
-                if (32 * j < left) tc_mma<kPair>(d, wd + 2 * j, xd + 2 * j, id, col + 8, col, b > begin || j > 0);
+                for (int c = 0; c < S::xs_atoms; ++c) tc_copy_atom<kPair>(col + 4 * c, from + 32 * (c + 1));
+              }
+              __syncwarp();
+            }
+            wait_on(full_bar(stage), phase, ctl);
+            tc_fence_after();
+            const bool done = b + S::deep >= end;  // of the piece
+            const bool word_done = ((b + S::deep) & 3) == 0 || done;
+            if (elect_one()) {
+#pragma unroll
+              for (int h = 0; h < S::deep; ++h) {
+                if (b + h >= end) break;
+                tc_mma_block<kPair>(d, w_desc + (uint64_t)((stage * S::deep + h) * (kWBytes >> 4)),
+                                    x_desc + (uint64_t)((stage * S::deep + h) * (x_bytes >> 4)),
+                                    with_byte(idesc, (b + h) & 3), col + 8, col, b + h > begin,
+                                    min(4, (a.K - (b + h) * kBlockK + 31) / 32));
+              }
               tc_commit<kPair>(empty_bar(stage));
-              if (word_done) tc_commit<kPair>(sempty_bar(buf));
-              if (b + 1 == end) tc_commit<kPair>(afull_bar(na & 1));
+              if (word_done) tc_commit<kPair>(sempty_bar(slot));
+              if (done) tc_commit<kPair>(afull_bar(na & 1));
             }
             __syncwarp();
             if (word_done) ++ns;
@@ -514,7 +564,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + c0;
     uint32_t na = 0;
     bool ok = true;
-    for (long long i = first; i < a.tiles && ok; i += step) {
+    for (int i = first; i < a.tiles && ok; i += step) {
       const Place at = place_of(i, a);
       const int n = at.n * S::tile_rows + half * kRows + row, t0 = at.t * a.tn + c0;
       float sum[S::acc];
@@ -557,9 +607,16 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
         }
       }
       if (ok && a.split == 1 && n < a.N) {
-#pragma unroll
-        for (int c = 0; c < S::acc; ++c)
-          if (c < mine && t0 + c < a.T) store_y(a, t0 + c, n, sum[c]);
+        const int there = min(mine, a.T - t0);  // tokens
+        if (a.y_dtype == MOE_FP32)
+          store_column<S::acc>(static_cast<float*>(a.y) + (long long)t0 * a.y_stride + n, a.y_stride, sum, there,
+                               [](float v) { return v; });
+        else if (a.y_dtype == MOE_BF16)
+          store_column<S::acc>(static_cast<uint16_t*>(a.y) + (long long)t0 * a.y_stride + n, a.y_stride, sum, there,
+                               [](float v) { return (uint16_t)pack16x2<MOE_BF16>(v, 0.0f); });
+        else
+          store_column<S::acc>(static_cast<uint16_t*>(a.y) + (long long)t0 * a.y_stride + n, a.y_stride, sum, there,
+                               [](float v) { return (uint16_t)pack16x2<MOE_FP16>(v, 0.0f); });
       }
     }
   }
@@ -595,7 +652,7 @@ bool make_map(CUtensorMap* map, const moe_fp8_rows_t& m, int rows, int K, int bo
   if (!encode) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? m.row_stride : K)};
-  const cuuint32_t box[2] = {kStageK, (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {kBlockK, (cuuint32_t)box_rows};
   const cuuint32_t steps[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m.codes, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
@@ -654,20 +711,20 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   }
   a.tn = width(best);
   a.tiles_t = (g.T + a.tn - 1) / a.tn;
-  a.tiles = (long long)a.tiles_n * a.tiles_t;
+  a.tiles = a.tiles_n * a.tiles_t;
   a.split = 1;
   // a cluster's CTAs share a tile where there are too few tiles; what they send each other is held in 32 KB
   if (!S::wide)
     while (a.split < 8 && a.split < a.pieces && a.tiles * a.split * 2 <= slots) a.split *= 2;
   if (a.split > 1 && a.tn > 8 * a.split) a.split = 1;
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
-  const int room = (S::smem - 1024 - kHeader - recv) / (kWBytes + a.tn / S::ctas * kStageK);
+  const int room = (S::smem - 1024 - kHeader - recv) / (S::deep * (kWBytes + a.tn / S::ctas * kBlockK));
   a.stages = room < kMaxStages ? room : kMaxStages;
   CUtensorMap wmap, xmap;
   if (!make_map(&wmap, g.w, g.N, g.K, kRows) || !make_map(&xmap, g.x, g.T, g.K, a.tn / S::ctas))
     return cudaErrorInvalidValue;
   const int ctas = kPair ? 2 : a.split;
-  const long long grid = a.split > 1 ? a.tiles * a.split : (a.tiles < slots ? a.tiles : slots) * ctas;
+  const long long grid = a.split > 1 ? (long long)a.tiles * a.split : (a.tiles < slots ? a.tiles : slots) * ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(S::threads);
