@@ -40,9 +40,9 @@ namespace {
 constexpr int kRows = 128;         // rows of w of a CTA's tile
 constexpr int kBlockK = 128;       // values (bytes) of K that share a scale: a row of a swizzled tile
 constexpr int kWBytes = kRows * kBlockK;
-constexpr int kScaleSlots = 4;     // words of scales on their way
+constexpr int kScaleSlots = 2;     // words of scales on their way
 constexpr int kHeader = 1024 + kScaleSlots * 1536;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 5;
 constexpr int kMaxTokens = 240;    // of a tile: two accumulators and the scales fill tensor memory
 
 // kCols: tokens of a tile at most. kPair: two CTAs share a tile of 256 rows of
@@ -61,6 +61,10 @@ struct Shape {
   // blocks of 128 values of K of a stage: a stage's waits and arrivals cost the issuing warp as much as four MMAs, so
   // that with one block it could not keep the tensor cores busy (8192 x 10240 x 4096: 384 us)
   static constexpr int deep = wide ? 2 : 1;
+  // A word of scales is four blocks: so many stages. The columns that a word's scales are copied to were those of the
+  // word before the last one, whose MMAs have to be done: they are where the ring has come round to a word's first
+  // stage, if it has no more stages than a word and one more.
+  static constexpr int word_stages = 4 / deep, most_stages = word_stages + 1;
   static constexpr int asked = wide ? 32 : 16;                 // columns that are read from tensor memory together
   // registers a thread of the two warpgroups that hold sums and of the other two: 256 x 184 + 256 x 72 of the launch's 512 x 128
   static constexpr int many = wide ? 184 : 0, few = wide ? 72 : 0;
@@ -79,6 +83,7 @@ struct Args {
   void* y;
   long long y_stride;
   int y_dtype;
+  int pairs;              // 16-bit results of two rows of w can be written together
   int T, N, K;
   int tn;                 // tokens of a tile, a multiple of 16
   int tiles_n, tiles_t;
@@ -318,6 +323,27 @@ __device__ __forceinline__ void store_column(To* y, long long stride, const floa
     y += 8 * stride;
   }
 }
+// The same for 16-bit results two rows of w at a time (N and the stride even, y 4-byte aligned): lanes 2 l and 2 l + 1
+// exchange, the even one then has both rows' results for tokens 0, 2, ..., the odd one for 1, 3, ... By the whole warp;
+// `in`: this lane's row is one of w's.
+template <int kAcc, int kType>
+__device__ __forceinline__ void store_pairs(uint16_t* y, long long stride, const float (&sum)[kAcc], int there, bool in,
+                                            int lane) {
+  const bool odd = lane & 1;
+  y += odd ? stride - 1 : 0;
+#pragma unroll
+  for (int c = 0; c < kAcc; c += 8) {
+    if (c >= there) break;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float mine = odd ? sum[c + j + 1] : sum[c + j];
+      const float other = __shfl_xor_sync(~0u, odd ? sum[c + j] : sum[c + j + 1], 1);
+      const uint32_t v = pack16x2<kType>(odd ? other : mine, odd ? mine : other);
+      if (in && c + j + (odd ? 1 : 0) < there) *reinterpret_cast<uint32_t*>(y + j * stride) = v;
+    }
+    y += 8 * stride;
+  }
+}
 
 template <int kCols, bool kPair>
 __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPair>::per_sm)
@@ -329,11 +355,9 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   const uint32_t base = smem_u32(smem);
   auto full_bar = [&](int s) { return base + 8u * s; };
   auto empty_bar = [&](int s) { return base + 8u * (kMaxStages + s); };
-  auto sfull_bar = [&](int i) { return base + 8u * (2 * kMaxStages + i); };
-  auto sempty_bar = [&](int i) { return base + 8u * (2 * kMaxStages + 4 + i); };
-  auto afull_bar = [&](int i) { return base + 8u * (2 * kMaxStages + 8 + i); };
-  auto aempty_bar = [&](int i) { return base + 8u * (2 * kMaxStages + 10 + i); };
-  const uint32_t drain_bar = base + 8u * (2 * kMaxStages + 12);
+  auto afull_bar = [&](int i) { return base + 8u * (2 * kMaxStages + i); };
+  auto aempty_bar = [&](int i) { return base + 8u * (2 * kMaxStages + 2 + i); };
+  const uint32_t drain_bar = base + 8u * (2 * kMaxStages + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 516);
   const uint32_t s_scales = base + 1024, s_w = base + kHeader, s_x = s_w + (uint32_t)a.stages * S::deep * kWBytes;
@@ -346,12 +370,8 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full_bar(s), 1);
+      mbar_init(full_bar(s), 1 + 4 * S::ctas);  // the tiles' bytes, and the warps that bring scales
       mbar_init(empty_bar(s), 1);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(sfull_bar(i), 4 * S::ctas);
-      mbar_init(sempty_bar(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(afull_bar(i), 1);
@@ -375,6 +395,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   // blocks of 128 values of K: all of them, and this CTA's
   const int blocks = (a.K + kBlockK - 1) / kBlockK, per_piece = a.piece / kBlockK;
   const int b0 = min(blocks, p0 * per_piece), b1 = min(blocks, p1 * per_piece);
+  const int b2 = b0 + (b1 - b0 + 3) / 4 * 4;  // in whole words: the last stages may be empty
   if (warp == S::load_warp && lane == 0) {
     tma_prefetch_map(&wmap);
     tma_prefetch_map(&xmap);
@@ -430,25 +451,32 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
     if (i < a.tiles) enter();
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) ask(q[u]);
-    const int words = (b1 - b0 + 3) / 4;
-    const uint32_t mine = first < a.tiles ? (uint32_t)((a.tiles - first + step - 1) / step * words) : 0u;
+    const uint32_t mine = first < a.tiles ? (uint32_t)((a.tiles - first + step - 1) / step * ((b2 - b0) / 4)) : 0u;
+    int stage = 0;
+    uint32_t phase = 0;
     bool ok = true;
     for (uint32_t n = 0; n < mine && ok;) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u, ++n) {
         if (n >= mine) break;
-        const int slot = n % kScaleSlots;
-        ok = wait_warp(sempty_bar(slot), ((n / kScaleSlots) & 1) ^ 1u, ctl);
-        if (!ok) break;
-        uint8_t* atoms = smem + 1024 + slot * S::slot_bytes + lane * 16 + warp * 4;
+        for (int j = 0; j < S::word_stages; ++j) {
+          ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
+          if (!ok) break;
+          if (j == 0) {
+            // (the copies of the word before the last one, from this slot, are done as its MMAs are)
+            uint8_t* atoms = smem + 1024 + (n % kScaleSlots) * S::slot_bytes + lane * 16 + warp * 4;
 #pragma unroll
-        for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint32_t*>(atoms + c * 512) = q[u].v[c];
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair) arrive_peer(peer(sfull_bar(slot), 0));
-          else mbar_arrive(sfull_bar(slot));
+            for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint32_t*>(atoms + c * 512) = q[u].v[c];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          if (lane == 0) {
+            if constexpr (kPair) arrive_peer(peer(full_bar(stage), 0));
+            else mbar_arrive(full_bar(stage));
+          }
+          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
+        if (!ok) break;
         ask(q[u]);
       }
     }
@@ -465,14 +493,14 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
       for (int i = first; i < a.tiles && ok; i += step) {
         const Place at = place_of(i, a);
         const int n0 = at.n * S::tile_rows + half * kRows, t0 = at.t * a.tn + half * (a.tn / 2);
-        for (int b = b0; b < b1; b += S::deep, ++n) {
+        for (int b = b0; b < b2; b += S::deep, ++n) {
           ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
           if (!ok) break;
           if (elect_one()) {
-            const int here = min(S::deep, b1 - b);
+            const int here = min(S::deep, b1 - b);  // (none: only the arrival)
             // a pair's loads are all counted by the first CTA, whose MMAs read both CTAs' stages
             const uint32_t bar = kPair ? peer(full_bar(stage), 0) : full_bar(stage);
-            if (half == 0) mbar_expect_tx(full_bar(stage), S::ctas * here * (kWBytes + x_bytes));
+            if (half == 0) mbar_expect_tx(full_bar(stage), S::ctas * max(here, 0) * (kWBytes + x_bytes));
 #pragma unroll
             for (int h = 0; h < S::deep; ++h) {
               if (h >= here) break;
@@ -507,41 +535,36 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + (na & 1) * S::acc_cols;
-          const int begin = p * per_piece, end = min(b1, begin + per_piece);
-          for (int b = begin; b < end; b += S::deep) {
-            const int slot = ns % kScaleSlots;
+          const int begin = p * per_piece, end = min(b1, begin + per_piece), whole = begin + (end - begin + 3) / 4 * 4;
+          for (int b = begin; b < whole; b += S::deep) {
             const uint32_t col = tmem + 2 * S::acc_cols + (ns & 1) * S::scale_cols;
-            if ((b & 3) == 0) {
-              // the word before the last one was in these columns
-              if (ns >= 2) wait_on(sempty_bar((ns - 2) % kScaleSlots), ((ns - 2) / kScaleSlots) & 1, ctl);
-              wait_on(sfull_bar(slot), (ns / kScaleSlots) & 1, ctl);
-              if (elect_one()) {
-                const uint64_t from = atom_desc + (uint64_t)(slot * (S::slot_bytes >> 4));
+            wait_on(full_bar(stage), phase, ctl);
+            tc_fence_after();
+            if (elect_one()) {
+              if ((b & 3) == 0) {
+                const uint64_t from = atom_desc + (uint64_t)((ns % kScaleSlots) * (S::slot_bytes >> 4));
                 tc_copy_atom<kPair>(col + 8, from);
 #pragma unroll
                 for (int c = 0; c < S::xs_atoms; ++c) tc_copy_atom<kPair>(col + 4 * c, from + 32 * (c + 1));
               }
-              __syncwarp();
-            }
-            wait_on(full_bar(stage), phase, ctl);
-            tc_fence_after();
-            const bool done = b + S::deep >= end;  // of the piece
-            const bool word_done = ((b + S::deep) & 3) == 0 || done;
-            if (elect_one()) {
+              const uint64_t wd = w_desc + (uint64_t)(stage * S::deep * (kWBytes >> 4));
+              const uint64_t xd = x_desc + (uint64_t)(stage * S::deep * (x_bytes >> 4));
+              const uint32_t id = with_byte(idesc, b & 3);
+              if ((b + S::deep) * kBlockK <= a.K) {
 #pragma unroll
-              for (int h = 0; h < S::deep; ++h) {
-                if (b + h >= end) break;
-                tc_mma_block<kPair>(d, w_desc + (uint64_t)((stage * S::deep + h) * (kWBytes >> 4)),
-                                    x_desc + (uint64_t)((stage * S::deep + h) * (x_bytes >> 4)),
-                                    with_byte(idesc, (b + h) & 3), col + 8, col, b + h > begin,
-                                    min(4, (a.K - (b + h) * kBlockK + 31) / 32));
+                for (int h = 0; h < S::deep; ++h)
+                  tc_mma_block<kPair>(d, wd + h * (kWBytes >> 4), xd + h * (x_bytes >> 4), id + h * with_byte(0, 1), col + 8,
+                                      col, b + h > begin, 4);
+              } else {  // the end of K
+                for (int h = 0; b + h < end && h < S::deep; ++h)
+                  tc_mma_block<kPair>(d, wd + h * (kWBytes >> 4), xd + h * (x_bytes >> 4), id + h * with_byte(0, 1), col + 8,
+                                      col, b + h > begin, min(4, (a.K - (b + h) * kBlockK + 31) / 32));
               }
               tc_commit<kPair>(empty_bar(stage));
-              if (word_done) tc_commit<kPair>(sempty_bar(slot));
-              if (done) tc_commit<kPair>(afull_bar(na & 1));
+              if (b + S::deep >= whole) tc_commit<kPair>(afull_bar(na & 1));
             }
             __syncwarp();
-            if (word_done) ++ns;
+            if (((b + S::deep) & 3) == 0) ++ns;
             if (++stage == a.stages) { stage = 0; phase ^= 1u; }
           }
         }
@@ -606,17 +629,21 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
           else mbar_arrive(freed + 8u * (na & 1));
         }
       }
-      if (ok && a.split == 1 && n < a.N) {
-        const int there = min(mine, a.T - t0);  // tokens
-        if (a.y_dtype == MOE_FP32)
-          store_column<S::acc>(static_cast<float*>(a.y) + (long long)t0 * a.y_stride + n, a.y_stride, sum, there,
-                               [](float v) { return v; });
-        else if (a.y_dtype == MOE_BF16)
-          store_column<S::acc>(static_cast<uint16_t*>(a.y) + (long long)t0 * a.y_stride + n, a.y_stride, sum, there,
-                               [](float v) { return (uint16_t)pack16x2<MOE_BF16>(v, 0.0f); });
+      if (!ok || (!S::wide && a.split > 1)) continue;
+      const int there = min(mine, a.T - t0);  // tokens
+      const long long at_y = (long long)t0 * a.y_stride + n;
+      uint16_t* y16 = static_cast<uint16_t*>(a.y) + at_y;
+      if (a.y_dtype == MOE_FP32) {
+        if (n < a.N)
+          store_column<S::acc>(static_cast<float*>(a.y) + at_y, a.y_stride, sum, there, [](float v) { return v; });
+      } else if (a.pairs) {
+        if (a.y_dtype == MOE_BF16) store_pairs<S::acc, MOE_BF16>(y16, a.y_stride, sum, there, n < a.N, lane);
+        else store_pairs<S::acc, MOE_FP16>(y16, a.y_stride, sum, there, n < a.N, lane);
+      } else if (n < a.N) {
+        if (a.y_dtype == MOE_BF16)
+          store_column<S::acc>(y16, a.y_stride, sum, there, [](float v) { return (uint16_t)pack16x2<MOE_BF16>(v, 0.0f); });
         else
-          store_column<S::acc>(static_cast<uint16_t*>(a.y) + (long long)t0 * a.y_stride + n, a.y_stride, sum, there,
-                               [](float v) { return (uint16_t)pack16x2<MOE_FP16>(v, 0.0f); });
+          store_column<S::acc>(y16, a.y_stride, sum, there, [](float v) { return (uint16_t)pack16x2<MOE_FP16>(v, 0.0f); });
       }
     }
   }
@@ -698,11 +725,12 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   const int least = (g.T + kCols - 1) / kCols;
   int best = least;
   if (S::wide) {
-    // the number of rounds of tiles times a tile's time: a few narrower tiles may fill the last round
+    // the number of rounds of tiles times a tile's time (its MMAs, and what each stage and its end cost beside them):
+    // more and narrower tiles may fill the last round
     long long cost = 0;
     for (int n = least; n <= 2 * least + 2; ++n) {
       const int tn = width(n), tiles_t = (g.T + tn - 1) / tn;
-      const long long c = ((long long)a.tiles_n * tiles_t + slots - 1) / slots * (tn + 16);
+      const long long c = ((long long)a.tiles_n * tiles_t + slots - 1) / slots * (tn + 200);
       if (n == least || c < cost) {
         cost = c;
         best = n;
@@ -719,7 +747,7 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   if (a.split > 1 && a.tn > 8 * a.split) a.split = 1;
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
   const int room = (S::smem - 1024 - kHeader - recv) / (S::deep * (kWBytes + a.tn / S::ctas * kBlockK));
-  a.stages = room < kMaxStages ? room : kMaxStages;
+  a.stages = room < S::most_stages ? room : S::most_stages;
   CUtensorMap wmap, xmap;
   if (!make_map(&wmap, g.w, g.N, g.K, kRows) || !make_map(&xmap, g.x, g.T, g.K, a.tn / S::ctas))
     return cudaErrorInvalidValue;
@@ -752,6 +780,7 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   a.y = g.y;
   a.y_stride = g.y_stride;
   a.y_dtype = g.y_dtype;
+  a.pairs = g.y_dtype != MOE_FP32 && g.N % 2 == 0 && g.y_stride % 2 == 0 && reinterpret_cast<uintptr_t>(g.y) % 4 == 0;
   a.T = g.T;
   a.N = g.N;
   a.K = g.K;
