@@ -1,160 +1,169 @@
 // The residual stream's step between two blocks (moe_residual_norm):
 //   b = norm(block) w_post,  y = x + scale gate b,  normed = norm(y) w_pre
 // with norm(v) = v / sqrt(mean(v^2) + eps), in one pass: a row is read once,
-// kept in registers as fp32 over both sums of squares, and written once.
+// kept in registers over both sums of squares, and written once. Bound by
+// bytes (a row of 4096 moves 32 KB for 50,000 operations).
+//
+// A sum of squares is: eight values, a tree over the 32 threads that have 256
+// values together, and a tree over those sums (for rows of more). It does not depend on how a launch spreads rows over threads, so a
+// row's bits are the same in every call.
+//
+//  * Rows of at most 256: 8, 16 or 32 threads a row, several rows a thread in
+//    flight (the heads of queries and keys).
+//  * Longer rows, few of them (decode): a CTA a row, eight values a thread,
+//    everything asked for at once.
+//  * Longer rows, many of them: CTAs stay and take row after row, the next
+//    one's values on their way while the present one is worked on; the norms'
+//    weights wait in shared memory (read from L2 for every row they would be
+//    as many bytes again).
 #include <cstdint>
 
 #include <cuda_runtime.h>
 
 #include "dense_internal.h"
 #include "fp8_codec.cuh"
+#include "internal.h"
 #include "ldcg.cuh"
 #include "pdl.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRowThreads = 256;  // of a CTA whose rows have 8, 16 or 32 threads each
+constexpr int kSmallThreads = 256;
 
+// Eight fp32 values in pairs: one instruction multiplies or adds both of a pair.
+struct F8 {
+  uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t x) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(x));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 template <int kType>
-__device__ __forceinline__ void unpack8(const uint4& p, float* v) {
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+__device__ __forceinline__ F8 unpack8(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  F8 f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<kType>(w[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    const float2 u = unpack2<kType>(w[i]);
+    f.p[i] = pair_of(u.x, u.y);
   }
+  return f;
 }
 template <int kType>
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack16x2<kType>(v[0], v[1]), pack16x2<kType>(v[2], v[3]), pack16x2<kType>(v[4], v[5]),
-                    pack16x2<kType>(v[6], v[7]));
-}
-
-// Sum over a row's threads: G of a warp, or all of a CTA (G == 0).
-template <int G>
-__device__ __forceinline__ float row_sum(float s, float* shared) {
-  constexpr int width = G == 0 ? 32 : G;
+__device__ __forceinline__ uint4 pack8(const F8& f) {
+  uint32_t w[4];
 #pragma unroll
-  for (int o = 1; o < width; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
-  if constexpr (G == 0) {
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = shared[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) s += shared[w];
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = split(f.p[i]);
+    w[i] = pack16x2<kType>(u.x, u.y);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ F8 times(const F8& f, uint64_t by) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = mul2(f.p[i], by);
+  return r;
+}
+__device__ __forceinline__ F8 times(const F8& f, const F8& by) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = mul2(f.p[i], by.p[i]);
+  return r;
+}
+__device__ __forceinline__ float squares(const F8& f) {
+  uint64_t s = mul2(f.p[0], f.p[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(f.p[i], f.p[i], s);
+  const float2 u = split(s);
+  return u.x + u.y;
+}
+template <int kWidth>
+__device__ __forceinline__ float tree_sum(float s) {
+#pragma unroll
+  for (int o = 1; o < kWidth; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
   return s;
 }
 
-// NV groups of 8 values a thread: value 8 (i * threads + thread) + j of a row.
-template <int kType, int G, int NV>
-__global__ void __launch_bounds__(G == 0 ? 1024 : kRowThreads) residual_norm_kernel(moe_residual_norm_t a) {
-  __shared__ float sums[2][32];
-  pdl_wait();
-  pdl_trigger();
-  const int threads = G == 0 ? blockDim.x : G;
-  const int at = G == 0 ? threadIdx.x : threadIdx.x % G;
-  const long long row = G == 0 ? (long long)blockIdx.x
-                               : (long long)blockIdx.x * (kRowThreads / (G == 0 ? 1 : G)) + threadIdx.x / (G == 0 ? 1 : G);
-  const bool live = row < (long long)a.tokens * a.heads;
-  const int t = live ? (int)(row / a.heads) : 0, h = live ? (int)(row - (long long)t * a.heads) : 0;
-  const float n = (float)a.dim;
-  auto place = [&](const moe_heads_t& m) {
-    return static_cast<uint16_t*>(m.data) + (long long)t * m.token_stride + (long long)h * m.head_stride;
-  };
-  float y[NV][8], b[NV][8];
-  const bool has_block = a.block.data != nullptr;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int d = 8 * (i * threads + at);
-    uint4 px = make_uint4(0, 0, 0, 0), pb = px;
-    if (live && d < a.dim) {
-      px = ld_cg(reinterpret_cast<const uint4*>(place(a.x) + d));
-      if (has_block) pb = ld_cg(reinterpret_cast<const uint4*>(place(a.block) + d));
-    }
-    unpack8<kType>(px, y[i]);
-    unpack8<kType>(pb, b[i]);
+// Where a row's eight values from d on are.
+__device__ __forceinline__ uint16_t* place(const moe_heads_t& m, int t, int h, int d) {
+  return static_cast<uint16_t*>(m.data) + (long long)t * m.token_stride + (long long)h * m.head_stride + d;
+}
+__device__ __forceinline__ uint4 load8(const moe_heads_t& m, int t, int h, int d) {
+  return ld_cg(reinterpret_cast<const uint4*>(place(m, t, h, d)));
+}
+// The gate of eight values: as they are, or one for the row (its bits in .x).
+__device__ __forceinline__ uint4 load_gate(const moe_gate_t& g, int t, int h, int d) {
+  const uint16_t* p =
+      static_cast<const uint16_t*>(g.data) + (long long)t * g.token_stride + (long long)h * g.head_stride;
+  return g.dim_stride ? ld_cg(reinterpret_cast<const uint4*>(p + d)) : make_uint4(__ldcg(p), 0, 0, 0);
+}
+__device__ __forceinline__ F8 as_f8(const float4& a, const float4& b) {
+  return {{pair_of(a.x, a.y), pair_of(a.z, a.w), pair_of(b.x, b.y), pair_of(b.z, b.w)}};
+}
+__device__ __forceinline__ F8 load_weights(const float* w, int d) {
+  const float4 one = make_float4(1, 1, 1, 1);
+  if (!w) return as_f8(one, one);
+  return as_f8(ld_cg(reinterpret_cast<const float4*>(w + d)), ld_cg(reinterpret_cast<const float4*>(w + d + 4)));
+}
+
+// x + residual_scale gate b r (b normed already but for its r).
+template <int kType>
+__device__ __forceinline__ F8 add_block(const moe_residual_norm_t& a, const uint4& gate, F8 b, float r, const uint4& x) {
+  float by = a.residual_scale * r;
+  if (a.gate.data) {
+    if (a.gate.dim_stride) b = times(b, unpack8<kType>(gate));
+    else by *= unpack2<kType>(gate.x).x;
   }
-  if (has_block) {
-    float r = 1.0f;
-    if (a.post_norm) {
-      float s = 0.0f;
+  const uint64_t by2 = pair_of(by, by);
+  F8 y = unpack8<kType>(x);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s += b[i][j] * b[i][j];
-      r = 1.0f / sqrtf(row_sum<G>(s, sums[0]) / n + a.eps);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int d = 8 * (i * threads + at);
-      if (!live || d >= a.dim) continue;
-      if (a.post_norm) {
-        float w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-        if (a.post_weight) {
-          *reinterpret_cast<float4*>(w) = ld_cg(reinterpret_cast<const float4*>(a.post_weight + d));
-          *reinterpret_cast<float4*>(w + 4) = ld_cg(reinterpret_cast<const float4*>(a.post_weight + d + 4));
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[i][j] = b[i][j] * r * w[j];
-      }
-      if (a.gate.data) {
-        const uint16_t* p = static_cast<const uint16_t*>(a.gate.data) + (long long)t * a.gate.token_stride +
-                            (long long)h * a.gate.head_stride;
-        float g[8];
-        if (a.gate.dim_stride) {
-          unpack8<kType>(ld_cg(reinterpret_cast<const uint4*>(p + d)), g);
-        } else {
-          const float one = unpack2<kType>(__ldcg(p)).x;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = one;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[i][j] *= g[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] += a.residual_scale * b[i][j];
-      if (a.y.data) *reinterpret_cast<uint4*>(place(a.y) + d) = pack8<kType>(y[i]);
-    }
-  }
-  if (!a.normed.data && !a.quantized.codes) return;
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s += y[i][j] * y[i][j];
-  const float r = 1.0f / sqrtf(row_sum<G>(s, sums[1]) / n + a.eps);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int d = 8 * (i * threads + at);
-    const bool mine = live && d < a.dim;
-    float w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-    if (mine && a.pre_weight) {
-      *reinterpret_cast<float4*>(w) = ld_cg(reinterpret_cast<const float4*>(a.pre_weight + d));
-      *reinterpret_cast<float4*>(w + 4) = ld_cg(reinterpret_cast<const float4*>(a.pre_weight + d + 4));
-    }
+  for (int i = 0; i < 4; ++i) y.p[i] = fma2(b.p[i], by2, y.p[i]);
+  return y;
+}
+
+// normed = y r w of eight values to where it is asked for. `mine`: they are the row's. kWidth threads next to each other
+// have a block of 128 (or the whole of a shorter row).
+template <int kType, int kWidth>
+__device__ __forceinline__ void write_normed(const moe_residual_norm_t& a, int t, int h, int d, bool mine, F8 y, float r,
+                                             const F8& w) {
+  y = times(times(y, pair_of(r, r)), w);
+  if (mine && a.normed.data) *reinterpret_cast<uint4*>(place(a.normed, t, h, d)) = pack8<kType>(y);
+  if (a.quantized.codes) {
     float amax = 0.0f;
+    float2 u[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      y[i][j] = y[i][j] * r * w[j];
-      amax = fmaxf(amax, finite_size(y[i][j]));
+    for (int i = 0; i < 4; ++i) {
+      u[i] = split(y.p[i]);
+      amax = fmaxf(amax, fmaxf(finite_size(u[i].x), finite_size(u[i].y)));
     }
-    if (mine && a.normed.data) *reinterpret_cast<uint4*>(place(a.normed) + d) = pack8<kType>(y[i]);
-    if (a.quantized.codes) {
-      // 16 threads (all of a row of 64 values at most) have a block of 128
-      constexpr int width = G == 8 ? 8 : 16;
+    if (!mine) amax = 0.0f;
 #pragma unroll
-      for (int o = 1; o < width; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-      const uint32_t scale = e8m0_of(amax);
-      if (mine) {
-        const float inv = e8m0_inverse(scale);
-        *reinterpret_cast<uint2*>(a.quantized.codes + (long long)t * a.quantized.row_stride + d) =
-            make_uint2(e4m3x4_of(y[i][0], y[i][1], y[i][2], y[i][3], inv),
-                       e4m3x4_of(y[i][4], y[i][5], y[i][6], y[i][7], inv));
-      }
-      uint8_t* scales = a.quantized.scales + (long long)t * a.quantized.scale_stride;
-      if (mine && d % kFp8Block == 0) {
+    for (int o = 1; o < kWidth; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    const uint32_t scale = e8m0_of(amax);
+    if (mine) {
+      const float inv = e8m0_inverse(scale);
+      *reinterpret_cast<uint2*>(a.quantized.codes + (long long)t * a.quantized.row_stride + d) =
+          make_uint2(e4m3x4_of(u[0].x, u[0].y, u[1].x, u[1].y, inv), e4m3x4_of(u[2].x, u[2].y, u[3].x, u[3].y, inv));
+      if (d % kFp8Block == 0) {
+        uint8_t* scales = a.quantized.scales + (long long)t * a.quantized.scale_stride;
         scales[d / kFp8Block] = (uint8_t)scale;
         if (d + kFp8Block >= a.dim)  // the last block: the rest of its word
           for (int e = d / kFp8Block + 1; e % 4; ++e) scales[e] = (uint8_t)kNoScale;
@@ -163,27 +172,219 @@ __global__ void __launch_bounds__(G == 0 ? 1024 : kRowThreads) residual_norm_ker
   }
 }
 
-template <int kType, int G, int NV>
-cudaError_t launch(const moe_residual_norm_t& a, cudaStream_t s) {
-  const long long rows = (long long)a.tokens * a.heads;
-  if constexpr (G > 0) {
-    constexpr int per = kRowThreads / G;
-    return launch_pdl(residual_norm_kernel<kType, G, NV>, dim3((unsigned)((rows + per - 1) / per)), dim3(kRowThreads), 0,
-                      s, a);
-  } else {
-    const int threads = ((a.dim / 8 + NV - 1) / NV + 31) / 32 * 32;
-    return launch_pdl(residual_norm_kernel<kType, 0, NV>, dim3((unsigned)rows), dim3((unsigned)threads), 0, s, a);
+// Rows of at most 8 G values, G threads each, kRows rows of a thread at a time.
+template <int kType, int G, int kRows>
+__global__ void __launch_bounds__(kSmallThreads) residual_norm_small(const __grid_constant__ moe_residual_norm_t a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kPer = kSmallThreads / G;
+  const int d = 8 * (threadIdx.x % G);
+  const int rows = a.tokens * a.heads, step = gridDim.x * kPer;
+  const bool inside = d < a.dim, has_block = a.block.data != nullptr;
+  const float n = (float)a.dim;
+  F8 pre = {}, post = {};
+  if (inside) {
+    pre = load_weights(a.pre_weight, d);
+    if (a.post_norm) post = load_weights(a.post_weight, d);
   }
+  // (counted from the CTA's first row, so that all of a warp's threads go round together)
+  for (long long first = (long long)blockIdx.x * kPer; first < rows; first += (long long)kRows * step) {
+    uint4 x[kRows], b[kRows], g[kRows];
+    int t[kRows], h[kRows];
+    bool mine[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const long long row = first + threadIdx.x / G + (long long)k * step;
+      mine[k] = inside && row < rows;
+      t[k] = mine[k] ? (int)row / a.heads : 0;
+      h[k] = mine[k] ? (int)row - t[k] * a.heads : 0;
+      x[k] = b[k] = g[k] = make_uint4(0, 0, 0, 0);
+      if (mine[k]) {
+        x[k] = load8(a.x, t[k], h[k], d);
+        if (has_block) {
+          b[k] = load8(a.block, t[k], h[k], d);
+          if (a.gate.data) g[k] = load_gate(a.gate, t[k], h[k], d);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      F8 y;
+      if (has_block) {
+        F8 v = unpack8<kType>(b[k]);
+        float r = 1.0f;
+        if (a.post_norm) {
+          r = 1.0f / sqrtf(tree_sum<G>(squares(v)) / n + a.eps);
+          v = times(v, post);
+        }
+        y = add_block<kType>(a, g[k], v, r, x[k]);
+        if (mine[k] && a.y.data) *reinterpret_cast<uint4*>(place(a.y, t[k], h[k], d)) = pack8<kType>(y);
+      } else {
+        y = unpack8<kType>(x[k]);
+      }
+      if (a.normed.data || a.quantized.codes) {  // (values past a row are 0)
+        const float r = 1.0f / sqrtf(tree_sum<G>(squares(y)) / n + a.eps);
+        write_normed<kType, (G < 16 ? G : 16)>(a, t[k], h[k], d, mine[k], y, r, pre);
+      }
+    }
+  }
+}
+
+// The sum over a row: a tree over the trees' sums of all its 256-value pieces (64 at most). `sums` is not written again
+// before the call after the next one.
+template <int NV>
+__device__ __forceinline__ float row_sum(const float (&s)[NV], float* sums) {
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pieces = NV * warps;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const float tree = tree_sum<32>(s[i]);
+    if (lane == 0) sums[i * warps + warp] = tree;
+  }
+  __syncthreads();
+  float mine = lane < pieces ? sums[lane] : 0.0f;
+  if (pieces > 32 && 32 + lane < pieces) mine += sums[32 + lane];
+  return tree_sum<32>(mine);
+}
+
+// Longer rows, a CTA each: eight values 8 (i * threads + thread) .. of a row, i < NV. kStay: CTAs go from row to row.
+// (Their threads and CTAs on an SM: room for the next row's values in registers.)
+constexpr int stay_threads(int nv) { return nv == 4 ? 512 : 256; }
+constexpr int stay_ctas(int nv) { return nv == 4 ? 1 : nv == 2 ? 3 : 4; }
+template <int kType, int NV, bool kStay>
+__global__ void __launch_bounds__(kStay ? stay_threads(NV) : 1024, kStay ? stay_ctas(NV) : 1)
+    residual_norm_rows(const __grid_constant__ moe_residual_norm_t a) {
+  extern __shared__ float4 weights[];  // kStay: post (each eight values' first four, then their others), then pre
+  __shared__ float sums[2][2][64];
+  const int threads = blockDim.x, rows = a.tokens * a.heads;
+  const bool has_block = a.block.data != nullptr;
+  const float n = (float)a.dim;
+  auto at = [&](int i) { return 8 * (i * threads + (int)threadIdx.x); };
+  pdl_wait();
+  pdl_trigger();
+  uint4 x[NV], b[NV], g[NV];
+  auto token = [&](int row) { return a.heads == 1 ? row : row / a.heads; };
+  auto ask = [&](int row, uint4* px, uint4* pb) {
+    const int t = token(row), h = row - t * a.heads;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      px[i] = pb[i] = make_uint4(0, 0, 0, 0);
+      if (at(i) < a.dim) {
+        px[i] = load8(a.x, t, h, at(i));
+        if (has_block) pb[i] = load8(a.block, t, h, at(i));
+      }
+    }
+  };
+  int row = blockIdx.x;
+  ask(row, x, b);
+  F8 post[kStay ? 1 : NV], pre[kStay ? 1 : NV];
+  const int eights = a.dim / 8;
+  if constexpr (kStay) {
+    for (int d = 4 * threadIdx.x; d < a.dim; d += 4 * threads) {
+      const float4 one = make_float4(1, 1, 1, 1);
+      const int to = d / 8 + (d & 4 ? eights : 0);
+      weights[to] = a.post_weight ? ld_cg(reinterpret_cast<const float4*>(a.post_weight + d)) : one;
+      weights[2 * eights + to] = a.pre_weight ? ld_cg(reinterpret_cast<const float4*>(a.pre_weight + d)) : one;
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at(i) < a.dim) {
+        post[i] = load_weights(a.post_weight, at(i));
+        pre[i] = load_weights(a.pre_weight, at(i));
+      } else {
+        post[i] = pre[i] = {};
+      }
+  }
+  auto held = [&](const F8* own, int i, int from) {
+    if constexpr (!kStay) return own[i];
+    const int e = from * eights + i * threads + threadIdx.x;
+    return at(i) < a.dim ? as_f8(weights[e], weights[e + eights]) : F8{};
+  };
+  for (int turn = 0;; turn ^= 1) {
+    const int t = token(row), h = row - t * a.heads;
+    if (has_block && a.gate.data) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        g[i] = at(i) < a.dim ? load_gate(a.gate, t, h, at(i)) : make_uint4(0, 0, 0, 0);
+    }
+    uint4 nx[NV], nb[NV];
+    const bool more = kStay && row + (int)gridDim.x < rows;
+    if (more) ask(row + gridDim.x, nx, nb);
+    F8 y[NV];
+    float s[NV];
+    if (has_block) {
+      float r = 1.0f;
+      if (a.post_norm) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] = squares(unpack8<kType>(b[i]));
+        r = 1.0f / sqrtf(row_sum<NV>(s, sums[turn][0]) / n + a.eps);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        F8 v = unpack8<kType>(b[i]);
+        if (a.post_norm) v = times(v, held(post, i, 0));
+        y[i] = add_block<kType>(a, g[i], v, r, x[i]);
+        if (a.y.data && at(i) < a.dim) *reinterpret_cast<uint4*>(place(a.y, t, h, at(i))) = pack8<kType>(y[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) y[i] = unpack8<kType>(x[i]);
+    }
+    if (a.normed.data || a.quantized.codes) {  // (values past the row are 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s[i] = squares(y[i]);
+      const float r = 1.0f / sqrtf(row_sum<NV>(s, sums[turn][1]) / n + a.eps);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) write_normed<kType, 16>(a, t, h, at(i), at(i) < a.dim, y[i], r, held(pre, i, 2));
+    }
+    if (!more) break;
+    row += gridDim.x;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = nx[i];
+      b[i] = nb[i];
+    }
+  }
+}
+
+template <int kType, int G>
+cudaError_t launch_small(const moe_residual_norm_t& a, cudaStream_t s) {
+  constexpr int per = kSmallThreads / G;
+  const long long rows = (long long)a.tokens * a.heads, ctas = (rows + per - 1) / per;
+  const long long most = 8LL * num_sms();
+  const unsigned grid = (unsigned)(ctas < most ? ctas : most);
+  if (a.block.data) return launch_pdl(residual_norm_small<kType, G, 2>, dim3(grid), dim3(kSmallThreads), 0, s, a);
+  return launch_pdl(residual_norm_small<kType, G, 4>, dim3(grid), dim3(kSmallThreads), 0, s, a);
+}
+
+template <int kType, int NV>
+cudaError_t launch_staying(const moe_residual_norm_t& a, cudaStream_t s) {
+  const int threads = ((a.dim / 8 + NV - 1) / NV + 31) / 32 * 32;
+  const size_t smem = (size_t)a.dim * 8;
+  const cudaError_t err = cudaFuncSetAttribute(residual_norm_rows<kType, NV, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kMaxNormDim);
+  if (err != cudaSuccess) return err;
+  const int by_threads = stay_threads(NV) * stay_ctas(NV) / threads, by_smem = (int)(200 * 1024 / (smem + 2048));
+  int per_sm = by_threads < by_smem ? by_threads : by_smem;
+  per_sm = per_sm < 1 ? 1 : per_sm > 32 ? 32 : per_sm;
+  const long long rows = (long long)a.tokens * a.heads, most = (long long)per_sm * num_sms();
+  return launch_pdl(residual_norm_rows<kType, NV, true>, dim3((unsigned)(rows < most ? rows : most)), dim3(threads), smem, s,
+                    a);
 }
 
 template <int kType>
 cudaError_t launch_typed(const moe_residual_norm_t& a, cudaStream_t s) {
-  if (a.dim <= 64) return launch<kType, 8, 1>(a, s);
-  if (a.dim <= 128) return launch<kType, 16, 1>(a, s);
-  if (a.dim <= 256) return launch<kType, 32, 1>(a, s);
-  if (a.dim <= 512) return launch<kType, 32, 2>(a, s);
-  if (a.dim <= 8192) return launch<kType, 0, 1>(a, s);
-  return launch<kType, 0, 2>(a, s);
+  if (a.dim <= 64) return launch_small<kType, 8>(a, s);
+  if (a.dim <= 128) return launch_small<kType, 16>(a, s);
+  if (a.dim <= 256) return launch_small<kType, 32>(a, s);
+  const long long rows = (long long)a.tokens * a.heads;
+  const int threads = (a.dim / 8 + 31) / 32 * 32;
+  if (rows * threads <= 2048LL * num_sms() && threads <= 1024)
+    return launch_pdl(residual_norm_rows<kType, 1, false>, dim3((unsigned)rows), dim3(threads), 0, s, a);
+  if (a.dim <= 2048) return launch_staying<kType, 1>(a, s);
+  if (a.dim <= 4096) return launch_staying<kType, 2>(a, s);
+  return launch_staying<kType, 4>(a, s);
 }
 
 }  // namespace
