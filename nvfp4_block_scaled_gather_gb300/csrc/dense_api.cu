@@ -101,7 +101,9 @@ extern "C" {
 int moe_residual_norm(const moe_residual_norm_t* args, cudaStream_t stream) {
   const int st = norm_status(args);
   if (st != MOE_OK || args->tokens == 0) return st;
-  return status_of(launch_residual_norm(*args, stream));
+  int* word = status_ptr();
+  if (!word) return MOE_ERR_CUDA;
+  return status_of(launch_residual_norm(*args, word, stream));
 }
 
 int moe_fp8_quantize_rows(const uint16_t* x, long long x_stride, int rows, int K, int dtype,

@@ -24,7 +24,7 @@ inline long long fp8_scale_bytes(long long K) { return 4 * ((K + 511) / 512); }
 // row's bits do not depend on how a launch divides its work.
 inline int fp8_piece(int K) { return 512 * ((K + 4095) / 4096); }
 
-cudaError_t launch_residual_norm(const moe_residual_norm_t& a, cudaStream_t s);
+cudaError_t launch_residual_norm(const moe_residual_norm_t& a, int* status, cudaStream_t s);
 
 cudaError_t launch_fp8_quantize(const uint16_t* x, long long x_stride, int rows, int K, int dtype,
                                 const moe_fp8_rows_t& out, cudaStream_t s);

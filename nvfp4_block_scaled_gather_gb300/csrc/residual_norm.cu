@@ -15,7 +15,8 @@
 //  * Longer rows, many of them: CTAs stay and take row after row, the next
 //    one's values on their way while the present one is worked on; the norms'
 //    weights wait in shared memory (read from L2 for every row they would be
-//    as many bytes again).
+//    as many bytes again). Up to 8192 values the rows come to shared memory by
+//    bulk copies, longer ones to registers.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -24,12 +25,24 @@
 #include "fp8_codec.cuh"
 #include "internal.h"
 #include "ldcg.cuh"
+#include "mbar.cuh"
 #include "pdl.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kSmallThreads = 256;
+
+// What the host works out for a launch.
+struct Shape {
+  float inv_dim, eps;
+  uint32_t magic;  // row / heads = row * magic >> shift, for rows below 2^31
+  int shift;
+  int* status;
+};
+__device__ __forceinline__ int token_of(int row, int heads, const Shape& s) {
+  return heads == 1 ? row : (int)(((uint64_t)(uint32_t)row * s.magic) >> s.shift);
+}
 
 // Eight fp32 values in pairs: one instruction multiplies or adds both of a pair.
 struct F8 {
@@ -95,12 +108,31 @@ __device__ __forceinline__ float squares(const F8& f) {
   const float2 u = split(s);
   return u.x + u.y;
 }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// Until the row is there. Bounded: after that the call is reported as failed.
+__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kWaitCycles) {
+      atomicExch(status, (int)MOE_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
 template <int kWidth>
 __device__ __forceinline__ float tree_sum(float s) {
 #pragma unroll
   for (int o = 1; o < kWidth; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
   return s;
 }
+
+// 1 / sqrt(mean + eps) of a sum of squares (the approximate root is good to two ulps).
+__device__ __forceinline__ float inverse_rms(float sum, const Shape& s) { return rsqrtf(fmaf(sum, s.inv_dim, s.eps)); }
 
 // Where a row's eight values from d on are.
 __device__ __forceinline__ uint16_t* place(const moe_heads_t& m, int t, int h, int d) {
@@ -172,22 +204,35 @@ __device__ __forceinline__ void write_normed(const moe_residual_norm_t& a, int t
   }
 }
 
-// Rows of at most 8 G values, G threads each, kRows rows of a thread at a time.
-template <int kType, int G, int kRows>
-__global__ void __launch_bounds__(kSmallThreads) residual_norm_small(const __grid_constant__ moe_residual_norm_t a) {
+// Rows of at most 8 G values, G threads each, kRows rows of a thread at a time. kBlock: with a block's output.
+template <int kType, int G, int kRows, bool kBlock>
+__global__ void __launch_bounds__(kSmallThreads, kBlock ? 4 : 5) residual_norm_small(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
   pdl_wait();
   pdl_trigger();
   constexpr int kPer = kSmallThreads / G;
   const int d = 8 * (threadIdx.x % G);
   const int rows = a.tokens * a.heads, step = gridDim.x * kPer;
-  const bool inside = d < a.dim, has_block = a.block.data != nullptr;
-  const float n = (float)a.dim;
+  const bool inside = d < a.dim;
   F8 pre = {}, post = {};
   if (inside) {
     pre = load_weights(a.pre_weight, d);
-    if (a.post_norm) post = load_weights(a.post_weight, d);
+    if (kBlock && a.post_norm) post = load_weights(a.post_weight, d);
   }
+  uint4 nx[kRows], nb[kRows];
+  auto ask = [&](long long first) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const long long row = first + threadIdx.x / G + (long long)k * step;
+      nx[k] = nb[k] = make_uint4(0, 0, 0, 0);
+      if (inside && row < rows) {
+        const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
+        nx[k] = load8(a.x, t, h, d);
+        if constexpr (kBlock) nb[k] = load8(a.block, t, h, d);
+      }
+    }
+  };
   // (counted from the CTA's first row, so that all of a warp's threads go round together)
+  ask((long long)blockIdx.x * kPer);
   for (long long first = (long long)blockIdx.x * kPer; first < rows; first += (long long)kRows * step) {
     uint4 x[kRows], b[kRows], g[kRows];
     int t[kRows], h[kRows];
@@ -196,25 +241,22 @@ __global__ void __launch_bounds__(kSmallThreads) residual_norm_small(const __gri
     for (int k = 0; k < kRows; ++k) {
       const long long row = first + threadIdx.x / G + (long long)k * step;
       mine[k] = inside && row < rows;
-      t[k] = mine[k] ? (int)row / a.heads : 0;
+      t[k] = mine[k] ? token_of((int)row, a.heads, shape) : 0;
       h[k] = mine[k] ? (int)row - t[k] * a.heads : 0;
-      x[k] = b[k] = g[k] = make_uint4(0, 0, 0, 0);
-      if (mine[k]) {
-        x[k] = load8(a.x, t[k], h[k], d);
-        if (has_block) {
-          b[k] = load8(a.block, t[k], h[k], d);
-          if (a.gate.data) g[k] = load_gate(a.gate, t[k], h[k], d);
-        }
-      }
+      g[k] = make_uint4(0, 0, 0, 0);
+      if (kBlock && mine[k] && a.gate.data) g[k] = load_gate(a.gate, t[k], h[k], d);
+      x[k] = nx[k];
+      b[k] = nb[k];
     }
+    ask(first + (long long)kRows * step);
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       F8 y;
-      if (has_block) {
+      if constexpr (kBlock) {
         F8 v = unpack8<kType>(b[k]);
         float r = 1.0f;
         if (a.post_norm) {
-          r = 1.0f / sqrtf(tree_sum<G>(squares(v)) / n + a.eps);
+          r = inverse_rms(tree_sum<G>(squares(v)), shape);
           v = times(v, post);
         }
         y = add_block<kType>(a, g[k], v, r, x[k]);
@@ -223,7 +265,7 @@ __global__ void __launch_bounds__(kSmallThreads) residual_norm_small(const __gri
         y = unpack8<kType>(x[k]);
       }
       if (a.normed.data || a.quantized.codes) {  // (values past a row are 0)
-        const float r = 1.0f / sqrtf(tree_sum<G>(squares(y)) / n + a.eps);
+        const float r = inverse_rms(tree_sum<G>(squares(y)), shape);
         write_normed<kType, (G < 16 ? G : 16)>(a, t[k], h[k], d, mine[k], y, r, pre);
       }
     }
@@ -247,24 +289,19 @@ __device__ __forceinline__ float row_sum(const float (&s)[NV], float* sums) {
 }
 
 // Longer rows, a CTA each: eight values 8 (i * threads + thread) .. of a row, i < NV. kStay: CTAs go from row to row.
-// (Their threads and CTAs on an SM: room for the next row's values in registers.)
-constexpr int stay_threads(int nv) { return nv == 4 ? 512 : 256; }
-constexpr int stay_ctas(int nv) { return nv == 4 ? 1 : nv == 2 ? 3 : 4; }
 template <int kType, int NV, bool kStay>
-__global__ void __launch_bounds__(kStay ? stay_threads(NV) : 1024, kStay ? stay_ctas(NV) : 1)
-    residual_norm_rows(const __grid_constant__ moe_residual_norm_t a) {
+__global__ void __launch_bounds__(kStay ? 512 : 1024)
+    residual_norm_rows(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
   extern __shared__ float4 weights[];  // kStay: post (each eight values' first four, then their others), then pre
   __shared__ float sums[2][2][64];
   const int threads = blockDim.x, rows = a.tokens * a.heads;
   const bool has_block = a.block.data != nullptr;
-  const float n = (float)a.dim;
   auto at = [&](int i) { return 8 * (i * threads + (int)threadIdx.x); };
   pdl_wait();
   pdl_trigger();
   uint4 x[NV], b[NV], g[NV];
-  auto token = [&](int row) { return a.heads == 1 ? row : row / a.heads; };
   auto ask = [&](int row, uint4* px, uint4* pb) {
-    const int t = token(row), h = row - t * a.heads;
+    const int t = token_of(row, a.heads, shape), h = row - t * a.heads;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       px[i] = pb[i] = make_uint4(0, 0, 0, 0);
@@ -302,7 +339,7 @@ __global__ void __launch_bounds__(kStay ? stay_threads(NV) : 1024, kStay ? stay_
     return at(i) < a.dim ? as_f8(weights[e], weights[e + eights]) : F8{};
   };
   for (int turn = 0;; turn ^= 1) {
-    const int t = token(row), h = row - t * a.heads;
+    const int t = token_of(row, a.heads, shape), h = row - t * a.heads;
     if (has_block && a.gate.data) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -318,7 +355,7 @@ __global__ void __launch_bounds__(kStay ? stay_threads(NV) : 1024, kStay ? stay_
       if (a.post_norm) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[i] = squares(unpack8<kType>(b[i]));
-        r = 1.0f / sqrtf(row_sum<NV>(s, sums[turn][0]) / n + a.eps);
+        r = inverse_rms(row_sum<NV>(s, sums[turn][0]), shape);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -334,7 +371,7 @@ __global__ void __launch_bounds__(kStay ? stay_threads(NV) : 1024, kStay ? stay_
     if (a.normed.data || a.quantized.codes) {  // (values past the row are 0)
 #pragma unroll
       for (int i = 0; i < NV; ++i) s[i] = squares(y[i]);
-      const float r = 1.0f / sqrtf(row_sum<NV>(s, sums[turn][1]) / n + a.eps);
+      const float r = inverse_rms(row_sum<NV>(s, sums[turn][1]), shape);
 #pragma unroll
       for (int i = 0; i < NV; ++i) write_normed<kType, 16>(a, t, h, at(i), at(i) < a.dim, y[i], r, held(pre, i, 2));
     }
@@ -348,49 +385,163 @@ __global__ void __launch_bounds__(kStay ? stay_threads(NV) : 1024, kStay ? stay_
   }
 }
 
+// Rows of 257 to 8192, many of them: the same with the rows brought to shared memory by bulk copies, kSlots of them on
+// their way or being worked on, which leaves the registers to the arithmetic.
+constexpr int kSlots = 2;
+template <int kType, int NV>
+__global__ void __launch_bounds__(512, 2)
+    residual_norm_stream(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
+  extern __shared__ float4 weights[];  // post (each eight values' first four, then their others), pre, then the slots
+  __shared__ float sums[2][2][64];
+  __shared__ uint64_t landed[kSlots];
+  const int threads = blockDim.x, rows = a.tokens * a.heads, eights = a.dim / 8, bytes = 2 * a.dim;
+  const bool has_block = a.block.data != nullptr;
+  uint8_t* slots = reinterpret_cast<uint8_t*>(weights + 4 * eights);
+  auto eighth = [&](int i) { return i * threads + (int)threadIdx.x; };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(landed + i), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  auto bring = [&](int slot, long long row) {  // by one thread
+    if (row >= rows) return;
+    const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
+    const uint32_t bar = smem_u32(landed + slot), to = smem_u32(slots) + (uint32_t)(slot * 2 * bytes);
+    mbar_expect_tx(bar, has_block ? 2 * bytes : bytes);
+    bulk_load(to, place(a.x, t, h, 0), bytes, bar);
+    if (has_block) bulk_load(to + bytes, place(a.block, t, h, 0), bytes, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kSlots; ++i) bring(i, blockIdx.x + (long long)i * gridDim.x);
+  for (int d = 4 * threadIdx.x; d < a.dim; d += 4 * threads) {
+    const float4 one = make_float4(1, 1, 1, 1);
+    const int to = d / 8 + (d & 4 ? eights : 0);
+    weights[to] = a.post_weight ? ld_cg(reinterpret_cast<const float4*>(a.post_weight + d)) : one;
+    weights[2 * eights + to] = a.pre_weight ? ld_cg(reinterpret_cast<const float4*>(a.pre_weight + d)) : one;
+  }
+  __syncthreads();
+  const F8 none = {};
+  int slot = 0, turn = 0;
+  uint32_t parity = 0;
+  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
+    uint4 g[NV];
+    if (has_block && a.gate.data) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        g[i] = eighth(i) < eights ? load_gate(a.gate, t, h, 8 * eighth(i)) : make_uint4(0, 0, 0, 0);
+    }
+    wait_landed(smem_u32(landed + slot), parity, shape.status);
+    const uint4* x = reinterpret_cast<const uint4*>(slots + slot * 2 * bytes);
+    const uint4* b = x + eights;
+    F8 y[NV];
+    float s[NV];
+    if (has_block) {
+      float r = 1.0f;
+      if (a.post_norm) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          y[i] = eighth(i) < eights ? unpack8<kType>(b[eighth(i)]) : none;
+          s[i] = squares(y[i]);
+        }
+        r = inverse_rms(row_sum<NV>(s, sums[turn][0]), shape);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = eighth(i);
+        if (e >= eights) {
+          y[i] = none;
+          continue;
+        }
+        F8 v = a.post_norm ? times(y[i], as_f8(weights[e], weights[e + eights])) : unpack8<kType>(b[e]);
+        y[i] = add_block<kType>(a, g[i], v, r, x[e]);
+        if (a.y.data) *reinterpret_cast<uint4*>(place(a.y, t, h, 8 * e)) = pack8<kType>(y[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) y[i] = eighth(i) < eights ? unpack8<kType>(x[eighth(i)]) : none;
+    }
+    const bool more = a.normed.data || a.quantized.codes;
+    float r = 0.0f;
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s[i] = squares(y[i]);
+      r = inverse_rms(row_sum<NV>(s, sums[turn][1]), shape);  // (everyone has read the slot)
+    } else {
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) bring(slot, row + (long long)kSlots * gridDim.x);
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = eighth(i);
+        const F8 w = e < eights ? as_f8(weights[2 * eights + e], weights[3 * eights + e]) : none;
+        write_normed<kType, 16>(a, t, h, 8 * e, e < eights, y[i], r, w);
+      }
+    }
+    turn ^= 1;
+    if (++slot == kSlots) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+}
+
 template <int kType, int G>
-cudaError_t launch_small(const moe_residual_norm_t& a, cudaStream_t s) {
+cudaError_t launch_small(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
   constexpr int per = kSmallThreads / G;
   const long long rows = (long long)a.tokens * a.heads, ctas = (rows + per - 1) / per;
-  const long long most = 8LL * num_sms();
+  const long long most = (a.block.data ? 4LL : 5LL) * num_sms();
   const unsigned grid = (unsigned)(ctas < most ? ctas : most);
-  if (a.block.data) return launch_pdl(residual_norm_small<kType, G, 2>, dim3(grid), dim3(kSmallThreads), 0, s, a);
-  return launch_pdl(residual_norm_small<kType, G, 4>, dim3(grid), dim3(kSmallThreads), 0, s, a);
+  if (a.block.data) return launch_pdl(residual_norm_small<kType, G, 1, true>, dim3(grid), dim3(kSmallThreads), 0, s, a, shape);
+  return launch_pdl(residual_norm_small<kType, G, 2, false>, dim3(grid), dim3(kSmallThreads), 0, s, a, shape);
 }
 
 template <int kType, int NV>
-cudaError_t launch_staying(const moe_residual_norm_t& a, cudaStream_t s) {
+cudaError_t launch_stream(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
   const int threads = ((a.dim / 8 + NV - 1) / NV + 31) / 32 * 32;
-  const size_t smem = (size_t)a.dim * 8;
-  const cudaError_t err = cudaFuncSetAttribute(residual_norm_rows<kType, NV, true>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kMaxNormDim);
+  const size_t smem = (size_t)a.dim * (8 + 4 * kSlots);
+  const cudaError_t err = cudaFuncSetAttribute(residual_norm_stream<kType, NV>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 8192 * (8 + 4 * kSlots));
   if (err != cudaSuccess) return err;
-  const int by_threads = stay_threads(NV) * stay_ctas(NV) / threads, by_smem = (int)(200 * 1024 / (smem + 2048));
+  const int by_threads = 1024 / threads, by_smem = (int)(220 * 1024 / (smem + 2304));
   int per_sm = by_threads < by_smem ? by_threads : by_smem;
   per_sm = per_sm < 1 ? 1 : per_sm > 32 ? 32 : per_sm;
   const long long rows = (long long)a.tokens * a.heads, most = (long long)per_sm * num_sms();
-  return launch_pdl(residual_norm_rows<kType, NV, true>, dim3((unsigned)(rows < most ? rows : most)), dim3(threads), smem, s,
-                    a);
+  return launch_pdl(residual_norm_stream<kType, NV>, dim3((unsigned)(rows < most ? rows : most)), dim3(threads), smem, s, a,
+                    shape);
 }
 
 template <int kType>
-cudaError_t launch_typed(const moe_residual_norm_t& a, cudaStream_t s) {
-  if (a.dim <= 64) return launch_small<kType, 8>(a, s);
-  if (a.dim <= 128) return launch_small<kType, 16>(a, s);
-  if (a.dim <= 256) return launch_small<kType, 32>(a, s);
+cudaError_t launch_typed(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
+  if (a.dim <= 64) return launch_small<kType, 8>(a, shape, s);
+  if (a.dim <= 128) return launch_small<kType, 16>(a, shape, s);
+  if (a.dim <= 256) return launch_small<kType, 32>(a, shape, s);
   const long long rows = (long long)a.tokens * a.heads;
   const int threads = (a.dim / 8 + 31) / 32 * 32;
   if (rows * threads <= 2048LL * num_sms() && threads <= 1024)
-    return launch_pdl(residual_norm_rows<kType, 1, false>, dim3((unsigned)rows), dim3(threads), 0, s, a);
-  if (a.dim <= 2048) return launch_staying<kType, 1>(a, s);
-  if (a.dim <= 4096) return launch_staying<kType, 2>(a, s);
-  return launch_staying<kType, 4>(a, s);
+    return launch_pdl(residual_norm_rows<kType, 1, false>, dim3((unsigned)rows), dim3(threads), 0, s, a, shape);
+  if (a.dim <= 2048) return launch_stream<kType, 1>(a, shape, s);
+  if (a.dim <= 8192) return launch_stream<kType, 2>(a, shape, s);
+  // rows whose weights and slots would not fit shared memory
+  const size_t smem = (size_t)a.dim * 8;
+  const cudaError_t err = cudaFuncSetAttribute(residual_norm_rows<kType, 4, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kMaxNormDim);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(residual_norm_rows<kType, 4, true>, dim3((unsigned)(rows < num_sms() ? rows : num_sms())),
+                    dim3(((a.dim / 8 + 3) / 4 + 31) / 32 * 32), smem, s, a, shape);
 }
 
 }  // namespace
 
-cudaError_t launch_residual_norm(const moe_residual_norm_t& a, cudaStream_t s) {
-  return a.dtype == MOE_BF16 ? launch_typed<MOE_BF16>(a, s) : launch_typed<MOE_FP16>(a, s);
+cudaError_t launch_residual_norm(const moe_residual_norm_t& a, int* status, cudaStream_t s) {
+  Shape shape = {1.0f / (float)a.dim, a.eps, 0, 31, status};
+  // rounded up: off by less than heads / 2^shift a row, which 2^31 rows do not add up to one
+  while ((1LL << (shape.shift - 31)) < a.heads) ++shape.shift;
+  shape.magic = (uint32_t)((1ULL << shape.shift) / (unsigned)a.heads + 1);
+  return a.dtype == MOE_BF16 ? launch_typed<MOE_BF16>(a, shape, s) : launch_typed<MOE_FP16>(a, shape, s);
 }
 
 }  // namespace moe
