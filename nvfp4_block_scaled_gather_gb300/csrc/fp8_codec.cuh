@@ -53,9 +53,10 @@ __device__ __forceinline__ float e8m0_inverse(uint32_t byte) { return __uint_as_
 
 // Codes of two values over their scale, the first in the low byte. The
 // product is exact up to fp32's smallest values, so a code is rounded once.
+// (An infinity would become the largest code: times 0 first it is NaN.)
 __device__ __forceinline__ uint32_t e4m3x2_of(float a, float b, float inverse) {
-  a = fabsf(a) < INFINITY ? a * inverse : NAN;
-  b = fabsf(b) < INFINITY ? b * inverse : NAN;
+  a = fmaf(a, inverse, a * 0.0f);
+  b = fmaf(b, inverse, b * 0.0f);
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;

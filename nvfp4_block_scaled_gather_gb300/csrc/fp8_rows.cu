@@ -3,63 +3,85 @@
 // A warp takes 512 values of a row, the four blocks whose scales are one word:
 // lane l has values 16 l .. 16 l + 15, eight lanes a block of 128. Its largest
 // magnitude goes around by shuffles; dividing by a power of two is a product.
+// Bound by bytes: the next word's values are on their way meanwhile.
 #include <cstdint>
 
 #include <cuda_runtime.h>
 
 #include "dense_internal.h"
 #include "fp8_codec.cuh"
+#include "internal.h"
 #include "ldcg.cuh"
 #include "pdl.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kCtas = 6;  // of an SM: the values on their way fit its registers
+
+struct Values {
+  uint4 a, b;  // 16 of them
+};
 
 template <int kType>
-__global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const uint16_t* x, long long x_stride, int rows, int K,
-                                                                int words, moe_fp8_rows_t out) {
+__global__ void __launch_bounds__(kThreads, kCtas) fp8_quantize_kernel(const uint16_t* x, long long x_stride, int rows,
+                                                                       int K, int words, moe_fp8_rows_t out) {
   pdl_wait();
   pdl_trigger();
-  const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (unit >= (long long)rows * words) return;
-  const int row = (int)(unit / words), word = (int)(unit - (long long)row * words);
-  const int k = word * 512 + lane * 16;
-  float v[16];
-  if (k < K) {
-    const uint4* p = reinterpret_cast<const uint4*>(x + (long long)row * x_stride + k);
-    const uint4 a = ld_cg(p), b = ld_cg(p + 1);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int step = gridDim.x * (kThreads / 32), step_row = step / words, step_word = step - step_row * words;
+  // this warp's row and word, and the next one's (whose values are on their way)
+  int row, word;
+  {
+    const int first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    row = first / words;
+    word = first - row * words;
+  }
+  auto ask = [&](int r, int w) {
+    Values v = {};
+    const int k = w * 512 + lane * 16;
+    if (r < rows && k < K) {
+      const uint4* p = reinterpret_cast<const uint4*>(x + (long long)r * x_stride + k);
+      v.a = ld_cg(p);
+      v.b = ld_cg(p + 1);
+    }
+    return v;
+  };
+  Values next = ask(row, word);
+  while (row < rows) {
+    const Values now = next;
+    const int r = row, w = word, k = w * 512 + lane * 16;
+    row += step_row;
+    word += step_word;
+    if (word >= words) {
+      word -= words;
+      ++row;
+    }
+    next = ask(row, word);
+    const uint32_t bits[8] = {now.a.x, now.a.y, now.a.z, now.a.w, now.b.x, now.b.y, now.b.z, now.b.w};
+    float v[16], amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 f = unpack2<kType>(w[i]);
+      const float2 f = unpack2<kType>(bits[i]);
       v[2 * i] = f.x;
       v[2 * i + 1] = f.y;
+      amax = fmaxf(amax, fmaxf(finite_size(f.x), finite_size(f.y)));
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    const uint32_t scale = e8m0_of(amax);
+    if (k < K) {
+      const float inv = e8m0_inverse(scale);
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = e4m3x4_of(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
+      *reinterpret_cast<uint4*>(out.codes + (long long)r * out.row_stride + k) = make_uint4(c[0], c[1], c[2], c[3]);
+    }
+    uint32_t all = (w * 512 + (lane & ~7) * 16 < K ? scale : kNoScale) << (8 * (lane >> 3));
+    all |= __shfl_xor_sync(~0u, all, 8);
+    all |= __shfl_xor_sync(~0u, all, 16);
+    if (lane == 0) *reinterpret_cast<uint32_t*>(out.scales + (long long)r * out.scale_stride + 4 * w) = all;
   }
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_size(v[i]));
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  const uint32_t scale = e8m0_of(amax);
-  if (k < K) {
-    const float inv = e8m0_inverse(scale);
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x4_of(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
-    *reinterpret_cast<uint4*>(out.codes + (long long)row * out.row_stride + k) = make_uint4(c[0], c[1], c[2], c[3]);
-  }
-  const uint32_t mine = (word * 512 + (lane & ~7) * 16 < K ? scale : kNoScale) << (8 * (lane >> 3));
-  uint32_t all = mine;
-  all |= __shfl_xor_sync(~0u, all, 8);
-  all |= __shfl_xor_sync(~0u, all, 16);
-  if (lane == 0) *reinterpret_cast<uint32_t*>(out.scales + (long long)row * out.scale_stride + 4 * word) = all;
 }
 
 }  // namespace
@@ -68,10 +90,9 @@ cudaError_t launch_fp8_quantize(const uint16_t* x, long long x_stride, int rows,
                                 const moe_fp8_rows_t& out, cudaStream_t s) {
   const int words = (K + 511) / 512;
   const long long units = (long long)rows * words;
-  const long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32), most = (long long)kCtas * num_sms();
   auto* kernel = dtype == MOE_BF16 ? fp8_quantize_kernel<MOE_BF16> : fp8_quantize_kernel<MOE_FP16>;
-  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, x, x_stride, rows, K, words, out);
+  return launch_pdl(kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, s, x, x_stride, rows, K, words, out);
 }
 
 }  // namespace moe
