@@ -43,6 +43,7 @@ constexpr int kWBytes = kRows * kBlockK;
 constexpr int kScaleSlots = 2;     // words of scales on their way
 constexpr int kHeader = 1024 + kScaleSlots * 1536;
 constexpr int kMaxStages = 5;
+constexpr int kMostSplit = 8;      // CTAs of a cluster
 constexpr int kMaxTokens = 240;    // of a tile: two accumulators and the scales fill tensor memory
 
 // kCols: tokens of a tile at most. kPair: two CTAs share a tile of 256 rows of
@@ -209,6 +210,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// (without waiting for this thread's stores)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // The address of the same place in another CTA of the cluster.
 __device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   __syncwarp();
   if (!kPair && a.split > 1) {
     if (warp < 4 || warp >= S::load_warp) cluster_wait();  // (the others have)
-    cluster_arrive();                                      // nothing more is sent from here
+    cluster_arrive_relaxed();                              // nothing more is sent from here
     // A CTA that has its sums needs its peers no more, nor they it. One that gave up may still be sent some.
     if (__any_sync(~0u, *abort_flag)) cluster_wait();
   }
@@ -766,8 +769,8 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   a.tiles = a.tiles_n * a.tiles_t;
   a.split = 1;
   // a cluster's CTAs share a tile where there are too few tiles; what they send each other is held in 32 KB
-  if (!S::wide)
-    while (a.split < 8 && a.split < a.pieces && a.tiles * a.split * 2 <= slots) a.split *= 2;
+  if (!S::wide && a.pieces > 1)
+    while (a.split < kMostSplit && (long long)a.tiles * a.split * 2 <= slots) a.split *= 2;
   if (a.split > 1 && a.tn > 8 * a.split) a.split = 1;
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
   const int room = (S::smem - 1024 - kHeader - recv) / (S::deep * (kWBytes + a.tn / S::ctas * kBlockK));
@@ -811,9 +814,14 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   a.piece = fp8_piece(g.K);
   a.pieces = (g.K + a.piece - 1) / a.piece;
   a.status = g.status;
-  if (g.T <= 16) return launch<16, false>(g, a, s);
-  if (g.T <= 32) return launch<32, false>(g, a, s);
-  if (g.T <= 64 || g.N <= kRows) return launch<64, false>(g, a, s);
+  // The narrowest tiles of which a cluster each runs at one time: few tokens, or little of everything. Else the
+  // narrowest that hold all tokens of a decode batch (every row of w is read once), or pairs. (64 tokens x 4096 x 11008:
+  // 15 us in clusters, 22 in pairs; x 5120 x 4096, more tiles than run at once: 17 and 11.)
+  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * Shape<16, false>::per_sm;
+  auto clusters = [&](int cols) { return rows * ((g.T + cols - 1) / cols) * kMostSplit <= slots; };
+  if (g.T <= 16 || clusters(16)) return launch<16, false>(g, a, s);
+  if (g.T <= 32 || clusters(32)) return launch<32, false>(g, a, s);
+  if (clusters(64) || g.N <= kRows) return launch<64, false>(g, a, s);
   return launch<kMaxTokens, true>(g, a, s);
 }
 
