@@ -141,9 +141,7 @@ int moe_fp8_linear(const uint16_t* x, long long x_stride, int T, int K, int dtyp
   if (!word) return MOE_ERR_CUDA;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   const moe_fp8_rows_t rows = {codes, codes + align256((size_t)T * K), K, fp8_scale_bytes(K)};
-  const cudaError_t e = launch_fp8_quantize(x, x_stride, T, K, dtype, rows, stream);
-  if (e != cudaSuccess) return status_of(e);
-  return status_of(launch_fp8_gemm({rows, *w, T, N, K, y, y_stride, y_dtype, word}, stream));
+  return status_of(launch_fp8_linear(x, x_stride, dtype, {rows, *w, T, N, K, y, y_stride, y_dtype, word}, stream));
 }
 
 }  // extern "C"

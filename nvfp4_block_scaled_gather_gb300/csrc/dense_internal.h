@@ -38,5 +38,7 @@ struct Fp8Gemm {
   int* status;
 };
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s);
+// The same of 16-bit rows x; g.x is where their 8-bit rows go, if they go anywhere.
+cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, const Fp8Gemm& g, cudaStream_t s);
 
 }  // namespace moe

@@ -81,6 +81,8 @@ struct Shape {
 struct Args {
   const uint8_t *ws, *xs;
   long long ws_stride, xs_stride;
+  const uint16_t* x16;    // rows to be quantized on the way (kFrom)
+  long long x16_stride;
   void* y;
   long long y_stride;
   int y_dtype;
@@ -350,7 +352,10 @@ __device__ __forceinline__ void store_pairs(uint16_t* y, long long stride, const
   }
 }
 
-template <int kCols, bool kPair>
+// kFrom: what the tokens come as, 8-bit rows or (narrow tiles) a 16-bit type, MOE_BF16 or MOE_FP16: then the warps that
+// bring scales quantize the tokens' values as they go.
+constexpr int kFromRows = -1;
+template <int kCols, bool kPair, int kFrom>
 __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPair>::per_sm)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ Args a) {
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   if (warp == S::load_warp) {
     if (elect_one()) {
       tma_prefetch_map(&wmap);
-      tma_prefetch_map(&xmap);
+      if constexpr (kFrom == kFromRows) tma_prefetch_map(&xmap);
       // the rows of w may be those that the kernel before this one writes: they are asked for in L2 only
       if (first < a.tiles) {
         const int n0 = place_of(first, a).n * S::tile_rows + half * kRows;
@@ -430,6 +435,89 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
 
   if (warp < 4) {
     if constexpr (S::wide) give_registers<S::few>();
+    if constexpr (kFrom != kFromRows) {
+      // ========================== scale words of w, and the tokens ==========================
+      // Warp g has the scale words of w's rows 32 g .. 32 g + 31. Of the tokens thread i has, of token i / 16 (and the one
+      // 8 on), values 8 (i % 16) .. of each of a word's four blocks: 16 threads a block's largest magnitude.
+      static_assert(kCols == 16 && S::deep == 1, "two tokens a thread, a block a stage");
+      const int part = threadIdx.x & 15, token = threadIdx.x >> 4;
+      uint4 raw[2][4];
+      uint32_t ww = 0;
+      int i = b0 < b1 ? first : a.tiles, b = b0;  // of the next word to ask for
+      auto ask = [&] {
+        if (i >= a.tiles) return;
+        const Place at = place_of(i, a);
+        const int n = at.n * kRows + 32 * warp + lane;
+        ww = n < a.N ? ld_cg(reinterpret_cast<const uint32_t*>(a.ws + n * a.ws_stride + b)) : 0u;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int t = at.t * a.tn + token + 8 * u;
+          const uint16_t* row = a.x16 + t * a.x16_stride;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = (b + j) * kBlockK + 8 * part;
+            raw[u][j] = t < a.T && k < a.K ? ld_cg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
+          }
+        }
+        b += 4;
+        if (b >= b1) {
+          b = b0;
+          i += step;
+        }
+      };
+      ask();
+      const uint32_t mine = first < a.tiles ? (uint32_t)((a.tiles - first + step - 1) / step * ((b2 - b0) / 4)) : 0u;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (uint32_t n = 0; n < mine && ok; ++n) {
+        uint32_t scales[2] = {0, 0}, codes[2][4][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t bits[4] = {raw[u][j].x, raw[u][j].y, raw[u][j].z, raw[u][j].w};
+            float v[8], amax = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack2<kFrom>(bits[e]);
+              v[2 * e] = f.x;
+              v[2 * e + 1] = f.y;
+              amax = fmaxf(amax, fmaxf(finite_size(f.x), finite_size(f.y)));
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+            const uint32_t scale = e8m0_of(amax);
+            const float inv = e8m0_inverse(scale);
+            codes[u][j][0] = e4m3x4_of(v[0], v[1], v[2], v[3], inv);
+            codes[u][j][1] = e4m3x4_of(v[4], v[5], v[6], v[7], inv);
+            scales[u] |= scale << (8 * j);
+          }
+        }
+        const uint32_t now = ww;
+        ask();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
+          if (!ok) break;
+          if (j == 0) {
+            // (the copies of the word before the last one, from this slot, are done as its MMAs are)
+            uint8_t* atoms = smem + 1024 + (n % kScaleSlots) * S::slot_bytes;
+            *reinterpret_cast<uint32_t*>(atoms + lane * 16 + warp * 4) = now;
+            if (part < 2) *reinterpret_cast<uint32_t*>(atoms + 512 + (token + 8 * part) * 16) = part ? scales[1] : scales[0];
+          }
+          // 16-byte piece c of row r at piece c ^ (r % 8); the second token's row is 8 on
+          uint8_t* tile = smem + (s_x - base) + stage * x_bytes + token * kBlockK + (((part >> 1) ^ token) << 4) + (part & 1) * 8;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<uint2*>(tile + u * 8 * kBlockK) = make_uint2(codes[u][j][0], codes[u][j][1]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full_bar(stage));
+          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+        }
+      }
+    } else {
     // ================================ scale words ================================
     // Group g of 32 rows is warp g % 4's: w's rows, then the tokens'. A lane has a row's word, in its place of the atom
     // that the MMA warp copies to tensor memory. (Stores from here to tensor memory wait for the MMAs that are queued.)
@@ -495,6 +583,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
         ask(q[u]);
       }
     }
+    }
   } else if (warp >= S::load_warp) {
     if constexpr (S::wide) give_registers<S::few>();
     if (warp == S::load_warp) {
@@ -515,12 +604,14 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
             const int here = min(S::deep, b1 - b);  // (none: only the arrival)
             // a pair's loads are all counted by the first CTA, whose MMAs read both CTAs' stages
             const uint32_t bar = kPair ? peer(full_bar(stage), 0) : full_bar(stage);
-            if (half == 0) mbar_expect_tx(full_bar(stage), S::ctas * max(here, 0) * (kWBytes + x_bytes));
+            if (half == 0)
+              mbar_expect_tx(full_bar(stage), S::ctas * max(here, 0) * (kWBytes + (kFrom == kFromRows ? x_bytes : 0)));
 #pragma unroll
             for (int h = 0; h < S::deep; ++h) {
               if (h >= here) break;
               tma_load<kPair>(s_w + (stage * S::deep + h) * kWBytes, &wmap, (b + h) * kBlockK, n0, bar);
-              tma_load<kPair>(s_x + (stage * S::deep + h) * x_bytes, &xmap, (b + h) * kBlockK, t0, bar);
+              if constexpr (kFrom == kFromRows)
+                tma_load<kPair>(s_x + (stage * S::deep + h) * x_bytes, &xmap, (b + h) * kBlockK, t0, bar);
             }
           }
           __syncwarp();
@@ -732,17 +823,17 @@ int pairs_at_once() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<kCols, true>, &cfg) != cudaSuccess || n < 1) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<kCols, true, kFromRows>, &cfg) != cudaSuccess || n < 1) return 0;
     known[dev] = n;
   }
   return known[dev];
 }
 
-template <int kCols, bool kPair>
+template <int kCols, bool kPair, int kFrom = kFromRows>
 cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   using S = Shape<kCols, kPair>;
   cudaError_t err =
-      cudaFuncSetAttribute(fp8_gemm_kernel<kCols, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
+      cudaFuncSetAttribute(fp8_gemm_kernel<kCols, kPair, kFrom>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
   if (err != cudaSuccess) return err;
   long long slots = (long long)num_sms() * S::per_sm;
   if constexpr (kPair) slots = pairs_at_once<kCols>();
@@ -775,8 +866,9 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
   const int room = (S::smem - 1024 - kHeader - recv) / (S::deep * (kWBytes + a.tn / S::ctas * kBlockK));
   a.stages = room < S::most_stages ? room : S::most_stages;
-  CUtensorMap wmap, xmap;
-  if (!make_map(&wmap, g.w, g.N, g.K, kRows) || !make_map(&xmap, g.x, g.T, g.K, a.tn / S::ctas))
+  CUtensorMap wmap, xmap = {};
+  if (!make_map(&wmap, g.w, g.N, g.K, kRows) ||
+      (kFrom == kFromRows && !make_map(&xmap, g.x, g.T, g.K, a.tn / S::ctas)))
     return cudaErrorInvalidValue;
   const int ctas = kPair ? 2 : a.split;
   const long long grid = a.split > 1 ? (long long)a.tiles * a.split : (a.tiles < slots ? a.tiles : slots) * ctas;
@@ -793,12 +885,14 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<kCols, kPair>, wmap, xmap, a);
+  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<kCols, kPair, kFrom>, wmap, xmap, a);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
+namespace {
+
+Args common_args(const Fp8Gemm& g) {
   Args a = {};
   a.ws = g.w.scales;
   a.xs = g.x.scales;
@@ -814,15 +908,39 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   a.piece = fp8_piece(g.K);
   a.pieces = (g.K + a.piece - 1) / a.piece;
   a.status = g.status;
-  // The narrowest tiles of which a cluster each runs at one time: few tokens, or little of everything. Else the
-  // narrowest that hold all tokens of a decode batch (every row of w is read once), or pairs. (64 tokens x 4096 x 11008:
-  // 15 us in clusters, 22 in pairs; x 5120 x 4096, more tiles than run at once: 17 and 11.)
+  return a;
+}
+
+// Whether all tiles of so many tokens run at one time, a cluster each.
+bool clusters_fit(const Fp8Gemm& g, int cols) {
   const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * Shape<16, false>::per_sm;
-  auto clusters = [&](int cols) { return rows * ((g.T + cols - 1) / cols) * kMostSplit <= slots; };
-  if (g.T <= 16 || clusters(16)) return launch<16, false>(g, a, s);
-  if (g.T <= 32 || clusters(32)) return launch<32, false>(g, a, s);
-  if (clusters(64) || g.N <= kRows) return launch<64, false>(g, a, s);
+  return rows * ((g.T + cols - 1) / cols) * kMostSplit <= slots;
+}
+
+}  // namespace
+
+// The narrowest tiles of which a cluster each runs at one time: few tokens, or little of everything. Else the narrowest
+// that hold all tokens of a decode batch (every row of w is read once), or pairs. (64 tokens x 4096 x 11008: 15 us in
+// clusters, 22 in pairs; x 5120 x 4096, more tiles than run at once: 17 and 11.)
+cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
+  const Args a = common_args(g);
+  if (g.T <= 16 || clusters_fit(g, 16)) return launch<16, false>(g, a, s);
+  if (g.T <= 32 || clusters_fit(g, 32)) return launch<32, false>(g, a, s);
+  if (clusters_fit(g, 64) || g.N <= kRows) return launch<64, false>(g, a, s);
   return launch<kMaxTokens, true>(g, a, s);
+}
+
+cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, const Fp8Gemm& g, cudaStream_t s) {
+  // Where a cluster shares a tile each CTA quantizes its part of K on the way (one token x 5120 x 4096: 7 us, 9.9 with a
+  // launch before it); CTAs that go from tile to tile would do it again for each.
+  if ((g.T <= 16 && (g.N + kRows - 1) / kRows <= num_sms()) || clusters_fit(g, 16)) {
+    Args a = common_args(g);
+    a.x16 = x;
+    a.x16_stride = x_stride;
+    return dtype == MOE_BF16 ? launch<16, false, MOE_BF16>(g, a, s) : launch<16, false, MOE_FP16>(g, a, s);
+  }
+  const cudaError_t e = launch_fp8_quantize(x, x_stride, g.T, g.K, dtype, g.x, s);
+  return e != cudaSuccess ? e : launch_fp8_gemm(g, s);
 }
 
 }  // namespace moe
