@@ -21,6 +21,7 @@
 //    (distributed shared memory; CTA r has 128 / split of the tile's rows).
 //  * Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT,
 //    waits for its copies and MMAs, frees tensor memory and returns.
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -807,7 +808,7 @@ bool make_map(CUtensorMap* map, const moe_fp8_rows_t& m, int rows, int K, int bo
 // Pairs of CTAs that run at one time on the current device (a GPC with an odd number of SMs leaves one out).
 template <int kCols>
 int pairs_at_once() {
-  static int known[64] = {0};
+  static std::atomic<int> known[64];  // (zero)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (known[dev] == 0) {
@@ -832,8 +833,7 @@ int pairs_at_once() {
 template <int kCols, bool kPair, int kFrom = kFromRows>
 cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   using S = Shape<kCols, kPair>;
-  cudaError_t err =
-      cudaFuncSetAttribute(fp8_gemm_kernel<kCols, kPair, kFrom>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
+  const cudaError_t err = allow_smem<fp8_gemm_kernel<kCols, kPair, kFrom>, S::smem>();
   if (err != cudaSuccess) return err;
   long long slots = (long long)num_sms() * S::per_sm;
   if constexpr (kPair) slots = pairs_at_once<kCols>();

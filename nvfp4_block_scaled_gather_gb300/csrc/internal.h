@@ -2,9 +2,10 @@
 // Each returns cudaSuccess or the launch error; arguments are validated by
 // the C-ABI layer (moe_api.cu) before these are called.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
-#include <cuda_runtime_api.h>
+#include <cuda_runtime.h>
 
 #include "moe_nvfp4.h"
 
@@ -34,6 +35,20 @@ inline size_t token_sf_bytes(long long R_max, long long G_max, long long K, int 
 }
 
 int num_sms();  // SM count of the current device (cached per device)
+
+// Lets a kernel have so much dynamic shared memory on the current device: asked once a device (the call takes as long as
+// half a launch). kKernel and kBytes tell the kernels apart.
+template <auto kKernel, int kBytes>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ULL << dev, std::memory_order_release);
+  return e;
+}
 
 // Host-side argument checks of moe_nvfp4_layer (everything but the
 // workspace): MOE_OK, MOE_ERR_INVALID or MOE_ERR_SHAPE. T == 0 is valid.

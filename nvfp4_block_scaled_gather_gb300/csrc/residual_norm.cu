@@ -503,8 +503,7 @@ template <int kType, int NV>
 cudaError_t launch_stream(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
   const int threads = ((a.dim / 8 + NV - 1) / NV + 31) / 32 * 32;
   const size_t smem = (size_t)a.dim * (8 + 4 * kSlots);
-  const cudaError_t err = cudaFuncSetAttribute(residual_norm_stream<kType, NV>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 8192 * (8 + 4 * kSlots));
+  const cudaError_t err = allow_smem<residual_norm_stream<kType, NV>, 8192 * (8 + 4 * kSlots)>();
   if (err != cudaSuccess) return err;
   const int by_threads = 1024 / threads, by_smem = (int)(220 * 1024 / (smem + 2304));
   int per_sm = by_threads < by_smem ? by_threads : by_smem;
@@ -527,8 +526,7 @@ cudaError_t launch_typed(const moe_residual_norm_t& a, const Shape& shape, cudaS
   if (a.dim <= 8192) return launch_stream<kType, 2>(a, shape, s);
   // rows whose weights and slots would not fit shared memory
   const size_t smem = (size_t)a.dim * 8;
-  const cudaError_t err = cudaFuncSetAttribute(residual_norm_rows<kType, 4, true>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kMaxNormDim);
+  const cudaError_t err = allow_smem<residual_norm_rows<kType, 4, true>, 8 * kMaxNormDim>();
   if (err != cudaSuccess) return err;
   return launch_pdl(residual_norm_rows<kType, 4, true>, dim3((unsigned)(rows < num_sms() ? rows : num_sms())),
                     dim3(((a.dim / 8 + 3) / 4 + 31) / 32 * 32), smem, s, a, shape);

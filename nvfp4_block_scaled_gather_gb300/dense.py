@@ -16,7 +16,7 @@ import struct
 import torch
 
 from . import _native
-from .attention import BF16, FP16, _heads, _scratch, _stream
+from .attention import BF16, FP16, _scratch, _stream
 from ._native import _check
 
 c_int, c_size_t, c_void_p, c_longlong, c_float = (ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong,
@@ -37,10 +37,10 @@ class Gate(ctypes.Structure):
 
 # the structs as bytes, at a fifth of the time that the classes take
 _rows_bytes = struct.Struct("PPqq").pack
-_gate_bytes = struct.Struct("PqqiI").pack   # (padded to 8 bytes)
-_norm_head = struct.Struct("iiii").pack     # tokens, heads, dim, dtype
-_norm_mid = struct.Struct("ffiIPP").pack    # residual_scale, eps, post_norm, padding, post_weight, pre_weight
-_NO_HEADS, _NO_GATE, _NO_ROWS = bytes(24), bytes(32), bytes(32)
+# moe_residual_norm_t: tokens, heads, dim, dtype; x; block; gate (padded to 8 bytes); residual_scale, eps, post_norm,
+# padding, post_weight, pre_weight; y; normed; quantized
+_norm_bytes = struct.Struct("iiii" "Pqq" "Pqq" "PqqiI" "ffiIPP" "Pqq" "Pqq").pack
+_NO_PART, _NO_GATE, _NO_ROWS = (0, 0, 0), (0, 0, 0, 0), bytes(32)
 
 _SIGS = {
     "moe_residual_norm": (c_int, [c_void_p, c_void_p]),
@@ -211,21 +211,43 @@ def moe_fp8_linear(x, w: Fp8Rows, y, workspace, stream=None):
           *_scratch(workspace, dev), _stream(stream, dev))
 
 
-def _three(t):
-    """[tokens, dim] as rows of one head."""
-    return t.unsqueeze(1) if t.dim() == 2 else t
+def _part(name, t, dtype, tokens, heads, dim, device: int):
+    """[tokens, dim] or [tokens, heads, dim] with dim contiguous: address, token and head stride."""
+    if t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
+    shape = t.shape
+    if len(shape) == 3:
+        if shape[0] != tokens or shape[1] != heads or shape[2] != dim:
+            raise ValueError(f"{name} must be like x {(tokens, heads, dim)}, got {tuple(shape)}")
+    elif len(shape) != 2 or heads != 1 or shape[0] != tokens or shape[1] != dim:
+        raise ValueError(f"{name} must be like x {(tokens, heads, dim)}, got {tuple(shape)}")
+    if t.is_contiguous():
+        ts, hs = heads * dim, dim
+    else:
+        strides = t.stride()
+        ts, hs, ds = strides if len(strides) == 3 else (strides[0], 0, strides[1])
+        if ds != 1 and dim != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous, got {strides}")
+    # a stride along one element says nothing
+    if tokens <= 1:
+        ts = 0
+    if heads <= 1:
+        hs = 0
+    if ts % 8 or hs % 8:
+        raise ValueError(f"{name}: the strides of tokens and heads must be multiples of 8 elements, got {t.stride()}")
+    return t.data_ptr(), ts, hs
 
 
 def _norm_weight(name, w, dim, device: int):
     if w is None:
         return 0
-    if w.dtype is not _FLOAT32 or w.shape != (dim,) or not w.is_contiguous() or w.get_device() != device:
+    if w.dtype is not _FLOAT32 or w.dim() != 1 or w.numel() != dim or not w.is_contiguous() or w.get_device() != device:
         raise ValueError(f"{name} must be a contiguous float32 tensor {(dim,)} on cuda:{device}")
     return w.data_ptr()
 
 
 def _gate(g, dtype, shape, device: int):
-    """A factor for each element, by broadcasting: sizes of 1 are held along."""
+    """A factor for each element, by broadcasting: sizes of 1 are held along. Address and strides."""
     if g.dim() == 2 and shape[1] == 1:
         g = g.unsqueeze(1)
     if g.dtype is not dtype or g.get_device() != device:
@@ -236,7 +258,7 @@ def _gate(g, dtype, shape, device: int):
     if ds not in (0, 1) or ds == 1 and (ts % 8 or hs % 8):
         raise ValueError(f"gate: the last dimension must be contiguous (or 1) and the other strides multiples of 8 "
                          f"elements, got {g.stride()}")
-    return _gate_bytes(g.data_ptr(), ts, hs, ds, 0)
+    return g.data_ptr(), ts, hs, ds
 
 
 def moe_residual_norm(x, block=None, *, y=None, normed=None, quantized: Fp8Rows = None, pre_weight=None,
@@ -249,30 +271,32 @@ def moe_residual_norm(x, block=None, *, y=None, normed=None, quantized: Fp8Rows 
 
     x, block, y and normed [tokens, dim], or [tokens, heads, dim] with every head normed by itself; outputs that are
     None are not written. gate broadcasts to x's shape."""
-    x = _three(x)
-    dtype, dev = x.dtype, x.get_device()
+    dtype, dev, shape = x.dtype, x.get_device(), x.shape
     code = _CODES.get(dtype)
     if code is None:
         raise ValueError(f"x must be bfloat16 or float16, got {dtype}")
-    hx, shape = _heads("x", x, dtype, dev)
-    tokens, heads, dim = shape
-
-    def part(name, t):
-        if t is None:
-            return _NO_HEADS
-        packed, got = _heads(name, _three(t), dtype, dev)
-        if got != shape:
-            raise ValueError(f"{name} must be like x {tuple(shape)}, got {tuple(got)}")
-        return packed
-
+    if len(shape) == 2:
+        (tokens, dim), heads = shape, 1
+    elif len(shape) == 3:
+        tokens, heads, dim = shape
+    else:
+        raise ValueError(f"x must be [tokens, dim] or [tokens, heads, dim], got {tuple(shape)}")
+    if max(shape) > _MOST:
+        raise ValueError(f"x must have less than 2**31 of each, got {tuple(shape)}")
+    sizes = (dtype, tokens, heads, dim, dev)
     rows = _NO_ROWS
     if quantized is not None:
         rows = _rows_of("quantized", quantized, dev)
-        if (quantized.n, quantized.k) != (tokens, dim):
-            raise ValueError(f"quantized must have {tokens} rows of {dim}, got {quantized.n} of {quantized.k}")
-    args = (_norm_head(tokens, heads, dim, code) + hx + part("block", block)
-            + (_NO_GATE if gate is None else _gate(gate, dtype, shape, dev))
-            + _norm_mid(residual_scale, eps, 1 if post_norm else 0, 0, _norm_weight("post_weight", post_weight, dim, dev),
-                        _norm_weight("pre_weight", pre_weight, dim, dev))
-            + part("y", y) + part("normed", normed) + rows)
-    _call("moe_residual_norm", load().moe_residual_norm, args, _stream(stream, dev))
+        if quantized.n != tokens or quantized.k != dim or heads != 1:
+            raise ValueError(f"quantized must have {tokens} rows of {dim} (of one head), got {quantized.n} of {quantized.k}")
+    args = _norm_bytes(tokens, heads, dim, code, *_part("x", x, *sizes),
+                       *(_NO_PART if block is None else _part("block", block, *sizes)),
+                       *(_NO_GATE if gate is None else _gate(gate, dtype, (tokens, heads, dim), dev)), 0,
+                       residual_scale, eps, 1 if post_norm else 0, 0,
+                       0 if post_weight is None else _norm_weight("post_weight", post_weight, dim, dev),
+                       0 if pre_weight is None else _norm_weight("pre_weight", pre_weight, dim, dev),
+                       *(_NO_PART if y is None else _part("y", y, *sizes)),
+                       *(_NO_PART if normed is None else _part("normed", normed, *sizes))) + rows
+    status = load().moe_residual_norm(args, _stream(stream, dev))
+    if status:
+        _check("moe_residual_norm", status)

@@ -9,7 +9,6 @@ import numpy as np
 import pytest
 import torch
 
-from nvfp4_block_scaled_gather_gb300 import attention as A
 from nvfp4_block_scaled_gather_gb300 import dense as D
 from oracle import dense as OD
 from tests.conftest import ROOT
@@ -82,9 +81,8 @@ def test_linear_refusals(lib):
 
 def norm_args(tokens=4, heads=1, dim=256, dtype=0, x=(4096, 256, 0), block=(8192, 256, 0), gate=(0, 0, 0, 0), scale=1.0, eps=1e-6,
               post=0, post_weight=0, pre_weight=0, y=(12288, 256, 0), normed=(16384, 256, 0), quantized=(0, 0, 0, 0)):
-    return (D._norm_head(tokens, heads, dim, dtype) + A._heads_bytes(*x) + A._heads_bytes(*block) + D._gate_bytes(*gate, 0)
-            + D._norm_mid(scale, eps, post, 0, post_weight, pre_weight) + A._heads_bytes(*y) + A._heads_bytes(*normed)
-            + D._rows_bytes(*quantized))
+    return D._norm_bytes(tokens, heads, dim, dtype, *x, *block, *gate, 0, scale, eps, post, 0, post_weight, pre_weight, *y,
+                         *normed) + D._rows_bytes(*quantized)
 
 
 def test_norm_refusals(lib):
@@ -115,8 +113,15 @@ def test_binding_refuses_what_torch_can_see():
         D.Fp8Rows(codes, scales)  # not on a GPU
     with pytest.raises(ValueError, match="must be bfloat16 or float16"):
         D.moe_residual_norm(torch.zeros((2, 8)))
-    with pytest.raises(ValueError, match="like x"):
-        D.moe_residual_norm(torch.zeros((2, 8), dtype=torch.bfloat16), torch.zeros((2, 16), dtype=torch.bfloat16))
+    for x, block in (((2, 8), (2, 16)), ((2, 8), (3, 8)), ((2, 2, 8), (2, 16)), ((2, 8), (2, 2, 8)), ((2, 8), (8,))):
+        with pytest.raises(ValueError, match="like x"):
+            D.moe_residual_norm(torch.zeros(x, dtype=torch.bfloat16), torch.zeros(block, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="tokens, dim"):
+        D.moe_residual_norm(torch.zeros(8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="contiguous"):
+        D.moe_residual_norm(torch.zeros((8, 16), dtype=torch.bfloat16)[:, ::2])
+    with pytest.raises(ValueError, match="multiples of 8"):
+        D.moe_residual_norm(torch.zeros((8, 12), dtype=torch.bfloat16)[:, :8])
     with pytest.raises(ValueError, match="post_weight must be"):
         D._norm_weight("post_weight", torch.zeros(8, dtype=torch.bfloat16), 8, -1)
     x = torch.zeros((2, 3, 8), dtype=torch.bfloat16)
@@ -126,7 +131,7 @@ def test_binding_refuses_what_torch_can_see():
                        (torch.zeros((2, 3, 9), dtype=torch.bfloat16)[..., :8], "multiples of 8")):
         with pytest.raises(ValueError, match=text):
             D._gate(gate, torch.bfloat16, (2, 3, 8), -1)
-    strides = [ctypes.c_longlong.from_buffer_copy(D._gate(g, torch.bfloat16, s, -1), 8).value for g, s in (
+    strides = [D._gate(g, torch.bfloat16, s, -1)[1] for g, s in (
         (torch.zeros((2, 1, 1), dtype=torch.bfloat16), (2, 3, 8)), (torch.zeros((1, 1, 8), dtype=torch.bfloat16), (2, 3, 8)),
         (torch.zeros((2, 8), dtype=torch.bfloat16), (2, 1, 8)))]
     assert strides == [1, 0, 8]
