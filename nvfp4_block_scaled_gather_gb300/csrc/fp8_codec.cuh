@@ -65,4 +65,40 @@ __device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d
   return e4m3x2_of(a, b, inverse) | (e4m3x2_of(c, d, inverse) << 16);
 }
 
+// The largest finite magnitude of 2 kWords 16-bit values each of kWidth threads next to each other, as fp32. By whole
+// warps.
+template <int kType, int kWidth, int kWords>
+__device__ __forceinline__ float finite_block_max(const uint32_t (&w)[kWords]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const float2 v = unpack2<kType>(w[i]);
+    amax = fmaxf(amax, fmaxf(finite_size(v.x), finite_size(v.y)));
+  }
+#pragma unroll
+  for (int o = 1; o < kWidth; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+  return amax;
+}
+// The same with infinities and NaN counted: then it is one of them. Magnitudes are compared as whole numbers, two at a
+// time.
+template <int kType, int kWidth, int kWords>
+__device__ __forceinline__ uint32_t block_max_bits(const uint32_t (&w)[kWords]) {
+  constexpr uint32_t kMagnitude = 0x7fff7fffu;
+  uint32_t m = w[0] & kMagnitude;
+#pragma unroll
+  for (int i = 1; i < kWords; ++i) m = __vmaxu2(m, w[i] & kMagnitude);
+#pragma unroll
+  for (int o = 1; o < kWidth; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(~0u, m, o));
+  return max(m & 0xffffu, m >> 16);
+}
+template <int kType>
+constexpr uint32_t kInfinityBits = kType == MOE_BF16 ? 0x7f80u : 0x7c00u;
+
+// The codes of four 16-bit values over a scale.
+template <int kType>
+__device__ __forceinline__ uint32_t e4m3x4_of(uint32_t lo, uint32_t hi, float inverse) {
+  const float2 a = unpack2<kType>(lo), b = unpack2<kType>(hi);
+  return e4m3x4_of(a.x, a.y, b.x, b.y, inverse);
+}
+
 }  // namespace moe

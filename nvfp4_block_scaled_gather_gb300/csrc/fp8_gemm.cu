@@ -41,9 +41,11 @@ namespace {
 constexpr int kRows = 128;         // rows of w of a CTA's tile
 constexpr int kBlockK = 128;       // values (bytes) of K that share a scale: a row of a swizzled tile
 constexpr int kWBytes = kRows * kBlockK;
-constexpr int kScaleSlots = 2;     // words of scales on their way
-constexpr int kHeader = 1024 + kScaleSlots * 1536;
 constexpr int kMaxStages = 5;
+constexpr int kScaleSlots = 2;     // words of scales on their way
+constexpr int kStageAtoms = 1024 + kScaleSlots * 1536;  // an atom for each stage, of tokens that are quantized here
+constexpr int kHeader = 7168;
+static_assert(kStageAtoms + kMaxStages * 512 <= kHeader, "");
 constexpr int kMostSplit = 8;      // CTAs of a cluster
 constexpr int kMaxTokens = 240;    // of a tile: two accumulators and the scales fill tensor memory
 
@@ -76,7 +78,7 @@ struct Shape {
   static constexpr int xs_words = (kCols + 31) / 32, xs_atoms = (xs_words + 3) / 4;
   static constexpr int slot_bytes = (1 + xs_atoms) * 512;      // w's atom, then the tokens'
   static constexpr int scale_cols = 16;                        // tokens' scales, then (at 8) those of w; two such
-  static constexpr int tmem = wide ? 512 : 2 * acc_cols + 2 * scale_cols <= 128 ? 128 : 256;
+  static constexpr int tmem = wide ? 512 : 2 * acc_cols + 2 * scale_cols + 32 <= 128 ? 128 : 256;
 };
 
 struct Args {
@@ -248,12 +250,12 @@ __device__ __forceinline__ uint64_t desc_atom(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
 // Instruction descriptor, kind::mxf8f6f4: A and B e4m3 (format 0), K-major,
-// e8m0 scales, M = m, N = n; `byte` of each scale word is used.
+// e8m0 scales, M = m, N = n; bytes a and b of A's and B's scale words are used.
 __device__ __forceinline__ uint32_t idesc_mxf8(int m, int n) {
   return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int byte) {
-  return idesc | ((uint32_t)byte << 4) | ((uint32_t)byte << 29);
+__device__ __forceinline__ uint32_t with_bytes(uint32_t idesc, int a, int b) {
+  return idesc | ((uint32_t)b << 4) | ((uint32_t)a << 29);
 }
 
 // True in one lane of a converged warp, always the same.
@@ -438,84 +440,94 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
     if constexpr (S::wide) give_registers<S::few>();
     if constexpr (kFrom != kFromRows) {
       // ========================== scale words of w, and the tokens ==========================
-      // Warp g has the scale words of w's rows 32 g .. 32 g + 31. Of the tokens thread i has, of token i / 16 (and the one
-      // 8 on), values 8 (i % 16) .. of each of a word's four blocks: 16 threads a block's largest magnitude.
-      static_assert(kCols == 16 && S::deep == 1, "two tokens a thread, a block a stage");
+      // (One tile a CTA.) Warp g has the scale words of w's rows 32 g .. 32 g + 31. Of the tokens thread i has, of tokens
+      // i / 16, 8 on and so on, values 8 (i % 16) .. of a block: 16 threads its largest magnitude. A stage's scales are an
+      // atom of their own, in the first byte. Values are asked for kAhead blocks ahead. (Kept short: with a word's four
+      // blocks worked on at once, 36 KB of instructions that run once, one token took 9.6 us instead of 7.6.)
+      static_assert(kCols <= 32 && S::deep == 1, "at most four tokens a thread, a block a stage");
+      constexpr int kTokens = kCols / 8, kAhead = 8 / kTokens;
+      struct Values {
+        uint4 x[kTokens];
+        uint32_t w;
+      };
       const int part = threadIdx.x & 15, token = threadIdx.x >> 4;
-      uint4 raw[2][4];
-      uint32_t ww = 0;
-      int i = b0 < b1 ? first : a.tiles, b = b0;  // of the next word to ask for
-      auto ask = [&] {
-        if (i >= a.tiles) return;
-        const Place at = place_of(i, a);
-        const int n = at.n * kRows + 32 * warp + lane;
-        ww = n < a.N ? ld_cg(reinterpret_cast<const uint32_t*>(a.ws + n * a.ws_stride + b)) : 0u;
+      const Place at = place_of(min(first, a.tiles - 1), a);
+      const int left = min(a.tn, a.T - at.t * a.tn);  // tokens
+      const uint16_t* x0 = a.x16 + (at.t * a.tn + token) * a.x16_stride + 8 * part;
+      const int n = at.n * kRows + 32 * warp + lane;
+      const uint8_t* w0 = n < a.N ? a.ws + n * a.ws_stride : nullptr;
+      auto ask = [&](int b, Values& v) {
+        if ((b & 3) == 0) v.w = w0 && b < b1 ? ld_cg(reinterpret_cast<const uint32_t*>(w0 + b)) : 0u;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int t = at.t * a.tn + token + 8 * u;
-          const uint16_t* row = a.x16 + t * a.x16_stride;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = (b + j) * kBlockK + 8 * part;
-            raw[u][j] = t < a.T && k < a.K ? ld_cg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
-          }
-        }
-        b += 4;
-        if (b >= b1) {
-          b = b0;
-          i += step;
+        for (int u = 0; u < kTokens; ++u) {
+          v.x[u] = make_uint4(0, 0, 0, 0);
+          if (token + 8 * u < left && b < b1 && b * kBlockK + 8 * part < a.K)
+            v.x[u] = ld_cg(reinterpret_cast<const uint4*>(x0 + 8 * u * a.x16_stride + b * kBlockK));
         }
       };
-      ask();
-      const uint32_t mine = first < a.tiles ? (uint32_t)((a.tiles - first + step - 1) / step * ((b2 - b0) / 4)) : 0u;
+      Values q[kAhead];
+      if (first < a.tiles) {
+#pragma unroll
+        for (int set = 0; set < kAhead; ++set) ask(b0 + set, q[set]);
+      }
       int stage = 0;
       uint32_t phase = 0;
-      bool ok = true;
-      for (uint32_t n = 0; n < mine && ok; ++n) {
-        uint32_t scales[2] = {0, 0}, codes[2][4][2];
+      bool ok = first < a.tiles;
+#pragma unroll 1
+      for (int b = b0; b < b2 && ok; b += kAhead) {  // (b2 - b0 is a multiple of four)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int two = 0; two < kAhead; two += 2) {  // two blocks' maxima at a time: their chains go side by side
+          uint32_t scales[2][kTokens];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t bits[4] = {raw[u][j].x, raw[u][j].y, raw[u][j].z, raw[u][j].w};
-            float v[8], amax = 0.0f;
+          for (int u = 0; u < kTokens; ++u) {
+            if (2 * warp + 8 * u >= left) break;  // none of this warp's
+            uint32_t most[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<kFrom>(bits[e]);
-              v[2 * e] = f.x;
-              v[2 * e + 1] = f.y;
-              amax = fmaxf(amax, fmaxf(finite_size(f.x), finite_size(f.y)));
+            for (int j = 0; j < 2; ++j) {
+              const uint4 x = q[two + j].x[u];
+              const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+              most[j] = block_max_bits<kFrom, 16>(words);
+              scales[j][u] = e8m0_of(unpack2<kFrom>(most[j]).x);
             }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-            const uint32_t scale = e8m0_of(amax);
-            const float inv = e8m0_inverse(scale);
-            codes[u][j][0] = e4m3x4_of(v[0], v[1], v[2], v[3], inv);
-            codes[u][j][1] = e4m3x4_of(v[4], v[5], v[6], v[7], inv);
-            scales[u] |= scale << (8 * j);
+            if (__any_sync(~0u, max(most[0], most[1]) >= kInfinityBits<kFrom>)) {
+#pragma unroll 1
+              for (int j = 0; j < 2; ++j) {
+                const uint4 x = j ? q[two + 1].x[u] : q[two].x[u];
+                const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t scale = e8m0_of(finite_block_max<kFrom, 16>(words));
+                if (j) scales[1][u] = scale;
+                else scales[0][u] = scale;
+              }
+            }
           }
-        }
-        const uint32_t now = ww;
-        ask();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
-          if (!ok) break;
-          if (j == 0) {
-            // (the copies of the word before the last one, from this slot, are done as its MMAs are)
-            uint8_t* atoms = smem + 1024 + (n % kScaleSlots) * S::slot_bytes;
-            *reinterpret_cast<uint32_t*>(atoms + lane * 16 + warp * 4) = now;
-            if (part < 2) *reinterpret_cast<uint32_t*>(atoms + 512 + (token + 8 * part) * 16) = part ? scales[1] : scales[0];
+          for (int j = 0; j < 2; ++j) {
+            Values& v = q[two + j];
+            ok = ok && wait_warp(empty_bar(stage), phase ^ 1u, ctl);
+            if (!ok) break;
+            const int now = b + two + j;
+            if ((now & 3) == 0)  // (the copies of the word before the last one, from this slot, are done as its MMAs are)
+              *reinterpret_cast<uint32_t*>(smem + 1024 + ((now - b0) >> 2) % kScaleSlots * S::slot_bytes + lane * 16 +
+                                           warp * 4) = v.w;
+            uint8_t* atom = smem + kStageAtoms + stage * 512 + token * 16;
+            // 16-byte piece c of row r at piece c ^ (r % 8); the other tokens' rows are 8 on
+            uint8_t* tile = smem + (s_x - base) + stage * x_bytes + token * kBlockK + (((part >> 1) ^ token) << 4) +
+                            (part & 1) * 8;
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u) {
+              if (2 * warp + 8 * u >= left) break;
+              const uint4 x = v.x[u];
+              const float inv = e8m0_inverse(scales[j][u]);
+              if (part == 0) *reinterpret_cast<uint32_t*>(atom + u * 128) = scales[j][u];
+              *reinterpret_cast<uint2*>(tile + u * 8 * kBlockK) =
+                  make_uint2(e4m3x4_of<kFrom>(x.x, x.y, inv), e4m3x4_of<kFrom>(x.z, x.w, inv));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full_bar(stage));
+            if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+            ask(now + kAhead, v);
           }
-          // 16-byte piece c of row r at piece c ^ (r % 8); the second token's row is 8 on
-          uint8_t* tile = smem + (s_x - base) + stage * x_bytes + token * kBlockK + (((part >> 1) ^ token) << 4) + (part & 1) * 8;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<uint2*>(tile + u * 8 * kBlockK) = make_uint2(codes[u][j][0], codes[u][j][1]);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full_bar(stage));
-          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
       }
     } else {
@@ -647,25 +659,33 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
             const uint32_t col = tmem + 2 * S::acc_cols + (ns & 1) * S::scale_cols;
             wait_on(full_bar(stage), phase, ctl);
             tc_fence_after();
+            // the columns of the tokens' scales, w's are 8 on; of tokens quantized here a stage's own (eight by turns, more
+            // than stages)
+            uint32_t xcol = col;
+            if constexpr (kFrom != kFromRows) xcol = tmem + 2 * S::acc_cols + 2 * S::scale_cols + (b - b0) % 8 * 4;
             if (elect_one()) {
+              const uint64_t from = atom_desc + (uint64_t)((ns % kScaleSlots) * (S::slot_bytes >> 4));
               if ((b & 3) == 0) {
-                const uint64_t from = atom_desc + (uint64_t)((ns % kScaleSlots) * (S::slot_bytes >> 4));
                 tc_copy_atom<kPair>(col + 8, from);
+                if constexpr (kFrom == kFromRows)
 #pragma unroll
-                for (int c = 0; c < S::xs_atoms; ++c) tc_copy_atom<kPair>(col + 4 * c, from + 32 * (c + 1));
+                  for (int c = 0; c < S::xs_atoms; ++c) tc_copy_atom<kPair>(col + 4 * c, from + 32 * (c + 1));
               }
+              if constexpr (kFrom != kFromRows)
+                tc_copy_atom<kPair>(xcol, atom_desc + (uint64_t)((kStageAtoms - 1024 + stage * 512) >> 4));
               const uint64_t wd = w_desc + (uint64_t)(stage * S::deep * (kWBytes >> 4));
               const uint64_t xd = x_desc + (uint64_t)(stage * S::deep * (x_bytes >> 4));
-              const uint32_t id = with_byte(idesc, b & 3);
+              const uint32_t id = with_bytes(idesc, b & 3, kFrom == kFromRows ? b & 3 : 0);
+              constexpr uint32_t kNext = (1u << 29) | (1u << 4);  // both bytes on (a stage of more than one block)
               if ((b + S::deep) * kBlockK <= a.K) {
 #pragma unroll
                 for (int h = 0; h < S::deep; ++h)
-                  tc_mma_block<kPair>(d, wd + h * (kWBytes >> 4), xd + h * (x_bytes >> 4), id + h * with_byte(0, 1), col + 8,
-                                      col, b + h > begin, 4);
+                  tc_mma_block<kPair>(d, wd + h * (kWBytes >> 4), xd + h * (x_bytes >> 4), id + h * kNext, col + 8, xcol,
+                                      b + h > begin, 4);
               } else {  // the end of K
                 for (int h = 0; b + h < end && h < S::deep; ++h)
-                  tc_mma_block<kPair>(d, wd + h * (kWBytes >> 4), xd + h * (x_bytes >> 4), id + h * with_byte(0, 1), col + 8,
-                                      col, b + h > begin, min(4, (a.K - (b + h) * kBlockK + 31) / 32));
+                  tc_mma_block<kPair>(d, wd + h * (kWBytes >> 4), xd + h * (x_bytes >> 4), id + h * kNext, col + 8, xcol,
+                                      b + h > begin, min(4, (a.K - (b + h) * kBlockK + 31) / 32));
               }
               tc_commit<kPair>(empty_bar(stage));
               if (b + S::deep >= whole) tc_commit<kPair>(afull_bar(na & 1));
@@ -830,6 +850,14 @@ int pairs_at_once() {
   return known[dev];
 }
 
+// CTAs that share a tile, where there are fewer tiles than CTAs that run at one time.
+int split_of(long long tiles, int pieces, long long slots) {
+  int split = 1;
+  if (pieces > 1)
+    while (split < kMostSplit && tiles * split * 2 <= slots) split *= 2;
+  return split;
+}
+
 template <int kCols, bool kPair, int kFrom = kFromRows>
 cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   using S = Shape<kCols, kPair>;
@@ -860,8 +888,7 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   a.tiles = a.tiles_n * a.tiles_t;
   a.split = 1;
   // a cluster's CTAs share a tile where there are too few tiles; what they send each other is held in 32 KB
-  if (!S::wide && a.pieces > 1)
-    while (a.split < kMostSplit && (long long)a.tiles * a.split * 2 <= slots) a.split *= 2;
+  if (!S::wide) a.split = split_of(a.tiles, a.pieces, slots);
   if (a.split > 1 && a.tn > 8 * a.split) a.split = 1;
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
   const int room = (S::smem - 1024 - kHeader - recv) / (S::deep * (kWBytes + a.tn / S::ctas * kBlockK));
@@ -931,14 +958,19 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
 }
 
 cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, const Fp8Gemm& g, cudaStream_t s) {
-  // Where a cluster shares a tile each CTA quantizes its part of K on the way (one token x 5120 x 4096: 7 us, 9.9 with a
-  // launch before it); CTAs that go from tile to tile would do it again for each.
-  if ((g.T <= 16 && (g.N + kRows - 1) / kRows <= num_sms()) || clusters_fit(g, 16)) {
-    Args a = common_args(g);
-    a.x16 = x;
-    a.x16_stride = x_stride;
+  // Where a cluster shares a tile each CTA quantizes its part of K on the way; CTAs that go from tile to tile would do it
+  // again for each. (One token x 5120 x 4096 7.5 us, 10.0 with a launch before it; 16 tokens 9.4 and 10.6; 32 tokens x 4096
+  // x 4096, 512 values of K a CTA, 9.5 and 10.1, but x 11008, 1536 values, 16.9 and 14.8: the quantizing takes longer than
+  // the tiles of w.)
+  Args a = common_args(g);
+  a.x16 = x;
+  a.x16_stride = x_stride;
+  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * Shape<16, false>::per_sm;
+  const int split = split_of(rows, a.pieces, slots);
+  if ((g.T <= 16 && split > 1) || clusters_fit(g, 16))
     return dtype == MOE_BF16 ? launch<16, false, MOE_BF16>(g, a, s) : launch<16, false, MOE_FP16>(g, a, s);
-  }
+  if (g.T <= 32 && split > 1 && (a.pieces + split - 1) / split * a.piece <= 512)
+    return dtype == MOE_BF16 ? launch<32, false, MOE_BF16>(g, a, s) : launch<32, false, MOE_FP16>(g, a, s);
   const cudaError_t e = launch_fp8_quantize(x, x_stride, g.T, g.K, dtype, g.x, s);
   return e != cudaSuccess ? e : launch_fp8_gemm(g, s);
 }

@@ -58,25 +58,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) fp8_quantize_kernel(const uin
       ++row;
     }
     next = ask(row, word);
-    const uint32_t bits[8] = {now.a.x, now.a.y, now.a.z, now.a.w, now.b.x, now.b.y, now.b.z, now.b.w};
-    float v[16], amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = unpack2<kType>(bits[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-      amax = fmaxf(amax, fmaxf(finite_size(f.x), finite_size(f.y)));
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    const uint32_t words_now[8] = {now.a.x, now.a.y, now.a.z, now.a.w, now.b.x, now.b.y, now.b.z, now.b.w};
+    const uint32_t most = block_max_bits<kType, 8>(words_now);
+    float amax = unpack2<kType>(most).x;
+    if (__any_sync(~0u, most >= kInfinityBits<kType>)) amax = finite_block_max<kType, 8>(words_now);
     const uint32_t scale = e8m0_of(amax);
-    if (k < K) {
-      const float inv = e8m0_inverse(scale);
-      uint32_t c[4];
+    const float inv = e8m0_inverse(scale);
+    uint32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = e4m3x4_of(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x4_of<kType>(words_now[2 * i], words_now[2 * i + 1], inv);
+    if (k < K)
       *reinterpret_cast<uint4*>(out.codes + (long long)r * out.row_stride + k) = make_uint4(c[0], c[1], c[2], c[3]);
-    }
     uint32_t all = (w * 512 + (lane & ~7) * 16 < K ? scale : kNoScale) << (8 * (lane >> 3));
     all |= __shfl_xor_sync(~0u, all, 8);
     all |= __shfl_xor_sync(~0u, all, 16);

@@ -248,16 +248,27 @@ def _norm_weight(name, w, dim, device: int):
 
 def _gate(g, dtype, shape, device: int):
     """A factor for each element, by broadcasting: sizes of 1 are held along. Address and strides."""
-    if g.dim() == 2 and shape[1] == 1:
-        g = g.unsqueeze(1)
     if g.dtype is not dtype or g.get_device() != device:
         raise ValueError(f"gate must be {dtype} on cuda:{device}, got {g.dtype} on {g.device}")
-    if g.dim() != 3 or any(a != b and a != 1 for a, b in zip(g.shape, shape)):
-        raise ValueError(f"gate must broadcast to {tuple(shape)}, got {tuple(g.shape)}")
-    ts, hs, ds = (0 if n == 1 else s for n, s in zip(g.shape, g.stride()))
-    if ds not in (0, 1) or ds == 1 and (ts % 8 or hs % 8):
+    tokens, heads, dim = shape
+    sizes, strides = g.shape, g.stride()
+    if len(sizes) == 3:
+        (t, h, d), (ts, hs, ds) = sizes, strides
+    elif len(sizes) == 2 and heads == 1:
+        (t, d), h, (ts, ds), hs = sizes, 1, strides, 0
+    else:
+        raise ValueError(f"gate must broadcast to {tuple(shape)}, got {tuple(sizes)}")
+    if t != tokens and t != 1 or h != heads and h != 1 or d != dim and d != 1:
+        raise ValueError(f"gate must broadcast to {tuple(shape)}, got {tuple(sizes)}")
+    if t == 1:
+        ts = 0
+    if h == 1:
+        hs = 0
+    if d == 1:
+        ds = 0
+    if ds != 0 and ds != 1 or ds == 1 and (ts % 8 or hs % 8):
         raise ValueError(f"gate: the last dimension must be contiguous (or 1) and the other strides multiples of 8 "
-                         f"elements, got {g.stride()}")
+                         f"elements, got {strides}")
     return g.data_ptr(), ts, hs, ds
 
 

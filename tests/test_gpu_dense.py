@@ -218,7 +218,7 @@ def test_results_past_the_types_largest_are_infinite(cuda):
 
 
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp32")])
-@pytest.mark.parametrize("t,n,k", [(1, 300, 1040), (12, 500, 4096), (16, 257, 80), (17, 384, 2048), (64, 1000, 512), (200, 640, 4112), (1000, 256, 528)])
+@pytest.mark.parametrize("t,n,k", [(1, 300, 1040), (12, 500, 4096), (16, 257, 80), (17, 384, 2048), (25, 640, 9216), (32, 20000, 1024), (29, 130, 20480), (9, 25000, 528), (64, 1000, 512), (70, 100, 4096), (200, 640, 4112), (1000, 256, 528)])
 def test_linear_is_quantizing_then_the_product(cuda, t, n, k, dtype, out):
     x = normal((t, k + 24), dtype, t)[:, 8:8 + k]
     w = quantize(normal((n, k), "bf16", n, k ** -0.5))
