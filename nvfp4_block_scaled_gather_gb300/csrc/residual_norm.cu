@@ -15,8 +15,8 @@
 //  * Longer rows, many of them: CTAs stay and take row after row, the next
 //    one's values on their way while the present one is worked on; the norms'
 //    weights wait in shared memory (read from L2 for every row they would be
-//    as many bytes again). Up to 8192 values the rows come to shared memory by
-//    bulk copies, longer ones to registers.
+//    as many bytes again). The rows come to shared memory by bulk copies; the
+//    longest, which would not fit beside the weights, to registers.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -385,11 +385,12 @@ __global__ void __launch_bounds__(kStay ? 512 : 1024)
   }
 }
 
-// Rows of 257 to 8192, many of them: the same with the rows brought to shared memory by bulk copies, kSlots of them on
+// Rows of 257 to kMaxStreamDim, many of them: the same with the rows brought to shared memory by bulk copies, kSlots of them on
 // their way or being worked on, which leaves the registers to the arithmetic.
 constexpr int kSlots = 2;
+constexpr int kMaxStreamDim = 14080;  // weights and slots within 225,280 bytes
 template <int kType, int NV>
-__global__ void __launch_bounds__(512, 2)
+__global__ void __launch_bounds__(512, NV == 4 ? 1 : 2)
     residual_norm_stream(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
   extern __shared__ float4 weights[];  // post (each eight values' first four, then their others), pre, then the slots
   __shared__ float sums[2][2][64];
@@ -503,7 +504,7 @@ template <int kType, int NV>
 cudaError_t launch_stream(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
   const int threads = ((a.dim / 8 + NV - 1) / NV + 31) / 32 * 32;
   const size_t smem = (size_t)a.dim * (8 + 4 * kSlots);
-  const cudaError_t err = allow_smem<residual_norm_stream<kType, NV>, 8192 * (8 + 4 * kSlots)>();
+  const cudaError_t err = allow_smem<residual_norm_stream<kType, NV>, kMaxStreamDim * (8 + 4 * kSlots)>();
   if (err != cudaSuccess) return err;
   const int by_threads = 1024 / threads, by_smem = (int)(220 * 1024 / (smem + 2304));
   int per_sm = by_threads < by_smem ? by_threads : by_smem;
@@ -524,6 +525,7 @@ cudaError_t launch_typed(const moe_residual_norm_t& a, const Shape& shape, cudaS
     return launch_pdl(residual_norm_rows<kType, 1, false>, dim3((unsigned)rows), dim3(threads), 0, s, a, shape);
   if (a.dim <= 2048) return launch_stream<kType, 1>(a, shape, s);
   if (a.dim <= 8192) return launch_stream<kType, 2>(a, shape, s);
+  if (a.dim <= kMaxStreamDim) return launch_stream<kType, 4>(a, shape, s);
   // rows whose weights and slots would not fit shared memory
   const size_t smem = (size_t)a.dim * 8;
   const cudaError_t err = allow_smem<residual_norm_rows<kType, 4, true>, 8 * kMaxNormDim>();
