@@ -51,15 +51,18 @@ __device__ __forceinline__ uint32_t e8m0_of(float amax) {
 // One over the scale, exactly (a byte of e8m0_of is at most 247).
 __device__ __forceinline__ float e8m0_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// Codes of two values over their scale, the first in the low byte. The
-// product is exact up to fp32's smallest values, so a code is rounded once.
-// (An infinity would become the largest code: times 0 first it is NaN.)
-__device__ __forceinline__ uint32_t e4m3x2_of(float a, float b, float inverse) {
-  a = fmaf(a, inverse, a * 0.0f);
-  b = fmaf(b, inverse, b * 0.0f);
+// Codes of two and four values, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) { return e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16); }
+// The same over a scale. The product is exact up to fp32's smallest values, so
+// a code is rounded once. (An infinity would become the largest code: times 0
+// first it is NaN.)
+__device__ __forceinline__ uint32_t e4m3x2_of(float a, float b, float inverse) {
+  return e4m3x2(fmaf(a, inverse, a * 0.0f), fmaf(b, inverse, b * 0.0f));
 }
 __device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d, float inverse) {
   return e4m3x2_of(a, b, inverse) | (e4m3x2_of(c, d, inverse) << 16);

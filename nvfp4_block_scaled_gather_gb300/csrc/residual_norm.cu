@@ -179,21 +179,39 @@ __device__ __forceinline__ void write_normed(const moe_residual_norm_t& a, int t
   y = times(times(y, pair_of(r, r)), w);
   if (mine && a.normed.data) *reinterpret_cast<uint4*>(place(a.normed, t, h, d)) = pack8<kType>(y);
   if (a.quantized.codes) {
-    float amax = 0.0f;
+    // magnitudes compared as whole numbers; an infinity or a NaN among a warp's takes it the way that leaves them out
+    constexpr uint32_t kInfinity = 0x7f800000u;
     float2 u[4];
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u[i] = split(y.p[i]);
-      amax = fmaxf(amax, fmaxf(finite_size(u[i].x), finite_size(u[i].y)));
+      m = max(m, max(__float_as_uint(u[i].x) & 0x7fffffffu, __float_as_uint(u[i].y) & 0x7fffffffu));
     }
-    if (!mine) amax = 0.0f;
+    if (!mine) m = 0;
 #pragma unroll
-    for (int o = 1; o < kWidth; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-    const uint32_t scale = e8m0_of(amax);
-    if (mine) {
+    for (int o = 1; o < kWidth; o <<= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+    uint32_t scale, lo, hi;
+    if (!__any_sync(~0u, m >= kInfinity)) {
+      scale = e8m0_of(__uint_as_float(m));
       const float inv = e8m0_inverse(scale);
-      *reinterpret_cast<uint2*>(a.quantized.codes + (long long)t * a.quantized.row_stride + d) =
-          make_uint2(e4m3x4_of(u[0].x, u[0].y, u[1].x, u[1].y, inv), e4m3x4_of(u[2].x, u[2].y, u[3].x, u[3].y, inv));
+      const F8 v = times(y, pair_of(inv, inv));
+      lo = e4m3x4(split(v.p[0]), split(v.p[1]));
+      hi = e4m3x4(split(v.p[2]), split(v.p[3]));
+    } else {
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(finite_size(u[i].x), finite_size(u[i].y)));
+      if (!mine) amax = 0.0f;
+#pragma unroll
+      for (int o = 1; o < kWidth; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+      scale = e8m0_of(amax);
+      const float inv = e8m0_inverse(scale);
+      lo = e4m3x4_of(u[0].x, u[0].y, u[1].x, u[1].y, inv);
+      hi = e4m3x4_of(u[2].x, u[2].y, u[3].x, u[3].y, inv);
+    }
+    if (mine) {
+      *reinterpret_cast<uint2*>(a.quantized.codes + (long long)t * a.quantized.row_stride + d) = make_uint2(lo, hi);
       if (d % kFp8Block == 0) {
         uint8_t* scales = a.quantized.scales + (long long)t * a.quantized.scale_stride;
         scales[d / kFp8Block] = (uint8_t)scale;
