@@ -12,15 +12,29 @@
 //    ascending order. So a launch may give the pieces of a tile to the CTAs
 //    of a cluster (few tiles: decode) or run them one after the other (many
 //    tiles) with the same bits.
-//  * Warp roles: four warps load scale words (a lane a row) and store them to
-//    tensor memory, all four lane quarters alike; four warps an accumulator's
-//    columns (one group, or two for wide tiles) add up pieces and write y;
-//    one warp loads tiles by TMA (128-byte swizzle) into a ring; one issues
-//    the MMAs, into two accumulators in turn.
+//  * Tiles: 16, 32 or 64 tokens x 128 rows of w, two CTAs an SM; or 240 tokens
+//    x 256 rows, two CTAs that share each MMA (a pair), one an SM.
+//  * Warp roles: one warp loads tiles by TMA (128-byte swizzle) into a ring;
+//    four bring scale words to shared memory (a lane a row), and where the
+//    tokens come as 16-bit rows, quantize them on the way; one issues the
+//    MMAs, into two accumulators in turn, and before a word's first one the
+//    copy of its scales to tensor memory; four, or eight of wide tiles, add up
+//    the pieces (a lane a row of w) and write y.
 //  * A cluster's CTAs send their pieces' sums to the CTA that adds a row up
 //    (distributed shared memory; CTA r has 128 / split of the tile's rows).
 //  * Every wait is bounded; on expiry the kernel records MOE_ERR_TIMEOUT,
 //    waits for its copies and MMAs, frees tensor memory and returns.
+//
+// What bounds it: of many tokens the tensor cores and the power limit. Between
+// stores a stage takes 965 cycles of the 960 that its MMAs need; a tile's 61 KB
+// of results hold the next tile up by an eighth of that at K = 4096, and the
+// clock falls (1.7 GHz with random codes, less with real ones): 8192 x 10240 x
+// 4096 takes 205 to 245 us, 2800 to 3350 TFLOP/s, where a large library product
+// of the same 8-bit values, without scales, takes 190 to 212 and with a scale
+// for each 32 values 216 to 220. Of decode batches over many rows of w the reads
+// of w (32 tokens x 100,003 x 4096: 67 us, 6.3 TB/s). Of small ones the chain
+// from the launch over the first tiles, the MMAs and the joined sums to the
+// store: 3.4 us for 256 x 1024, 6.6 for 5120 x 4096, one token.
 #include <atomic>
 #include <cstdint>
 
@@ -531,71 +545,71 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
         }
       }
     } else {
-    // ================================ scale words ================================
-    // Group g of 32 rows is warp g % 4's: w's rows, then the tokens'. A lane has a row's word, in its place of the atom
-    // that the MMA warp copies to tensor memory. (Stores from here to tensor memory wait for the MMAs that are queued.)
-    // Words are asked for kAhead ahead, each set in registers of its own (moving them would wait for them).
-    constexpr int kMine = (4 + S::xs_words + 3) / 4;
-    struct Words {
-      uint32_t v[kMine];
-    };
-    constexpr int kAhead = 4;
-    Words q[kAhead];
-    int i = b0 < b1 ? first : a.tiles, b = b0;  // of the next words to ask for
-    const uint8_t* from[kMine];                 // this lane's rows' scales, or none
-    auto enter = [&] {
-      const Place at = place_of(i, a);
-      const int n = at.n * S::tile_rows + half * kRows + 32 * warp + lane;
-      from[0] = n < a.N ? a.ws + n * a.ws_stride : nullptr;
+      // ================================ scale words ================================
+      // Group g of 32 rows is warp g % 4's: w's rows, then the tokens'. A lane has a row's word, in its place of the atom
+      // that the MMA warp copies to tensor memory. (Stores from here to tensor memory wait for the MMAs that are queued.)
+      // Words are asked for kAhead ahead, each set in registers of its own (moving them would wait for them).
+      constexpr int kMine = (4 + S::xs_words + 3) / 4;
+      struct Words {
+        uint32_t v[kMine];
+      };
+      constexpr int kAhead = 4;
+      Words q[kAhead];
+      int i = b0 < b1 ? first : a.tiles, b = b0;  // of the next words to ask for
+      const uint8_t* from[kMine];                 // this lane's rows' scales, or none
+      auto enter = [&] {
+        const Place at = place_of(i, a);
+        const int n = at.n * S::tile_rows + half * kRows + 32 * warp + lane;
+        from[0] = n < a.N ? a.ws + n * a.ws_stride : nullptr;
 #pragma unroll
-      for (int c = 1; c < kMine; ++c) {
-        const int first_row = 32 * (warp + 4 * (c - 1)), t = at.t * a.tn + first_row + lane;
-        from[c] = first_row < a.tn && t < a.T ? a.xs + t * a.xs_stride : nullptr;
-      }
-    };
-    auto ask = [&](Words& r) {
-      if (i >= a.tiles) return;
-#pragma unroll
-      for (int c = 0; c < kMine; ++c) r.v[c] = from[c] ? ld_cg(reinterpret_cast<const uint32_t*>(from[c] + b)) : 0u;
-      b += 4;
-      if (b >= b1) {
-        b = b0;
-        i += step;
-        if (i < a.tiles) enter();
-      }
-    };
-    if (i < a.tiles) enter();
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) ask(q[u]);
-    const uint32_t mine = first < a.tiles ? (uint32_t)((a.tiles - first + step - 1) / step * ((b2 - b0) / 4)) : 0u;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (uint32_t n = 0; n < mine && ok;) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u, ++n) {
-        if (n >= mine) break;
-        for (int j = 0; j < S::word_stages; ++j) {
-          ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
-          if (!ok) break;
-          if (j == 0) {
-            // (the copies of the word before the last one, from this slot, are done as its MMAs are)
-            uint8_t* atoms = smem + 1024 + (n % kScaleSlots) * S::slot_bytes + lane * 16 + warp * 4;
-#pragma unroll
-            for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint32_t*>(atoms + c * 512) = q[u].v[c];
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          if (lane == 0) {
-            if constexpr (kPair) arrive_peer(peer(full_bar(stage), 0));
-            else mbar_arrive(full_bar(stage));
-          }
-          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+        for (int c = 1; c < kMine; ++c) {
+          const int first_row = 32 * (warp + 4 * (c - 1)), t = at.t * a.tn + first_row + lane;
+          from[c] = first_row < a.tn && t < a.T ? a.xs + t * a.xs_stride : nullptr;
         }
-        if (!ok) break;
-        ask(q[u]);
+      };
+      auto ask = [&](Words& r) {
+        if (i >= a.tiles) return;
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) r.v[c] = from[c] ? ld_cg(reinterpret_cast<const uint32_t*>(from[c] + b)) : 0u;
+        b += 4;
+        if (b >= b1) {
+          b = b0;
+          i += step;
+          if (i < a.tiles) enter();
+        }
+      };
+      if (i < a.tiles) enter();
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) ask(q[u]);
+      const uint32_t mine = first < a.tiles ? (uint32_t)((a.tiles - first + step - 1) / step * ((b2 - b0) / 4)) : 0u;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (uint32_t n = 0; n < mine && ok;) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u, ++n) {
+          if (n >= mine) break;
+          for (int j = 0; j < S::word_stages; ++j) {
+            ok = wait_warp(empty_bar(stage), phase ^ 1u, ctl);
+            if (!ok) break;
+            if (j == 0) {
+              // (the copies of the word before the last one, from this slot, are done as its MMAs are)
+              uint8_t* atoms = smem + 1024 + (n % kScaleSlots) * S::slot_bytes + lane * 16 + warp * 4;
+#pragma unroll
+              for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint32_t*>(atoms + c * 512) = q[u].v[c];
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
+            if (lane == 0) {
+              if constexpr (kPair) arrive_peer(peer(full_bar(stage), 0));
+              else mbar_arrive(full_bar(stage));
+            }
+            if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          ask(q[u]);
+        }
       }
-    }
     }
   } else if (warp >= S::load_warp) {
     if constexpr (S::wide) give_registers<S::few>();
