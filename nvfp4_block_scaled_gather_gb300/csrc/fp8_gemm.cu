@@ -321,6 +321,15 @@ __device__ __forceinline__ Place place_of(int i, const Args& a) {
   return {group * kHigh + in - t * high, t};
 }
 
+// Two sums in one instruction.
+__device__ __forceinline__ void add_pair(float& a, float& b, uint32_t x, uint32_t y) {
+  asm("{\n\t.reg .b64 s, t;\n\t"
+      "mov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, t;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}\n"
+      : "+f"(a), "+f"(b)
+      : "r"(x), "r"(y));
+}
 __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
   const long long at = (long long)t * a.y_stride + n;
   if (a.y_dtype == MOE_FP32)
@@ -752,8 +761,8 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
               if (c + j < S::acc) tc_ld8(from + c + j, v + j);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < S::asked; ++j)
-              if (c + j < S::acc) sum[c + j] += __uint_as_float(v[j]);
+            for (int j = 0; j < S::asked; j += 2)
+              if (c + j < S::acc) add_pair(sum[c + j], sum[c + j + 1], v[j], v[j + 1]);
           }
         } else {
           const uint32_t cta = row / slice;
