@@ -239,9 +239,7 @@ def _part(name, t, dtype, tokens, heads, dim, device: int):
 
 
 def _norm_weight(name, w, dim, device: int):
-    if w is None:
-        return 0
-    if w.dtype is not _FLOAT32 or w.dim() != 1 or w.numel() != dim or not w.is_contiguous() or w.get_device() != device:
+    if w.dtype is not _FLOAT32 or w.shape != (dim,) or not w.is_contiguous() or w.get_device() != device:
         raise ValueError(f"{name} must be a contiguous float32 tensor {(dim,)} on cuda:{device}")
     return w.data_ptr()
 
@@ -294,20 +292,27 @@ def moe_residual_norm(x, block=None, *, y=None, normed=None, quantized: Fp8Rows 
         raise ValueError(f"x must be [tokens, dim] or [tokens, heads, dim], got {tuple(shape)}")
     if max(shape) > _MOST:
         raise ValueError(f"x must have less than 2**31 of each, got {tuple(shape)}")
-    sizes = (dtype, tokens, heads, dim, dev)
+    # of tensors like x without gaps (the usual ones) all is known but the address
+    whole = (heads * dim if tokens > 1 else 0, dim if heads > 1 else 0)
+
+    def part(name, t):
+        if t is None:
+            return _NO_PART
+        if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
+            return (t.data_ptr(), *whole)
+        return _part(name, t, dtype, tokens, heads, dim, dev)
+
     rows = _NO_ROWS
     if quantized is not None:
         rows = _rows_of("quantized", quantized, dev)
         if quantized.n != tokens or quantized.k != dim or heads != 1:
             raise ValueError(f"quantized must have {tokens} rows of {dim} (of one head), got {quantized.n} of {quantized.k}")
-    args = _norm_bytes(tokens, heads, dim, code, *_part("x", x, *sizes),
-                       *(_NO_PART if block is None else _part("block", block, *sizes)),
+    args = _norm_bytes(tokens, heads, dim, code, *part("x", x), *part("block", block),
                        *(_NO_GATE if gate is None else _gate(gate, dtype, (tokens, heads, dim), dev)), 0,
                        residual_scale, eps, 1 if post_norm else 0, 0,
                        0 if post_weight is None else _norm_weight("post_weight", post_weight, dim, dev),
                        0 if pre_weight is None else _norm_weight("pre_weight", pre_weight, dim, dev),
-                       *(_NO_PART if y is None else _part("y", y, *sizes)),
-                       *(_NO_PART if normed is None else _part("normed", normed, *sizes))) + rows
-    status = load().moe_residual_norm(args, _stream(stream, dev))
+                       *part("y", y), *part("normed", normed)) + rows
+    status = (_LIB or load()).moe_residual_norm(args, _stream(stream, dev))
     if status:
         _check("moe_residual_norm", status)
