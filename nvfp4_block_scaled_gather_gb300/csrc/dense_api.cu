@@ -50,7 +50,7 @@ int norm_status(const moe_residual_norm_t* a) {
   if (!a || a->tokens < 0 || a->heads <= 0 || a->dim <= 0 || !dtype_ok(a->dtype)) return MOE_ERR_INVALID;
   if (!std::isfinite(a->eps) || !(a->eps > 0) || !std::isfinite(a->residual_scale)) return MOE_ERR_INVALID;
   if (a->post_norm != 0 && a->post_norm != 1) return MOE_ERR_INVALID;
-  if (!a->block.data && (a->post_norm || a->gate.data || a->y.data)) return MOE_ERR_INVALID;
+  if (a->tokens > 0 && !a->block.data && (a->post_norm || a->gate.data || a->y.data)) return MOE_ERR_INVALID;
   if (a->post_weight && !a->post_norm) return MOE_ERR_INVALID;
   if (!a->y.data && !a->normed.data && !a->quantized.codes && a->tokens > 0) return MOE_ERR_INVALID;
   if (a->dim % 8 || a->dim > kMaxNormDim || (long long)a->tokens * a->heads > 0x7fffffffLL) return MOE_ERR_SHAPE;

@@ -1,4 +1,8 @@
 """The dense operators on the GPU against their definitions in 64 bits."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +12,8 @@ from nvfp4_block_scaled_gather_gb300 import dense as D
 from oracle import dense as OD
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}   # half a step, relative
@@ -251,6 +257,49 @@ def test_nothing_to_do(cuda):
     D.moe_residual_norm(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"))
     torch.cuda.synchronize()
     assert N.check_status() == 0
+
+
+def test_no_tokens_of_everything(cuda):
+    """Tensors without elements have no address."""
+    x, ones = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), torch.ones(64, device="cuda")
+    D.moe_residual_norm(x, x.clone(), y=x.clone(), normed=x.clone(), quantized=D.Fp8Rows.empty(0, 64), pre_weight=ones,
+                        post_norm=True, post_weight=ones, gate=torch.ones((1, 64), dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+    assert N.check_status() == 0
+
+
+FIRST_CALLS = """
+import torch
+from nvfp4_block_scaled_gather_gb300 import _native as N, dense as D
+rows = [torch.randn((t, 1040), device="cuda").bfloat16() for t in (1, 20, 300)]
+w, ones = D.Fp8Rows.empty(384, 1040), torch.ones(1040, device="cuda")
+w.codes.view(torch.uint8).copy_(torch.randint(0, 120, (384, 1040), device="cuda"))
+w.scales.fill_(120)
+def outputs():
+    return [(torch.zeros_like(x), D.Fp8Rows.empty(*x.shape), torch.zeros((x.shape[0], 384), device="cuda"),
+             torch.zeros((x.shape[0], 384), device="cuda"), D.linear_workspace(*x.shape)) for x in rows]
+def calls(outs):
+    for x, (n, q, y, z, ws) in zip(rows, outs):
+        D.moe_residual_norm(x, x, y=n, quantized=q, pre_weight=ones, post_norm=True)
+        D.moe_fp8_gemm(q, w, y)
+        D.moe_fp8_linear(x, w, z, ws)
+captured, eager = outputs(), outputs()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls(captured)
+graph.replay()
+calls(eager)
+torch.cuda.synchronize()
+assert N.check_status() == 0
+for a, b in zip(captured, eager):
+    assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2]) and torch.equal(a[3], b[3]) and a[2].any() and a[3].any()
+"""
+
+
+def test_a_process_whose_first_calls_are_captured(cuda):
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_a_graph_replays_products_on_new_inputs_and_another_stream(cuda):
