@@ -5,18 +5,25 @@
 // bytes (a row of 4096 moves 32 KB for 50,000 operations).
 //
 // A sum of squares is: eight values, a tree over the 32 threads that have 256
-// values together, and a tree over those sums (for rows of more). It does not depend on how a launch spreads rows over threads, so a
-// row's bits are the same in every call.
+// values together, and a tree over those sums (for rows of more). It does not
+// depend on how a launch spreads rows over threads, so a row's bits are the
+// same in every call.
 //
 //  * Rows of at most 256: 8, 16 or 32 threads a row, several rows a thread in
-//    flight (the heads of queries and keys).
+//    flight (the heads of queries and keys; 3001 x 40 heads of 128: 15 us, where
+//    a CTA a row took 46).
 //  * Longer rows, few of them (decode): a CTA a row, eight values a thread,
-//    everything asked for at once.
-//  * Longer rows, many of them: CTAs stay and take row after row, the next
-//    one's values on their way while the present one is worked on; the norms'
-//    weights wait in shared memory (read from L2 for every row they would be
-//    as many bytes again). The rows come to shared memory by bulk copies; the
-//    longest, which would not fit beside the weights, to registers.
+//    everything asked for at once (one row of 4096 2.3 us, 200 x 7168 6.5, 777 x
+//    2184 4.9: launch, and one load, two sums and one store after the other).
+//  * Longer rows, many of them: a CTA an SM stays, its groups of threads take row
+//    after row, the next ones on their way while the present ones are worked on;
+//    one copy of the norms' weights waits in shared memory (read from L2 for
+//    every row they would be as many bytes again). The rows come to shared
+//    memory by bulk copies: 16,384 x 4096 with both norms 84 us, 6.4 TB/s (120
+//    with a CTA a row); to 8-bit rows 8192 x 4096 48 us, 4.9 TB/s, short of
+//    issue slots.
+//  * The longest, whose weights and rows would not fit shared memory, come to
+//    registers.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -179,21 +186,20 @@ __device__ __forceinline__ void write_normed(const moe_residual_norm_t& a, int t
   y = times(times(y, pair_of(r, r)), w);
   if (mine && a.normed.data) *reinterpret_cast<uint4*>(place(a.normed, t, h, d)) = pack8<kType>(y);
   if (a.quantized.codes) {
-    // magnitudes compared as whole numbers; an infinity or a NaN among a warp's takes it the way that leaves them out
-    constexpr uint32_t kInfinity = 0x7f800000u;
+    // (a maximum leaves NaN out; an infinity among a warp's takes it the way that leaves those out)
     float2 u[4];
-    uint32_t m = 0;
+    float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u[i] = split(y.p[i]);
-      m = max(m, max(__float_as_uint(u[i].x) & 0x7fffffffu, __float_as_uint(u[i].y) & 0x7fffffffu));
+      most = fmaxf(most, fmaxf(fabsf(u[i].x), fabsf(u[i].y)));
     }
-    if (!mine) m = 0;
+    if (!mine) most = 0.0f;
 #pragma unroll
-    for (int o = 1; o < kWidth; o <<= 1) m = max(m, __shfl_xor_sync(~0u, m, o));
+    for (int o = 1; o < kWidth; o <<= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
     uint32_t scale, lo, hi;
-    if (!__any_sync(~0u, m >= kInfinity)) {
-      scale = e8m0_of(__uint_as_float(m));
+    if (!__any_sync(~0u, most == INFINITY)) {
+      scale = e8m0_of(most);
       const float inv = e8m0_inverse(scale);
       const F8 v = times(y, pair_of(inv, inv));
       lo = e4m3x4(split(v.p[0]), split(v.p[1]));
@@ -290,17 +296,26 @@ __global__ void __launch_bounds__(kSmallThreads, kBlock ? 4 : 5) residual_norm_s
   }
 }
 
+// The threads that have a row together: all of a CTA's, or a group of its warps with a barrier of its own.
+struct Group {
+  int threads, thread, barrier;  // barrier 0: the CTA's
+};
+__device__ __forceinline__ void sync(const Group& g) {
+  if (g.barrier == 0) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(g.barrier), "r"(g.threads) : "memory");
+}
+
 // The sum over a row: a tree over the trees' sums of all its 256-value pieces (64 at most). `sums` is not written again
 // before the call after the next one.
 template <int NV>
-__device__ __forceinline__ float row_sum(const float (&s)[NV], float* sums) {
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pieces = NV * warps;
+__device__ __forceinline__ float row_sum(const Group& g, const float (&s)[NV], float* sums) {
+  const int warps = g.threads >> 5, warp = g.thread >> 5, lane = threadIdx.x & 31, pieces = NV * warps;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const float tree = tree_sum<32>(s[i]);
     if (lane == 0) sums[i * warps + warp] = tree;
   }
-  __syncthreads();
+  sync(g);
   float mine = lane < pieces ? sums[lane] : 0.0f;
   if (pieces > 32 && 32 + lane < pieces) mine += sums[32 + lane];
   return tree_sum<32>(mine);
@@ -313,6 +328,7 @@ __global__ void __launch_bounds__(kStay ? 512 : 1024)
   extern __shared__ float4 weights[];  // kStay: post (each eight values' first four, then their others), then pre
   __shared__ float sums[2][2][64];
   const int threads = blockDim.x, rows = a.tokens * a.heads;
+  const Group all = {threads, (int)threadIdx.x, 0};
   const bool has_block = a.block.data != nullptr;
   auto at = [&](int i) { return 8 * (i * threads + (int)threadIdx.x); };
   pdl_wait();
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kStay ? 512 : 1024)
       if (a.post_norm) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[i] = squares(unpack8<kType>(b[i]));
-        r = inverse_rms(row_sum<NV>(s, sums[turn][0]), shape);
+        r = inverse_rms(row_sum<NV>(all, s, sums[turn][0]), shape);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(kStay ? 512 : 1024)
     if (a.normed.data || a.quantized.codes) {  // (values past the row are 0)
 #pragma unroll
       for (int i = 0; i < NV; ++i) s[i] = squares(y[i]);
-      const float r = inverse_rms(row_sum<NV>(s, sums[turn][1]), shape);
+      const float r = inverse_rms(row_sum<NV>(all, s, sums[turn][1]), shape);
 #pragma unroll
       for (int i = 0; i < NV; ++i) write_normed<kType, 16>(a, t, h, at(i), at(i) < a.dim, y[i], r, held(pre, i, 2));
     }
@@ -403,21 +419,32 @@ __global__ void __launch_bounds__(kStay ? 512 : 1024)
   }
 }
 
-// Rows of 257 to kMaxStreamDim, many of them: the same with the rows brought to shared memory by bulk copies, kSlots of them on
-// their way or being worked on, which leaves the registers to the arithmetic.
+// Rows of 257 to kMaxStreamDim, many of them: the same with the rows brought to shared memory by bulk copies, kSlots of
+// them on their way or being worked on, which leaves the registers to the arithmetic. A CTA is an SM's: groups of threads
+// with a row each, beside one copy of the weights.
 constexpr int kSlots = 2;
 constexpr int kMaxStreamDim = 14080;  // weights and slots within 225,280 bytes
+constexpr int kMostGroups = 15;       // barriers 1 .. 15
+template <int NV>
+constexpr int kMostThreads = NV == 4 ? 512 : 1024;  // (a row's of more than 8192 values are one group)
 template <int kType, int NV>
-__global__ void __launch_bounds__(512, NV == 4 ? 1 : 2)
-    residual_norm_stream(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
+__global__ void __launch_bounds__(kMostThreads<NV>, 1)
+    residual_norm_stream(const __grid_constant__ moe_residual_norm_t a, const Shape shape, const int group_threads) {
   extern __shared__ float4 weights[];  // post (each eight values' first four, then their others), pre, then the slots
-  __shared__ float sums[2][2][64];
-  __shared__ uint64_t landed[kSlots];
-  const int threads = blockDim.x, rows = a.tokens * a.heads, eights = a.dim / 8, bytes = 2 * a.dim;
+  __shared__ float sums[2][2][NV * kMostThreads<NV> / 32];
+  __shared__ uint64_t all_landed[kMostGroups][kSlots];
+  const int threads = NV == 4 ? blockDim.x : group_threads;
+  const int rows = a.tokens * a.heads, eights = a.dim / 8, bytes = 2 * a.dim;
+  const int group = NV == 4 ? 0 : __shfl_sync(~0u, (int)threadIdx.x / threads, 0);
+  const Group mine = {threads, (int)threadIdx.x - group * threads, NV == 4 ? 0 : group + 1};
+  const int own = group * NV * (threads / 32);  // of sums
+  uint64_t(&landed)[kSlots] = all_landed[group];
   const bool has_block = a.block.data != nullptr;
-  uint8_t* slots = reinterpret_cast<uint8_t*>(weights + 4 * eights);
-  auto eighth = [&](int i) { return i * threads + (int)threadIdx.x; };
-  if (threadIdx.x == 0) {
+  uint8_t* slots = reinterpret_cast<uint8_t*>(weights + 4 * eights) + group * kSlots * 2 * bytes;
+  auto eighth = [&](int i) { return i * threads + mine.thread; };
+  // (rows go over the CTAs first)
+  const long long first = blockIdx.x + (long long)group * gridDim.x, step = (NV == 4 ? 1LL : (long long)(blockDim.x / threads)) * gridDim.x;
+  if (mine.thread == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(landed + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -432,9 +459,9 @@ __global__ void __launch_bounds__(512, NV == 4 ? 1 : 2)
     bulk_load(to, place(a.x, t, h, 0), bytes, bar);
     if (has_block) bulk_load(to + bytes, place(a.block, t, h, 0), bytes, bar);
   };
-  if (threadIdx.x == 0)
-    for (int i = 0; i < kSlots; ++i) bring(i, blockIdx.x + (long long)i * gridDim.x);
-  for (int d = 4 * threadIdx.x; d < a.dim; d += 4 * threads) {
+  if (mine.thread == 0)
+    for (int i = 0; i < kSlots; ++i) bring(i, first + i * step);
+  for (int d = 4 * threadIdx.x; d < a.dim; d += 4 * (int)blockDim.x) {
     const float4 one = make_float4(1, 1, 1, 1);
     const int to = d / 8 + (d & 4 ? eights : 0);
     weights[to] = a.post_weight ? ld_cg(reinterpret_cast<const float4*>(a.post_weight + d)) : one;
@@ -444,7 +471,7 @@ __global__ void __launch_bounds__(512, NV == 4 ? 1 : 2)
   const F8 none = {};
   int slot = 0, turn = 0;
   uint32_t parity = 0;
-  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+  for (long long row = first; row < rows; row += step) {
     const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
     uint4 g[NV];
     if (has_block && a.gate.data) {
@@ -465,7 +492,7 @@ __global__ void __launch_bounds__(512, NV == 4 ? 1 : 2)
           y[i] = eighth(i) < eights ? unpack8<kType>(b[eighth(i)]) : none;
           s[i] = squares(y[i]);
         }
-        r = inverse_rms(row_sum<NV>(s, sums[turn][0]), shape);
+        r = inverse_rms(row_sum<NV>(mine, s, sums[turn][0] + own), shape);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -487,11 +514,11 @@ __global__ void __launch_bounds__(512, NV == 4 ? 1 : 2)
     if (more) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) s[i] = squares(y[i]);
-      r = inverse_rms(row_sum<NV>(s, sums[turn][1]), shape);  // (everyone has read the slot)
+      r = inverse_rms(row_sum<NV>(mine, s, sums[turn][1] + own), shape);  // (everyone has read the slot)
     } else {
-      __syncthreads();
+      sync(mine);
     }
-    if (threadIdx.x == 0) bring(slot, row + (long long)kSlots * gridDim.x);
+    if (mine.thread == 0) bring(slot, row + kSlots * step);
     if (more) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -521,15 +548,20 @@ cudaError_t launch_small(const moe_residual_norm_t& a, const Shape& shape, cudaS
 template <int kType, int NV>
 cudaError_t launch_stream(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
   const int threads = ((a.dim / 8 + NV - 1) / NV + 31) / 32 * 32;
-  const size_t smem = (size_t)a.dim * (8 + 4 * kSlots);
-  const cudaError_t err = allow_smem<residual_norm_stream<kType, NV>, kMaxStreamDim * (8 + 4 * kSlots)>();
+  constexpr int most_smem = kMaxStreamDim * (8 + 4 * kSlots);
+  const cudaError_t err = allow_smem<residual_norm_stream<kType, NV>, most_smem>();
   if (err != cudaSuccess) return err;
-  const int by_threads = 1024 / threads, by_smem = (int)(220 * 1024 / (smem + 2304));
-  int per_sm = by_threads < by_smem ? by_threads : by_smem;
-  per_sm = per_sm < 1 ? 1 : per_sm > 32 ? 32 : per_sm;
-  const long long rows = (long long)a.tokens * a.heads, most = (long long)per_sm * num_sms();
-  return launch_pdl(residual_norm_stream<kType, NV>, dim3((unsigned)(rows < most ? rows : most)), dim3(threads), smem, s, a,
-                    shape);
+  const long long rows = (long long)a.tokens * a.heads, grid = rows < num_sms() ? rows : num_sms();
+  long long groups = (most_smem - 8 * a.dim) / (4 * kSlots * a.dim);
+  groups = groups < kMostThreads<NV> / threads ? groups : kMostThreads<NV> / threads;
+  groups = groups < kMostGroups ? groups : kMostGroups;
+  // 16-bit norms of more than 15,360 values at a time come and go more slowly (16,384 x 4096: three groups 84 us, four 95;
+  // 30,000 x 2048: six 78, seven 82, eight 87; 16,384 x 3840: three 83, four 81); 8-bit ones have fewer bytes to write and
+  // more to do (8192 x 4096: three 53, four 49)
+  if (a.normed.data && groups * a.dim > 15360) groups = 15360 / a.dim < 2 ? (groups < 2 ? groups : 2) : 15360 / a.dim;
+  groups = groups < (rows + grid - 1) / grid ? groups : (rows + grid - 1) / grid;
+  return launch_pdl(residual_norm_stream<kType, NV>, dim3((unsigned)grid), dim3((unsigned)(groups * threads)),
+                    (size_t)a.dim * (8 + 4 * kSlots * groups), s, a, shape, threads);
 }
 
 template <int kType>
@@ -541,7 +573,8 @@ cudaError_t launch_typed(const moe_residual_norm_t& a, const Shape& shape, cudaS
   const int threads = (a.dim / 8 + 31) / 32 * 32;
   if (rows * threads <= 2048LL * num_sms() && threads <= 1024)
     return launch_pdl(residual_norm_rows<kType, 1, false>, dim3((unsigned)rows), dim3(threads), 0, s, a, shape);
-  if (a.dim <= 2048) return launch_stream<kType, 1>(a, shape, s);
+  // (sixteen values a thread: 30,000 x 2048 78 us, 93 with eight; x 1024 44.5 and 49.7; but 50,000 x 520 62.5 and 57.4)
+  if (a.dim <= 768) return launch_stream<kType, 1>(a, shape, s);
   if (a.dim <= 8192) return launch_stream<kType, 2>(a, shape, s);
   if (a.dim <= kMaxStreamDim) return launch_stream<kType, 4>(a, shape, s);
   // rows whose weights and slots would not fit shared memory
