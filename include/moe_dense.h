@@ -104,7 +104,8 @@ int moe_fp8_gemm(const moe_fp8_rows_t* x, int T, const moe_fp8_rows_t* w, int N,
 
 /* moe_fp8_quantize_rows of x [T, K], then moe_fp8_gemm: the same bits.
  * workspace: moe_fp8_linear_workspace_size(T, K) bytes, 256-byte aligned, any
- * contents; calls that share one run in stream order. */
+ * contents; calls that share one run in stream order. (Calls of few tokens
+ * quantize on the way and leave it as it is.) */
 size_t moe_fp8_linear_workspace_size(int T, int K);
 int moe_fp8_linear(const uint16_t* x, long long x_stride, int T, int K, int dtype, const moe_fp8_rows_t* w, int N,
                    void* y, long long y_stride, int y_dtype, void* workspace, size_t ws_bytes, cudaStream_t stream);

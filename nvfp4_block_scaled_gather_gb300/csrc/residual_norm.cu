@@ -13,14 +13,14 @@
 //    flight (the heads of queries and keys; 3001 x 40 heads of 128: 15 us, where
 //    a CTA a row took 46).
 //  * Longer rows, few of them (decode): a CTA a row, eight values a thread,
-//    everything asked for at once (one row of 4096 2.3 us, 200 x 7168 6.5, 777 x
-//    2184 4.9: launch, and one load, two sums and one store after the other).
+//    everything asked for at once (one row of 4096 2.3 us, 152 rows 3.1: launch,
+//    and one load, two sums and one store after the other).
 //  * Longer rows, many of them: a CTA an SM stays, its groups of threads take row
 //    after row, the next ones on their way while the present ones are worked on;
 //    one copy of the norms' weights waits in shared memory (read from L2 for
 //    every row they would be as many bytes again). The rows come to shared
 //    memory by bulk copies: 16,384 x 4096 with both norms 84 us, 6.4 TB/s (120
-//    with a CTA a row); to 8-bit rows 8192 x 4096 48 us, 4.9 TB/s, short of
+//    with a CTA a row); to 8-bit rows 8192 x 4096 47 us, 5.0 TB/s, short of
 //    issue slots.
 //  * The longest, whose weights and rows would not fit shared memory, come to
 //    registers.
@@ -230,7 +230,8 @@ __device__ __forceinline__ void write_normed(const moe_residual_norm_t& a, int t
 
 // Rows of at most 8 G values, G threads each, kRows rows of a thread at a time. kBlock: with a block's output.
 template <int kType, int G, int kRows, bool kBlock>
-__global__ void __launch_bounds__(kSmallThreads, kBlock ? 4 : 5) residual_norm_small(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
+__global__ void __launch_bounds__(kSmallThreads, kBlock ? 4 : 5)
+    residual_norm_small(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
   pdl_wait();
   pdl_trigger();
   constexpr int kPer = kSmallThreads / G;
@@ -443,7 +444,8 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
   uint8_t* slots = reinterpret_cast<uint8_t*>(weights + 4 * eights) + group * kSlots * 2 * bytes;
   auto eighth = [&](int i) { return i * threads + mine.thread; };
   // (rows go over the CTAs first)
-  const long long first = blockIdx.x + (long long)group * gridDim.x, step = (NV == 4 ? 1LL : (long long)(blockDim.x / threads)) * gridDim.x;
+  const long long first = blockIdx.x + (long long)group * gridDim.x;
+  const long long step = (NV == 4 ? 1LL : (long long)(blockDim.x / threads)) * gridDim.x;
   if (mine.thread == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(landed + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -471,14 +473,19 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
   const F8 none = {};
   int slot = 0, turn = 0;
   uint32_t parity = 0;
+  // the gate, asked for a row ahead (16,384 x 4096, a factor for each element: 104 us, 107 where it was asked for with its
+  // own row)
+  uint4 g[NV];
+  auto ask_gate = [&](long long row) {
+    if (!has_block || !a.gate.data || row >= rows) return;
+    const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      g[i] = eighth(i) < eights ? load_gate(a.gate, t, h, 8 * eighth(i)) : make_uint4(0, 0, 0, 0);
+  };
+  ask_gate(first);
   for (long long row = first; row < rows; row += step) {
     const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
-    uint4 g[NV];
-    if (has_block && a.gate.data) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        g[i] = eighth(i) < eights ? load_gate(a.gate, t, h, 8 * eighth(i)) : make_uint4(0, 0, 0, 0);
-    }
     wait_landed(smem_u32(landed + slot), parity, shape.status);
     const uint4* x = reinterpret_cast<const uint4*>(slots + slot * 2 * bytes);
     const uint4* b = x + eights;
@@ -505,6 +512,7 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
         y[i] = add_block<kType>(a, g[i], v, r, x[e]);
         if (a.y.data) *reinterpret_cast<uint4*>(place(a.y, t, h, 8 * e)) = pack8<kType>(y[i]);
       }
+      ask_gate(row + step);
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) y[i] = eighth(i) < eights ? unpack8<kType>(x[eighth(i)]) : none;
@@ -571,7 +579,10 @@ cudaError_t launch_typed(const moe_residual_norm_t& a, const Shape& shape, cudaS
   if (a.dim <= 256) return launch_small<kType, 32>(a, shape, s);
   const long long rows = (long long)a.tokens * a.heads;
   const int threads = (a.dim / 8 + 31) / 32 * 32;
-  if (rows * threads <= 2048LL * num_sms() && threads <= 1024)
+  // a CTA a row where all run at one time, up to four an SM (one row of 4096 2.3 us, 2.9 by groups; 304 rows 3.9 and 4.4;
+  // but 400 rows 6.0 and 5.1, 180 of 7168 6.4 and 5.3, 1000 of 512 3.2 and 3.0)
+  const int at_once = threads > 1024 ? 0 : threads > 256 ? 1024 / threads : 4;
+  if (rows <= (long long)at_once * num_sms())
     return launch_pdl(residual_norm_rows<kType, 1, false>, dim3((unsigned)rows), dim3(threads), 0, s, a, shape);
   // (sixteen values a thread: 30,000 x 2048 78 us, 93 with eight; x 1024 44.5 and 49.7; but 50,000 x 520 62.5 and 57.4)
   if (a.dim <= 768) return launch_stream<kType, 1>(a, shape, s);
