@@ -430,6 +430,16 @@ def test_the_residual_step(cuda, t, h, d, dtype, gate, post):
     assert N.check_status() == 0
 
 
+@pytest.mark.parametrize("t,h,d", [(3001, 1, 264), (911, 1, 512), (700, 1, 776), (1300, 1, 1024), (333, 3, 2048), (40, 19, 2184), (611, 1, 3840),
+                                   (460, 1, 4096), (320, 1, 5120), (170, 1, 7168), (305, 1, 8192), (330, 1, 8200), (160, 1, 14080),
+                                   (155, 1, 14088), (310, 1, 16384)])
+@pytest.mark.parametrize("dtype,gate,post", [("bf16", "none", True), ("fp16", "channel", False), ("fp16", "token", True), ("bf16", "element", True),
+                                             ("bf16", "head", False)])
+def test_the_residual_step_of_many_rows(cuda, t, h, d, dtype, gate, post):
+    """More rows than run at one time: groups of threads, or CTAs, go from row to row."""
+    test_the_residual_step(cuda, t, h, d, dtype, gate, post)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_heads_within_wider_rows(cuda, dtype):
     """Queries and keys of one product's rows, normed in place; the values behind them stay."""
