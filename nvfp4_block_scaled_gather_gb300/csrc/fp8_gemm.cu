@@ -873,12 +873,13 @@ int pairs_at_once() {
   return known[dev];
 }
 
-// CTAs that share a tile, where there are fewer tiles than CTAs that run at one time.
-int split_of(long long tiles, int pieces, long long slots) {
+// CTAs that share a tile of tn tokens, where there are fewer tiles than CTAs that run at one time; what they send each
+// other is held in 32 KB.
+int split_of(long long tiles, int pieces, long long slots, int tn = 16) {
   int split = 1;
   if (pieces > 1)
     while (split < kMostSplit && tiles * split * 2 <= slots) split *= 2;
-  return split;
+  return tn > 8 * split ? 1 : split;
 }
 
 template <int kCols, bool kPair, int kFrom = kFromRows>
@@ -910,9 +911,7 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   a.tiles_t = (g.T + a.tn - 1) / a.tn;
   a.tiles = a.tiles_n * a.tiles_t;
   a.split = 1;
-  // a cluster's CTAs share a tile where there are too few tiles; what they send each other is held in 32 KB
-  if (!S::wide) a.split = split_of(a.tiles, a.pieces, slots);
-  if (a.split > 1 && a.tn > 8 * a.split) a.split = 1;
+  if (!S::wide) a.split = split_of(a.tiles, a.pieces, slots, a.tn);
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
   const int room = (S::smem - 1024 - kHeader - recv) / (S::deep * (kWBytes + a.tn / S::ctas * kBlockK));
   a.stages = room < S::most_stages ? room : S::most_stages;
@@ -961,22 +960,34 @@ Args common_args(const Fp8Gemm& g) {
   return a;
 }
 
+constexpr int kNarrowPerSm = Shape<16, false>::per_sm;
+
 // Whether all tiles of so many tokens run at one time, a cluster each.
 bool clusters_fit(const Fp8Gemm& g, int cols) {
-  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * Shape<16, false>::per_sm;
+  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
   return rows * ((g.T + cols - 1) / cols) * kMostSplit <= slots;
 }
 
 }  // namespace
 
-// The narrowest tiles of which a cluster each runs at one time: few tokens, or little of everything. Else the narrowest
-// that hold all tokens of a decode batch (every row of w is read once), or pairs. (64 tokens x 4096 x 11008: 15 us in
-// clusters, 22 in pairs; x 5120 x 4096, more tiles than run at once: 17 and 11.)
+// The narrowest tiles that hold all tokens of a decode batch (every row of w is read once), or of which a cluster each
+// runs at one time; else pairs. A pair's time goes with K (from 3.5 us, and 1.3 for each 1024 values), a cluster's with
+// the sums that it sends, T N (from 3.5 us, and 1.8 for each 100,000): 64 tokens x 4096 x 11008 take 15 us in clusters and
+// 22 in pairs, 40 x 1024 x 4096 4.9 and 9.0, 64 x 1024 x 2048 5.4 and 5.7, but 64 x 2048 x 1024 6.2 and 4.4, 32 x 4096 x
+// 1024 6.3 and 4.5, 200 x 1024 x 2048 7.8 and 6.1; 64 x 5120 x 4096, more clusters than run at once, 17 and 11. Up to 16
+// tokens few sums are sent, and many rows of w are read faster by more CTAs: 16 x 8192 x 2048 6.7 us and 7.5 (x 1024 6.0
+// and 5.4). Tiles that no CTAs share read w at least as fast as pairs (32 x 20,000 x 1024 6.8 and 7.2).
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   const Args a = common_args(g);
-  if (g.T <= 16 || clusters_fit(g, 16)) return launch<16, false>(g, a, s);
-  if (g.T <= 32 || clusters_fit(g, 32)) return launch<32, false>(g, a, s);
-  if (clusters_fit(g, 64) || g.N <= kRows) return launch<64, false>(g, a, s);
+  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
+  // clusters rather than pairs (of one tile of w half of a pair's rows would be none)
+  const bool pays = (g.T + 7) / 8 * 8LL * g.N <= 72LL * g.K - 20000 || g.N <= kRows;
+  const bool by_itself = split_of(rows, a.pieces, slots, (g.T + 15) / 16 * 16) == 1;
+  const bool few = pays || by_itself || (g.T <= 16 && g.K > 1536);
+  auto fits = [&](int cols) { return (pays || a.pieces == 1) && clusters_fit(g, cols); };
+  if (g.T <= 16 ? few : fits(16)) return launch<16, false>(g, a, s);
+  if (g.T <= 32 ? few : fits(32)) return launch<32, false>(g, a, s);
+  if (g.N <= kRows || fits(64)) return launch<64, false>(g, a, s);
   return launch<kMaxTokens, true>(g, a, s);
 }
 
@@ -988,7 +999,7 @@ cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, 
   Args a = common_args(g);
   a.x16 = x;
   a.x16_stride = x_stride;
-  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * Shape<16, false>::per_sm;
+  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
   const int split = split_of(rows, a.pieces, slots);
   if ((g.T <= 16 && split > 1) || clusters_fit(g, 16))
     return dtype == MOE_BF16 ? launch<16, false, MOE_BF16>(g, a, s) : launch<16, false, MOE_FP16>(g, a, s);
