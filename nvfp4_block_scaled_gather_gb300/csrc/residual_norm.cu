@@ -19,9 +19,9 @@
 //    after row, the next ones on their way while the present ones are worked on;
 //    one copy of the norms' weights waits in shared memory (read from L2 for
 //    every row they would be as many bytes again). The rows come to shared
-//    memory by bulk copies: 16,384 x 4096 with both norms 84 us, 6.4 TB/s (120
-//    with a CTA a row); to 8-bit rows 8192 x 4096 47 us, 5.0 TB/s, short of
-//    issue slots.
+//    memory by bulk copies: 16,384 x 4096 with both norms 85 to 91 us, 5.9 to 6.3
+//    TB/s (120 with a CTA a row); to 8-bit rows 8192 x 4096 44 us, 5.3 TB/s,
+//    short of issue slots.
 //  * The longest, whose weights and rows would not fit shared memory, come to
 //    registers.
 #include <cstdint>
@@ -311,11 +311,25 @@ __device__ __forceinline__ void sync(const Group& g) {
 template <int NV>
 __device__ __forceinline__ float row_sum(const Group& g, const float (&s)[NV], float* sums) {
   const int warps = g.threads >> 5, warp = g.thread >> 5, lane = threadIdx.x & 31, pieces = NV * warps;
+  // NV trees in one: a lane sends half of the sums that it has and goes on with the others (lane l ends with sum l % NV)
+  float part[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const float tree = tree_sum<32>(s[i]);
-    if (lane == 0) sums[i * warps + warp] = tree;
+  for (int i = 0; i < NV; ++i) part[i] = s[i];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int left = NV / (2 * o);  // sums of a lane after this step
+    if (left >= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < left; ++i) {
+        const float keep = up ? part[2 * i + 1] : part[2 * i], send = up ? part[2 * i] : part[2 * i + 1];
+        part[i] = keep + __shfl_xor_sync(~0u, send, o);
+      }
+    } else {
+      part[0] += __shfl_xor_sync(~0u, part[0], o);
+    }
   }
+  if (lane < NV) sums[lane * warps + warp] = part[0];
   sync(g);
   float mine = lane < pieces ? sums[lane] : 0.0f;
   if (pieces > 32 && 32 + lane < pieces) mine += sums[32 + lane];
@@ -437,16 +451,16 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
   const int threads = NV == 4 ? blockDim.x : group_threads;
   const int rows = a.tokens * a.heads, eights = a.dim / 8, bytes = 2 * a.dim;
   const int group = NV == 4 ? 0 : __shfl_sync(~0u, (int)threadIdx.x / threads, 0);
-  const Group mine = {threads, (int)threadIdx.x - group * threads, NV == 4 ? 0 : group + 1};
+  const Group own_group = {threads, (int)threadIdx.x - group * threads, NV == 4 ? 0 : group + 1};
   const int own = group * NV * (threads / 32);  // of sums
   uint64_t(&landed)[kSlots] = all_landed[group];
   const bool has_block = a.block.data != nullptr;
   uint8_t* slots = reinterpret_cast<uint8_t*>(weights + 4 * eights) + group * kSlots * 2 * bytes;
-  auto eighth = [&](int i) { return i * threads + mine.thread; };
+  auto eighth = [&](int i) { return i * threads + own_group.thread; };
   // (rows go over the CTAs first)
   const long long first = blockIdx.x + (long long)group * gridDim.x;
   const long long step = (NV == 4 ? 1LL : (long long)(blockDim.x / threads)) * gridDim.x;
-  if (mine.thread == 0) {
+  if (own_group.thread == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(landed + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -461,7 +475,7 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
     bulk_load(to, place(a.x, t, h, 0), bytes, bar);
     if (has_block) bulk_load(to + bytes, place(a.block, t, h, 0), bytes, bar);
   };
-  if (mine.thread == 0)
+  if (own_group.thread == 0)
     for (int i = 0; i < kSlots; ++i) bring(i, first + i * step);
   for (int d = 4 * threadIdx.x; d < a.dim; d += 4 * (int)blockDim.x) {
     const float4 one = make_float4(1, 1, 1, 1);
@@ -470,9 +484,16 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
     weights[2 * eights + to] = a.pre_weight ? ld_cg(reinterpret_cast<const float4*>(a.pre_weight + d)) : one;
   }
   __syncthreads();
-  const F8 none = {};
   int slot = 0, turn = 0;
   uint32_t parity = 0;
+  // (a thread behind the row's end does the last values' work again, for nobody: it has no part in sums and writes nothing)
+  int e[NV];
+  bool mine[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    mine[i] = eighth(i) < eights;
+    e[i] = mine[i] ? eighth(i) : eights - 1;
+  }
   // the gate, asked for a row ahead (16,384 x 4096, a factor for each element: 104 us, 107 where it was asked for with its
   // own row)
   uint4 g[NV];
@@ -480,8 +501,7 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
     if (!has_block || !a.gate.data || row >= rows) return;
     const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      g[i] = eighth(i) < eights ? load_gate(a.gate, t, h, 8 * eighth(i)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < NV; ++i) g[i] = load_gate(a.gate, t, h, 8 * e[i]);
   };
   ask_gate(first);
   for (long long row = first; row < rows; row += step) {
@@ -496,43 +516,37 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
       if (a.post_norm) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          y[i] = eighth(i) < eights ? unpack8<kType>(b[eighth(i)]) : none;
-          s[i] = squares(y[i]);
+          y[i] = unpack8<kType>(b[e[i]]);
+          s[i] = mine[i] ? squares(y[i]) : 0.0f;
         }
-        r = inverse_rms(row_sum<NV>(mine, s, sums[turn][0] + own), shape);
+        r = inverse_rms(row_sum<NV>(own_group, s, sums[turn][0] + own), shape);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = eighth(i);
-        if (e >= eights) {
-          y[i] = none;
-          continue;
-        }
-        F8 v = a.post_norm ? times(y[i], as_f8(weights[e], weights[e + eights])) : unpack8<kType>(b[e]);
-        y[i] = add_block<kType>(a, g[i], v, r, x[e]);
-        if (a.y.data) *reinterpret_cast<uint4*>(place(a.y, t, h, 8 * e)) = pack8<kType>(y[i]);
+        F8 v = a.post_norm ? times(y[i], as_f8(weights[e[i]], weights[e[i] + eights])) : unpack8<kType>(b[e[i]]);
+        y[i] = add_block<kType>(a, g[i], v, r, x[e[i]]);
+        if (a.y.data && mine[i]) *reinterpret_cast<uint4*>(place(a.y, t, h, 8 * e[i])) = pack8<kType>(y[i]);
       }
       ask_gate(row + step);
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) y[i] = eighth(i) < eights ? unpack8<kType>(x[eighth(i)]) : none;
+      for (int i = 0; i < NV; ++i) y[i] = unpack8<kType>(x[e[i]]);
     }
     const bool more = a.normed.data || a.quantized.codes;
     float r = 0.0f;
     if (more) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) s[i] = squares(y[i]);
-      r = inverse_rms(row_sum<NV>(mine, s, sums[turn][1] + own), shape);  // (everyone has read the slot)
+      for (int i = 0; i < NV; ++i) s[i] = mine[i] ? squares(y[i]) : 0.0f;
+      r = inverse_rms(row_sum<NV>(own_group, s, sums[turn][1] + own), shape);  // (everyone has read the slot)
     } else {
-      sync(mine);
+      sync(own_group);
     }
-    if (mine.thread == 0) bring(slot, row + kSlots * step);
+    if (own_group.thread == 0) bring(slot, row + kSlots * step);
     if (more) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = eighth(i);
-        const F8 w = e < eights ? as_f8(weights[2 * eights + e], weights[3 * eights + e]) : none;
-        write_normed<kType, 16>(a, t, h, 8 * e, e < eights, y[i], r, w);
+        const F8 w = as_f8(weights[2 * eights + e[i]], weights[3 * eights + e[i]]);
+        write_normed<kType, 16>(a, t, h, 8 * e[i], mine[i], y[i], r, w);
       }
     }
     turn ^= 1;
@@ -563,10 +577,12 @@ cudaError_t launch_stream(const moe_residual_norm_t& a, const Shape& shape, cuda
   long long groups = (most_smem - 8 * a.dim) / (4 * kSlots * a.dim);
   groups = groups < kMostThreads<NV> / threads ? groups : kMostThreads<NV> / threads;
   groups = groups < kMostGroups ? groups : kMostGroups;
-  // 16-bit norms of more than 15,360 values at a time come and go more slowly (16,384 x 4096: three groups 84 us, four 95;
-  // 30,000 x 2048: six 78, seven 82, eight 87; 16,384 x 3840: three 83, four 81); 8-bit ones have fewer bytes to write and
-  // more to do (8192 x 4096: three 53, four 49)
-  if (a.normed.data && groups * a.dim > 15360) groups = 15360 / a.dim < 2 ? (groups < 2 ? groups : 2) : 15360 / a.dim;
+  // Beyond what memory keeps up with, more rows at a time make reads and writes get in each other's way: two outputs of 16
+  // bits take 12,288 values at a time (30,000 x 2048: five groups 77 us, six 86, eight 90; 12,000 x 5120: two 80, three 90;
+  // 16,384 x 4096: two 92, three 91, four 97), with a gate, which is more to do, 15,360 (4001 x 5120, a factor for each
+  // token: two 33.7, three 32.1). 8-bit outputs have fewer bytes and more to do (8192 x 4096: three groups 48 us, four 44).
+  const int most = a.gate.data ? 15360 : 12288;
+  if (a.normed.data && groups > 2 && groups * a.dim > most) groups = most / a.dim < 2 ? 2 : most / a.dim;
   groups = groups < (rows + grid - 1) / grid ? groups : (rows + grid - 1) / grid;
   return launch_pdl(residual_norm_stream<kType, NV>, dim3((unsigned)grid), dim3((unsigned)(groups * threads)),
                     (size_t)a.dim * (8 + 4 * kSlots * groups), s, a, shape, threads);
