@@ -230,7 +230,7 @@ __device__ __forceinline__ void write_normed(const moe_residual_norm_t& a, int t
 
 // Rows of at most 8 G values, G threads each, kRows rows of a thread at a time. kBlock: with a block's output.
 template <int kType, int G, int kRows, bool kBlock>
-__global__ void __launch_bounds__(kSmallThreads, kBlock ? 4 : 5)
+__global__ void __launch_bounds__(kSmallThreads, kBlock ? 4 : kRows == 4 ? 3 : 5)
     residual_norm_small(const __grid_constant__ moe_residual_norm_t a, const Shape shape) {
   pdl_wait();
   pdl_trigger();
@@ -557,14 +557,28 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
   }
 }
 
+template <int kType, int G, int kRows, bool kBlock>
+cudaError_t launch_small_by(int per_sm, const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
+  constexpr int per = kSmallThreads / G * kRows;
+  const long long turns = ((long long)a.tokens * a.heads + per - 1) / per, most = (long long)per_sm * num_sms();
+  return launch_pdl(residual_norm_small<kType, G, kRows, kBlock>, dim3((unsigned)(turns < most ? turns : most)),
+                    dim3(kSmallThreads), 0, s, a, shape);
+}
+// A CTA's start and end take as long as several turns of its loop, so few CTAs that stay: with a block one an SM, more for
+// rows that keep each busy for twelve turns (3000 rows of 256: one an SM 5.8 us, two 6.9, three 10.4; 30,000: 23.6, 18.3 and
+// 19.7; 300,000 of 128: 96, 64, 59 and with four 55). Without one, two rows of a thread at a time where all run at once
+// (200 tokens of 40 heads of 128: 3.4 us, four rows 3.6; 64 tokens 1.9 and 2.5), else four and three CTAs an SM (3001 tokens
+// 14.5 us, two rows and five CTAs 16.3).
 template <int kType, int G>
 cudaError_t launch_small(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
+  const long long rows = (long long)a.tokens * a.heads;
   constexpr int per = kSmallThreads / G;
-  const long long rows = (long long)a.tokens * a.heads, ctas = (rows + per - 1) / per;
-  const long long most = (a.block.data ? 4LL : 5LL) * num_sms();
-  const unsigned grid = (unsigned)(ctas < most ? ctas : most);
-  if (a.block.data) return launch_pdl(residual_norm_small<kType, G, 1, true>, dim3(grid), dim3(kSmallThreads), 0, s, a, shape);
-  return launch_pdl(residual_norm_small<kType, G, 2, false>, dim3(grid), dim3(kSmallThreads), 0, s, a, shape);
+  if (a.block.data) {
+    const long long busy = rows / (12LL * per * num_sms());
+    return launch_small_by<kType, G, 1, true>(busy < 1 ? 1 : busy > 4 ? 4 : (int)busy, a, shape, s);
+  }
+  if (rows <= 4LL * per * num_sms()) return launch_small_by<kType, G, 2, false>(2, a, shape, s);
+  return launch_small_by<kType, G, 4, false>(3, a, shape, s);
 }
 
 template <int kType, int NV>

@@ -452,6 +452,25 @@ def test_heads_within_wider_rows(cuda, dtype):
     assert torch.equal(rows[:, 640:], before[:, 640:])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("t,h,d", [(700, 14, 64), (2100, 10, 64), (1001, 12, 72), (811, 9, 128), (2011, 5, 128), (613, 5, 200), (1300, 4, 256)])
+def test_many_heads_within_wider_rows(cuda, t, h, d, dtype):
+    """Two or four rows of a thread at a time; the values behind the heads stay."""
+    rows = normal((t, (h + 2) * d), dtype, t)
+    before = rows.clone()
+    heads = rows.view(t, h + 2, d)[:, :h]
+    w = normal((d,), "fp32", 4)
+    D.moe_residual_norm(heads, normed=heads, pre_weight=w, eps=1e-6)
+    norm_holds(before.view(t, h + 2, d)[:, :h], None, dict(pre_weight=w, eps=1e-6), dtype, None, heads)
+    assert torch.equal(rows[:, h * d:], before[:, h * d:]) and N.check_status() == 0
+
+
+@pytest.mark.parametrize("t,h,d,gate", [(30011, 4, 8, "token"), (60013, 1, 64, "channel"), (9001, 7, 128, "head"), (30011, 1, 136, "element"),
+                                        (40009, 1, 256, "none")])
+def test_the_residual_step_of_many_short_rows(cuda, t, h, d, gate):
+    test_the_residual_step(cuda, t, h, d, "bf16", gate, True)
+
+
 def test_rows_held_along_and_gates_held_along(cuda):
     """One row for all tokens as x (stride 0), a gate of one number for all."""
     x = normal((1, 1, 256), "bf16", 1).expand(5, 3, 256)
