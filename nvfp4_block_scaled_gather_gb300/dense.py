@@ -19,8 +19,7 @@ from . import _native
 from .attention import BF16, FP16, _scratch, _stream
 from ._native import _check
 
-c_int, c_size_t, c_void_p, c_longlong, c_float = (ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong,
-                                                  ctypes.c_float)
+c_int, c_size_t, c_void_p, c_longlong = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong
 
 FP32 = 2  # MOE_FP32
 
@@ -30,12 +29,7 @@ class Fp8RowsStruct(ctypes.Structure):
     _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("row_stride", c_longlong), ("scale_stride", c_longlong)]
 
 
-class Gate(ctypes.Structure):
-    """moe_gate_t"""
-    _fields_ = [("data", c_void_p), ("token_stride", c_longlong), ("head_stride", c_longlong), ("dim_stride", c_int)]
-
-
-# the structs as bytes, at a fifth of the time that the classes take
+# the structs as bytes, at a fifth of the time that classes take
 _rows_bytes = struct.Struct("PPqq").pack
 # moe_residual_norm_t: tokens, heads, dim, dtype; x; block; gate (padded to 8 bytes); residual_scale, eps, post_norm,
 # padding, post_weight, pre_weight; y; normed; quantized
