@@ -69,12 +69,6 @@ _OUT_CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
 _MOST = 2 ** 31 - 1  # that an int of the library holds (ctypes would pass the low 32 bits on)
 
 
-def _call(name, fn, *args):
-    status = fn(*args)
-    if status:
-        _check(name, status)
-
-
 class Fp8Rows:
     """8-bit rows (moe_fp8_rows_t) whose memory is the caller's: codes [rows, k], float8_e4m3fn or uint8, and scales
     [rows, at least 4 * ceil(k / 512)] uint8 (e8m0: 2 ** (byte - 127)), one for each 128 values; both contiguous along
@@ -138,10 +132,14 @@ def _matrix(name, t, dtype, device: int):
 
 
 def _input16(name, t, device: int):
-    code = _CODES.get(t.dtype)
+    dtype, shape = t.dtype, t.shape
+    code = _CODES.get(dtype)
     if code is None:
-        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    p, rs, rows, k = _matrix(name, t, t.dtype, device)
+        raise ValueError(f"{name} must be bfloat16 or float16, got {dtype}")
+    # (rows without gaps are the usual ones; the library minds their length)
+    if len(shape) == 2 and 0 < shape[0] <= _MOST and shape[1] <= _MOST and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr(), shape[1] if shape[0] > 1 else 0, shape[0], shape[1], code
+    p, rs, rows, k = _matrix(name, t, dtype, device)
     if rs % 8:
         raise ValueError(f"{name}: the row stride must be a multiple of 8 elements, got {t.stride()}")
     return p, rs, rows, k, code
@@ -156,10 +154,13 @@ def _rows_of(name, r, device: int):
 
 
 def _output(y, rows, n, device: int):
-    code = _OUT_CODES.get(y.dtype)
+    dtype = y.dtype
+    code = _OUT_CODES.get(dtype)
     if code is None:
-        raise ValueError(f"y must be bfloat16, float16 or float32, got {y.dtype}")
-    p, rs, rows_y, n_y = _matrix("y", y, y.dtype, device)
+        raise ValueError(f"y must be bfloat16, float16 or float32, got {dtype}")
+    if y.shape == (rows, n) and y.is_contiguous() and y.get_device() == device:
+        return y.data_ptr(), n, code
+    p, rs, rows_y, n_y = _matrix("y", y, dtype, device)
     if rows_y != rows or n_y != n:
         raise ValueError(f"y must be [{rows}, {n}], got {tuple(y.shape)}")
     return p, rs, code
@@ -171,8 +172,9 @@ def moe_fp8_quantize_rows(x, out: Fp8Rows, stream=None):
     p, rs, rows, k, code = _input16("x", x, dev)
     if (rows, k) != (out.n, out.k):
         raise ValueError(f"out must have {rows} rows of {k}, got {out.n} of {out.k}")
-    _call("moe_fp8_quantize_rows", load().moe_fp8_quantize_rows, p, rs, rows, k, code, _rows_of("out", out, dev),
-          _stream(stream, dev))
+    status = (_LIB or load()).moe_fp8_quantize_rows(p, rs, rows, k, code, out.bytes, _stream(stream, dev))
+    if status:
+        _check("moe_fp8_quantize_rows", status)
 
 
 def moe_fp8_gemm(x: Fp8Rows, w: Fp8Rows, y, stream=None):
@@ -181,8 +183,9 @@ def moe_fp8_gemm(x: Fp8Rows, w: Fp8Rows, y, stream=None):
     if x.k != w.k:
         raise ValueError(f"x and w must have rows of one length, got {x.k} and {w.k}")
     p, rs, code = _output(y, x.n, w.n, dev)
-    _call("moe_fp8_gemm", load().moe_fp8_gemm, _rows_of("x", x, dev), x.n, _rows_of("w", w, dev), w.n, w.k, p, rs, code,
-          _stream(stream, dev))
+    status = (_LIB or load()).moe_fp8_gemm(_rows_of("x", x, dev), x.n, w.bytes, w.n, w.k, p, rs, code, _stream(stream, dev))
+    if status:
+        _check("moe_fp8_gemm", status)
 
 
 def linear_workspace(tokens: int, k: int, device="cuda"):
@@ -201,8 +204,11 @@ def moe_fp8_linear(x, w: Fp8Rows, y, workspace, stream=None):
     if k != w.k:
         raise ValueError(f"x and w must have rows of one length, got {k} and {w.k}")
     py, rsy, code_y = _output(y, rows, w.n, dev)
-    _call("moe_fp8_linear", load().moe_fp8_linear, p, rs, rows, k, code, w.bytes, w.n, py, rsy, code_y,
-          *_scratch(workspace, dev), _stream(stream, dev))
+    ws, ws_bytes = _scratch(workspace, dev)
+    status = (_LIB or load()).moe_fp8_linear(p, rs, rows, k, code, w.bytes, w.n, py, rsy, code_y, ws, ws_bytes,
+                                             _stream(stream, dev))
+    if status:
+        _check("moe_fp8_linear", status)
 
 
 def _part(name, t, dtype, tokens, heads, dim, device: int):
@@ -301,7 +307,8 @@ def moe_residual_norm(x, block=None, *, y=None, normed=None, quantized: Fp8Rows 
         rows = _rows_of("quantized", quantized, dev)
         if quantized.n != tokens or quantized.k != dim or heads != 1:
             raise ValueError(f"quantized must have {tokens} rows of {dim} (of one head), got {quantized.n} of {quantized.k}")
-    args = _norm_bytes(tokens, heads, dim, code, *part("x", x), *part("block", block),
+    px = (x.data_ptr(), *whole) if x.is_contiguous() else _part("x", x, dtype, tokens, heads, dim, dev)
+    args = _norm_bytes(tokens, heads, dim, code, *px, *part("block", block),
                        *(_NO_GATE if gate is None else _gate(gate, dtype, (tokens, heads, dim), dev)), 0,
                        residual_scale, eps, 1 if post_norm else 0, 0,
                        0 if post_weight is None else _norm_weight("post_weight", post_weight, dim, dev),
