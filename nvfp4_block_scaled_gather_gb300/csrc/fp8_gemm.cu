@@ -34,7 +34,7 @@
 // for each 32 values 216 to 220. Of decode batches over many rows of w the reads
 // of w (32 tokens x 100,003 x 4096: 67 us, 6.3 TB/s). Of small ones the chain
 // from the launch over the first tiles, the MMAs and the joined sums to the
-// store: 3.4 us for 256 x 1024, 6.6 for 5120 x 4096, one token.
+// store: 3.3 us for 256 x 1024, 6.6 for 5120 x 4096, one token.
 #include <atomic>
 #include <cstdint>
 
@@ -60,7 +60,7 @@ constexpr int kScaleSlots = 2;     // words of scales on their way
 constexpr int kStageAtoms = 1024 + kScaleSlots * 1536;  // an atom for each stage, of tokens that are quantized here
 constexpr int kHeader = 7168;
 static_assert(kStageAtoms + kMaxStages * 512 <= kHeader, "");
-constexpr int kMostSplit = 8;      // CTAs of a cluster
+constexpr int kMostSplit = 8;      // CTAs of a cluster, and pieces
 constexpr int kMaxTokens = 240;    // of a tile: two accumulators and the scales fill tensor memory
 
 // kCols: tokens of a tile at most. kPair: two CTAs share a tile of 256 rows of
@@ -238,10 +238,11 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// A value to another CTA's shared memory, whose barrier counts its bytes. (A warp's values go next to each other: 16
-// bytes a lane, each lane's in its own row, took 17 us instead of 10 for 32 tokens.)
-__device__ __forceinline__ void send(uint32_t addr, uint32_t v, uint32_t bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+// Four values to another CTA's shared memory, whose barrier counts their bytes. (A warp's go next to each other: with each
+// lane's in a row of its own 32 tokens took 17 us instead of 10.)
+__device__ __forceinline__ void send(uint32_t addr, const uint32_t* v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
                : "memory");
 }
 
@@ -339,6 +340,19 @@ __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
         (uint16_t)(a.y_dtype == MOE_BF16 ? pack16x2<MOE_BF16>(v, 0.0f) : pack16x2<MOE_FP16>(v, 0.0f));
 }
 
+// The pieces' sums at `p`, `apart` from each other, in ascending order (all are asked for first).
+__device__ __forceinline__ float sum_pieces(const float* p, int apart, int pieces) {
+  float part[kMostSplit];
+#pragma unroll
+  for (int i = 0; i < kMostSplit; ++i)
+    if (i < pieces) part[i] = p[i * apart];
+  float v = part[0];
+#pragma unroll
+  for (int i = 1; i < kMostSplit; ++i)
+    if (i < pieces) v += part[i];
+  return v;
+}
+
 // One row of w's results for `there` tokens, a warp's lanes next to each other.
 template <int kAcc, typename To, typename Round>
 __device__ __forceinline__ void store_column(To* y, long long stride, const float (&sum)[kAcc], int there, Round round) {
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 516);
   const uint32_t s_scales = base + 1024, s_w = base + kHeader, s_x = s_w + (uint32_t)a.stages * S::deep * kWBytes;
   const uint32_t x_bytes = (uint32_t)(a.tn / S::ctas) * kBlockK;  // a block's tokens in this CTA
-  // the sums that this CTA's rows get from its cluster: [pieces][tokens][128 / split]
+  // the sums that this CTA's rows get from its cluster: [pieces][tokens / 4][128 / split][4]
   const uint32_t recv_off = kHeader + (uint32_t)a.stages * S::deep * (kWBytes + x_bytes);
   float* recv = reinterpret_cast<float*>(smem + recv_off);
 
@@ -417,7 +431,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
     mbar_init(join_bar, 1);
     if (!kPair && a.split > 1) {
       const int t0 = place_of(blockIdx.x / a.split, a).t * a.tn;
-      mbar_expect_tx(join_bar, 4 * a.pieces * (kRows / a.split) * ((min(a.tn, a.T - t0) + 7) / 8 * 8));
+      mbar_expect_tx(join_bar, 4 * a.pieces * (kRows / a.split) * ((min(a.tn, a.T - t0) + 3) / 4 * 4));
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -741,7 +755,7 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
     for (int i = first; i < a.tiles && ok; i += step) {
       const Place at = place_of(i, a);
       const int n = at.n * S::tile_rows + half * kRows + row, t0 = at.t * a.tn + c0;
-      const int sent = (min(a.tn, a.T - t0) + 7) / 8 * 8;  // tokens whose sums go to peers
+      const int sent = (min(a.tn, a.T - t0) + 3) / 4 * 4;  // tokens whose sums go to peers
       float sum[S::acc];
 #pragma unroll
       for (int c = 0; c < S::acc; ++c) sum[c] = 0.0f;
@@ -766,13 +780,13 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
           }
         } else {
           const uint32_t cta = row / slice;
-          const uint32_t to = peer(base + recv_off, cta) + 4u * (uint32_t)(p * a.tn * slice + row % slice);
+          const uint32_t to = peer(base + recv_off, cta) + 4u * (uint32_t)(p * a.tn * slice) + 16u * (row % slice);
           const uint32_t bar = peer(join_bar, cta);
           for (int c = 0; c < sent; c += 8) {
             tc_ld8(from + c, v);
             tc_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) send(to + 4u * (uint32_t)((c + j) * slice), v[j], bar);
+            send(to + 4u * (uint32_t)(c * slice), v, bar);
+            if (c + 4 < sent) send(to + 4u * (uint32_t)((c + 4) * slice), v + 4, bar);
           }
         }
         tc_fence_before();
@@ -788,13 +802,27 @@ __global__ void __launch_bounds__(Shape<kCols, kPair>::threads, Shape<kCols, kPa
         ok = wait_warp(join_bar, 0, ctl);
         if (!ok) break;
         const int n0 = n - row + rank * slice, tokens = min(a.tn, a.T - t0), shift = 31 - __clz(slice);
-        for (int j = (int)threadIdx.x - 128; j < tokens << shift; j += 128) {
-          const int r = j & (slice - 1), t = j >> shift;
+        const int worker = (int)threadIdx.x - 128;
+        if (sent << shift <= 128) {  // one each
+          const int j = worker, r = (j >> 2) & (slice - 1), t = (j & 3) + (j >> (shift + 2) << 2);
+          if (n0 + r < a.N && t < tokens) store_y(a, t0 + t, n0 + r, sum_pieces(recv + j, a.tn * slice, a.pieces));
+          continue;
+        }
+        // four tokens at a time (16 x 6144 x 4096 7.6 us, 8.2 with one; 64 x 4096 x 4096 8.2 and 9.5; but 8 x 1024 x 1024 3.6
+        // and 3.4)
+        for (int j = worker; j < sent / 4 << shift; j += 128) {
+          const int r = j & (slice - 1), t = 4 * (j >> shift);
           if (n0 + r >= a.N) continue;
-          const float* piece = recv + j;
-          float v = piece[0];
-          for (int p = 1; p < a.pieces; ++p) v += piece[p * a.tn * slice];
-          store_y(a, t0 + t, n0 + r, v);
+          const float4* piece = reinterpret_cast<const float4*>(recv) + j;
+          float4 v = piece[0];
+          for (int p = 1; p < a.pieces; ++p) {
+            const float4 more = piece[p * (a.tn / 4) * slice];
+            v = make_float4(v.x + more.x, v.y + more.y, v.z + more.z, v.w + more.w);
+          }
+          store_y(a, t0 + t, n0 + r, v.x);
+          if (t + 1 < tokens) store_y(a, t0 + t + 1, n0 + r, v.y);
+          if (t + 2 < tokens) store_y(a, t0 + t + 2, n0 + r, v.z);
+          if (t + 3 < tokens) store_y(a, t0 + t + 3, n0 + r, v.w);
         }
         continue;
       }
@@ -971,19 +999,19 @@ bool clusters_fit(const Fp8Gemm& g, int cols) {
 }  // namespace
 
 // The narrowest tiles that hold all tokens of a decode batch (every row of w is read once), or of which a cluster each
-// runs at one time; else pairs. A pair's time goes with K (from 3.5 us, and 1.3 for each 1024 values), a cluster's with
-// the sums that it sends, T N (from 3.5 us, and 1.8 for each 100,000): 64 tokens x 4096 x 11008 take 15 us in clusters and
-// 22 in pairs, 40 x 1024 x 4096 4.9 and 9.0, 64 x 1024 x 2048 5.4 and 5.7, but 64 x 2048 x 1024 6.2 and 4.4, 32 x 4096 x
-// 1024 6.3 and 4.5, 200 x 1024 x 2048 7.8 and 6.1; 64 x 5120 x 4096, more clusters than run at once, 17 and 11. Up to 16
-// tokens few sums are sent, and many rows of w are read faster by more CTAs: 16 x 8192 x 2048 6.7 us and 7.5 (x 1024 6.0
-// and 5.4). Tiles that no CTAs share read w at least as fast as pairs (32 x 20,000 x 1024 6.8 and 7.2).
+// runs at one time; else pairs. A pair's time goes with K (from 3 us, and 1.3 for each 1024 values), a cluster's with the
+// sums that it sends, T N: 64 tokens x 4096 x 11008 take 13.4 us in clusters and 21.8 in pairs, 40 x 1024 x 4096 4.9 and 8.9,
+// 64 x 1024 x 2048 5.3 and 5.7, 64 x 512 x 1024 3.9 and 4.3, but 64 x 2048 x 1024 5.8 and 4.4, 32 x 4096 x 1024 5.8 and 4.5,
+// 200 x 1024 x 1536 6.5 and 5.4. Many rows of w for few tokens are read faster by more CTAs (16 x 8192 x 2048 6.2 us and 7.5,
+// 32 x 8192 x 2048 6.8 and 7.4; but 16 x 4096 x 1536 5.8 and 5.5). Tiles that no CTAs share read w at least as fast as pairs
+// (32 x 20,000 x 1024 6.8 and 7.2).
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   const Args a = common_args(g);
   const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
   // clusters rather than pairs (of one tile of w half of a pair's rows would be none)
-  const bool pays = (g.T + 7) / 8 * 8LL * g.N <= 72LL * g.K - 20000 || g.N <= kRows;
+  const bool pays = (g.T + 7) / 8 * 8LL * g.N <= (long long)g.K * g.K / 36 + 8000 || g.N <= kRows;
   const bool by_itself = split_of(rows, a.pieces, slots, (g.T + 15) / 16 * 16) == 1;
-  const bool few = pays || by_itself || (g.T <= 16 && g.K > 1536);
+  const bool few = pays || by_itself || g.K > 1536;
   auto fits = [&](int cols) { return (pays || a.pieces == 1) && clusters_fit(g, cols); };
   if (g.T <= 16 ? few : fits(16)) return launch<16, false>(g, a, s);
   if (g.T <= 32 ? few : fits(32)) return launch<32, false>(g, a, s);
