@@ -163,10 +163,13 @@ __device__ __forceinline__ F8 load_weights(const float* w, int d) {
   return as_f8(ld_cg(reinterpret_cast<const float4*>(w + d)), ld_cg(reinterpret_cast<const float4*>(w + d + 4)));
 }
 
-// x + residual_scale gate b r (b normed already but for its r).
+// A block's values times one over their root mean square, then times the norm's weights. (In this order: with the weights, or
+// a gate, first a product may pass fp32's largest value, which a factor of 0 makes NaN.)
+__device__ __forceinline__ F8 norm_block(const F8& b, float r, const F8& w) { return times(times(b, pair_of(r, r)), w); }
+// x + residual_scale gate b.
 template <int kType>
-__device__ __forceinline__ F8 add_block(const moe_residual_norm_t& a, const uint4& gate, F8 b, float r, const uint4& x) {
-  float by = a.residual_scale * r;
+__device__ __forceinline__ F8 add_block(const moe_residual_norm_t& a, const uint4& gate, F8 b, const uint4& x) {
+  float by = a.residual_scale;
   if (a.gate.data) {
     if (a.gate.dim_stride) b = times(b, unpack8<kType>(gate));
     else by *= unpack2<kType>(gate.x).x;
@@ -279,12 +282,8 @@ __global__ void __launch_bounds__(kSmallThreads, kBlock ? 4 : kRows == 4 ? 3 : 5
       F8 y;
       if constexpr (kBlock) {
         F8 v = unpack8<kType>(b[k]);
-        float r = 1.0f;
-        if (a.post_norm) {
-          r = inverse_rms(tree_sum<G>(squares(v)), shape);
-          v = times(v, post);
-        }
-        y = add_block<kType>(a, g[k], v, r, x[k]);
+        if (a.post_norm) v = norm_block(v, inverse_rms(tree_sum<G>(squares(v)), shape), post);
+        y = add_block<kType>(a, g[k], v, x[k]);
         if (mine[k] && a.y.data) *reinterpret_cast<uint4*>(place(a.y, t[k], h[k], d)) = pack8<kType>(y);
       } else {
         y = unpack8<kType>(x[k]);
@@ -409,8 +408,8 @@ __global__ void __launch_bounds__(kStay ? 512 : 1024)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         F8 v = unpack8<kType>(b[i]);
-        if (a.post_norm) v = times(v, held(post, i, 0));
-        y[i] = add_block<kType>(a, g[i], v, r, x[i]);
+        if (a.post_norm) v = norm_block(v, r, held(post, i, 0));
+        y[i] = add_block<kType>(a, g[i], v, x[i]);
         if (a.y.data && at(i) < a.dim) *reinterpret_cast<uint4*>(place(a.y, t, h, at(i))) = pack8<kType>(y[i]);
       }
     } else {
@@ -523,8 +522,8 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        F8 v = a.post_norm ? times(y[i], as_f8(weights[e[i]], weights[e[i] + eights])) : unpack8<kType>(b[e[i]]);
-        y[i] = add_block<kType>(a, g[i], v, r, x[e[i]]);
+        const F8 v = a.post_norm ? norm_block(y[i], r, as_f8(weights[e[i]], weights[e[i] + eights])) : unpack8<kType>(b[e[i]]);
+        y[i] = add_block<kType>(a, g[i], v, x[e[i]]);
         if (a.y.data && mine[i]) *reinterpret_cast<uint4*>(place(a.y, t, h, 8 * e[i])) = pack8<kType>(y[i]);
       }
       ask_gate(row + step);
