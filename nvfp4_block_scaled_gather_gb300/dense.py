@@ -72,7 +72,8 @@ _MOST = 2 ** 31 - 1  # that an int of the library holds (ctypes would pass the l
 class Fp8Rows:
     """8-bit rows (moe_fp8_rows_t) whose memory is the caller's: codes [rows, k], float8_e4m3fn or uint8, and scales
     [rows, at least 4 * ceil(k / 512)] uint8 (e8m0: 2 ** (byte - 127)), one for each 128 values; both contiguous along
-    their rows. `rows(n)` is a handle over the first n."""
+    their rows. `rows(n)` is a handle over the first n. Values may be written in place at any time; a handle whose tensors
+    have moved, or are others, since it was made is refused: make a new one."""
 
     def __init__(self, codes, scales):
         if codes.dim() != 2 or codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or not codes.is_cuda:
@@ -92,7 +93,10 @@ class Fp8Rows:
             raise ValueError(f"scales' rows must be contiguous, apart, and a multiple of 4 bytes from each other, got "
                              f"strides {scales.stride()}")
         self.codes, self.scales, self.n, self.k, self.device = codes, scales, rows, k, codes.get_device()
-        self.bytes = _rows_bytes(codes.data_ptr(), scales.data_ptr(), codes.stride(0) if rows > 1 else 0,
+        # (held here too: memory at an address that is still the tensors' is still theirs, whatever became of its shape)
+        self.held = codes.detach(), scales.detach()
+        self.at = codes.data_ptr(), scales.data_ptr()
+        self.bytes = _rows_bytes(*self.at, codes.stride(0) if rows > 1 else 0,
                                  scales.stride(0) if rows > 1 else 0)
 
     @classmethod
@@ -150,6 +154,8 @@ def _rows_of(name, r, device: int):
         raise ValueError(f"{name} must be Fp8Rows")
     if r.device != device:
         raise ValueError(f"{name} must be on cuda:{device}, got {r.codes.device}")
+    if (r.codes.data_ptr(), r.scales.data_ptr()) != r.at:
+        raise ValueError(f"{name}: its tensors are not where they were when the handle was made: make a new one")
     return r.bytes
 
 
@@ -172,7 +178,7 @@ def moe_fp8_quantize_rows(x, out: Fp8Rows, stream=None):
     p, rs, rows, k, code = _input16("x", x, dev)
     if (rows, k) != (out.n, out.k):
         raise ValueError(f"out must have {rows} rows of {k}, got {out.n} of {out.k}")
-    status = (_LIB or load()).moe_fp8_quantize_rows(p, rs, rows, k, code, out.bytes, _stream(stream, dev))
+    status = (_LIB or load()).moe_fp8_quantize_rows(p, rs, rows, k, code, _rows_of("out", out, dev), _stream(stream, dev))
     if status:
         _check("moe_fp8_quantize_rows", status)
 
@@ -183,7 +189,8 @@ def moe_fp8_gemm(x: Fp8Rows, w: Fp8Rows, y, stream=None):
     if x.k != w.k:
         raise ValueError(f"x and w must have rows of one length, got {x.k} and {w.k}")
     p, rs, code = _output(y, x.n, w.n, dev)
-    status = (_LIB or load()).moe_fp8_gemm(_rows_of("x", x, dev), x.n, w.bytes, w.n, w.k, p, rs, code, _stream(stream, dev))
+    status = (_LIB or load()).moe_fp8_gemm(_rows_of("x", x, dev), x.n, _rows_of("w", w, dev), w.n, w.k, p, rs, code,
+                                           _stream(stream, dev))
     if status:
         _check("moe_fp8_gemm", status)
 
@@ -205,8 +212,8 @@ def moe_fp8_linear(x, w: Fp8Rows, y, workspace, stream=None):
         raise ValueError(f"x and w must have rows of one length, got {k} and {w.k}")
     py, rsy, code_y = _output(y, rows, w.n, dev)
     ws, ws_bytes = _scratch(workspace, dev)
-    status = (_LIB or load()).moe_fp8_linear(p, rs, rows, k, code, w.bytes, w.n, py, rsy, code_y, ws, ws_bytes,
-                                             _stream(stream, dev))
+    status = (_LIB or load()).moe_fp8_linear(p, rs, rows, k, code, _rows_of("w", w, dev), w.n, py, rsy, code_y, ws,
+                                             ws_bytes, _stream(stream, dev))
     if status:
         _check("moe_fp8_linear", status)
 
