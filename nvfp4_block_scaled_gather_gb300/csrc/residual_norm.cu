@@ -34,6 +34,7 @@
 #include "ldcg.cuh"
 #include "mbar.cuh"
 #include "pdl.cuh"
+#include "row_slots.cuh"
 
 namespace moe {
 namespace {
@@ -120,16 +121,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// Until the row is there. Bounded: after that the call is reported as failed.
-__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity, int* status) {
-  if (mbar_try_wait(bar, parity)) return;
+// Until the row is there. Bounded: false, and the call is reported as failed, after that.
+__device__ __forceinline__ bool wait_landed(uint32_t bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (clock64() - t0 > kWaitCycles) {
       atomicExch(status, (int)MOE_ERR_TIMEOUT);
-      return;
+      return false;
     }
   }
+  return true;
 }
 template <int kWidth>
 __device__ __forceinline__ float tree_sum(float s) {
@@ -447,12 +449,14 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
   extern __shared__ float4 weights[];  // post (each eight values' first four, then their others), pre, then the slots
   __shared__ float sums[2][2][NV * kMostThreads<NV> / 32];
   __shared__ uint64_t all_landed[kMostGroups][kSlots];
+  __shared__ int all_gave_up[kMostGroups][2];  // a wait of this turn's row
   const int threads = NV == 4 ? blockDim.x : group_threads;
   const int rows = a.tokens * a.heads, eights = a.dim / 8, bytes = 2 * a.dim;
   const int group = NV == 4 ? 0 : __shfl_sync(~0u, (int)threadIdx.x / threads, 0);
   const Group own_group = {threads, (int)threadIdx.x - group * threads, NV == 4 ? 0 : group + 1};
   const int own = group * NV * (threads / 32);  // of sums
   uint64_t(&landed)[kSlots] = all_landed[group];
+  volatile int* gave_up = all_gave_up[group];
   const bool has_block = a.block.data != nullptr;
   uint8_t* slots = reinterpret_cast<uint8_t*>(weights + 4 * eights) + group * kSlots * 2 * bytes;
   auto eighth = [&](int i) { return i * threads + own_group.thread; };
@@ -461,21 +465,21 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
   const long long step = (NV == 4 ? 1LL : (long long)(blockDim.x / threads)) * gridDim.x;
   if (own_group.thread == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(landed + i), 1);
+    gave_up[0] = gave_up[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   pdl_wait();
   pdl_trigger();
   auto bring = [&](int slot, long long row) {  // by one thread
-    if (row >= rows) return;
     const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
     const uint32_t bar = smem_u32(landed + slot), to = smem_u32(slots) + (uint32_t)(slot * 2 * bytes);
     mbar_expect_tx(bar, has_block ? 2 * bytes : bytes);
     bulk_load(to, place(a.x, t, h, 0), bytes, bar);
     if (has_block) bulk_load(to + bytes, place(a.block, t, h, 0), bytes, bar);
   };
-  if (own_group.thread == 0)
-    for (int i = 0; i < kSlots; ++i) bring(i, first + i * step);
+  RowSlots<kSlots> on_way(step, rows);
+  if (own_group.thread == 0) on_way.start(first, bring);
   for (int d = 4 * threadIdx.x; d < a.dim; d += 4 * (int)blockDim.x) {
     const float4 one = make_float4(1, 1, 1, 1);
     const int to = d / 8 + (d & 4 ? eights : 0);
@@ -483,8 +487,7 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
     weights[2 * eights + to] = a.pre_weight ? ld_cg(reinterpret_cast<const float4*>(a.pre_weight + d)) : one;
   }
   __syncthreads();
-  int slot = 0, turn = 0;
-  uint32_t parity = 0;
+  int turn = 0;
   // (a thread behind the row's end does the last values' work again, for nobody: it has no part in sums and writes nothing)
   int e[NV];
   bool mine[NV];
@@ -505,8 +508,8 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
   ask_gate(first);
   for (long long row = first; row < rows; row += step) {
     const int t = token_of((int)row, a.heads, shape), h = (int)row - t * a.heads;
-    wait_landed(smem_u32(landed + slot), parity, shape.status);
-    const uint4* x = reinterpret_cast<const uint4*>(slots + slot * 2 * bytes);
+    if (!wait_landed(smem_u32(landed + on_way.slot), on_way.parity, shape.status)) gave_up[turn] = 1;
+    const uint4* x = reinterpret_cast<const uint4*>(slots + on_way.slot * 2 * bytes);
     const uint4* b = x + eights;
     F8 y[NV];
     float s[NV];
@@ -540,7 +543,14 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
     } else {
       sync(own_group);
     }
-    if (own_group.thread == 0) bring(slot, row + kSlots * step);
+    // A group in which a wait gave up ends here, all of its threads alike (the next row's flag is the other one): nothing
+    // more is asked for, and what is on its way is waited for.
+    if (gave_up[turn]) {
+      if (own_group.thread == 0)
+        on_way.leave(row, [&](int slot, uint32_t parity) { wait_landed(smem_u32(landed + slot), parity, shape.status); });
+      break;
+    }
+    if (own_group.thread == 0) on_way.again(row, bring);
     if (more) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -549,10 +559,7 @@ __global__ void __launch_bounds__(kMostThreads<NV>, 1)
       }
     }
     turn ^= 1;
-    if (++slot == kSlots) {
-      slot = 0;
-      parity ^= 1u;
-    }
+    on_way.next();
   }
 }
 
