@@ -149,9 +149,14 @@ def _input16(name, t, device: int):
     return p, rs, rows, k, code
 
 
-def _rows_of(name, r, device: int):
+def _handle(name, r) -> int:
+    """The device of a handle's rows."""
     if not isinstance(r, Fp8Rows):
-        raise ValueError(f"{name} must be Fp8Rows")
+        raise ValueError(f"{name} must be Fp8Rows, got {type(r).__name__}")
+    return r.device
+
+
+def _rows_of(name, r, device: int):
     if r.device != device:
         raise ValueError(f"{name} must be on cuda:{device}, got {r.codes.device}")
     if (r.codes.data_ptr(), r.scales.data_ptr()) != r.at:
@@ -174,7 +179,7 @@ def _output(y, rows, n, device: int):
 
 def moe_fp8_quantize_rows(x, out: Fp8Rows, stream=None):
     """x [rows, k], bfloat16 or float16, as 8-bit rows."""
-    dev = out.device
+    dev = _handle("out", out)
     p, rs, rows, k, code = _input16("x", x, dev)
     if (rows, k) != (out.n, out.k):
         raise ValueError(f"out must have {rows} rows of {k}, got {out.n} of {out.k}")
@@ -185,7 +190,8 @@ def moe_fp8_quantize_rows(x, out: Fp8Rows, stream=None):
 
 def moe_fp8_gemm(x: Fp8Rows, w: Fp8Rows, y, stream=None):
     """y [x's rows, w's rows] = x w^T over dequantized values, bfloat16, float16 or float32."""
-    dev = w.device
+    dev = _handle("w", w)
+    _handle("x", x)
     if x.k != w.k:
         raise ValueError(f"x and w must have rows of one length, got {x.k} and {w.k}")
     p, rs, code = _output(y, x.n, w.n, dev)
@@ -206,7 +212,7 @@ def linear_workspace(tokens: int, k: int, device="cuda"):
 def moe_fp8_linear(x, w: Fp8Rows, y, workspace, stream=None):
     """y = x w^T with x [rows, k], bfloat16 or float16, quantized on the way: moe_fp8_quantize_rows, then
     moe_fp8_gemm."""
-    dev = w.device
+    dev = _handle("w", w)
     p, rs, rows, k, code = _input16("x", x, dev)
     if k != w.k:
         raise ValueError(f"x and w must have rows of one length, got {k} and {w.k}")
@@ -311,6 +317,7 @@ def moe_residual_norm(x, block=None, *, y=None, normed=None, quantized: Fp8Rows 
 
     rows = _NO_ROWS
     if quantized is not None:
+        _handle("quantized", quantized)
         rows = _rows_of("quantized", quantized, dev)
         if quantized.n != tokens or quantized.k != dim or heads != 1:
             raise ValueError(f"quantized must have {tokens} rows of {dim} (of one head), got {quantized.n} of {quantized.k}")

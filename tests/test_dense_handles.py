@@ -99,3 +99,11 @@ def test_memory_that_a_handle_was_made_of_stays(lib):
     r, storage = D.Fp8Rows(codes, zeros(6, 4)), codes.untyped_storage()._cdata
     codes.data = zeros(6, 64)
     assert any(t.untyped_storage()._cdata == storage for t in r.held)
+
+
+@pytest.mark.parametrize("what", [torch.zeros((6, 64), dtype=torch.uint8), "rows"])
+def test_other_things_than_handles_are_refused(lib, what):
+    for call in calls_with(what):
+        with pytest.raises(ValueError, match="must be Fp8Rows"):
+            call()
+    assert not lib.calls
