@@ -105,6 +105,8 @@ class Fp8Rows:
                    torch.empty((rows, 4 * -(-k // 512)), dtype=torch.uint8, device=device))
 
     def rows(self, n):
+        if not 0 <= n <= self.n:
+            raise ValueError(f"there are {self.n} rows, not {n}")
         return self if n == self.n else Fp8Rows(self.codes[:n], self.scales[:n])
 
     def dequantized(self):

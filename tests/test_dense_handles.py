@@ -107,3 +107,14 @@ def test_other_things_than_handles_are_refused(lib, what):
         with pytest.raises(ValueError, match="must be Fp8Rows"):
             call()
     assert not lib.calls
+
+
+@pytest.mark.parametrize("n", [-1, 7, 100])
+def test_a_handle_over_more_rows_than_there_are(n):
+    with pytest.raises(ValueError, match="6 rows"):
+        handle().rows(n)
+
+
+def test_a_handle_over_the_first_rows():
+    r = handle()
+    assert r.rows(6) is r and r.rows(2).n == 2 and r.rows(0).n == 0 and r.rows(2).at == r.at
