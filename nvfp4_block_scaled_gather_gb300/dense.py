@@ -205,7 +205,7 @@ def moe_fp8_gemm(x: Fp8Rows, w: Fp8Rows, y, stream=None):
 
 def linear_workspace(tokens: int, k: int, device="cuda"):
     """The scratch of moe_fp8_linear for calls of up to `tokens` rows of k."""
-    size = load().moe_fp8_linear_workspace_size(tokens, k)
+    size = load().moe_fp8_linear_workspace_size(tokens, k) if 0 <= tokens <= _MOST and 0 <= k <= _MOST else 0
     if size == 0:
         raise ValueError(f"no product of {tokens} rows of {k}: k must be a positive multiple of 16, both within limits")
     return torch.empty(size, dtype=torch.uint8, device=device)

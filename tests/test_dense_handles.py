@@ -118,3 +118,14 @@ def test_a_handle_over_more_rows_than_there_are(n):
 def test_a_handle_over_the_first_rows():
     r = handle()
     assert r.rows(6) is r and r.rows(2).n == 2 and r.rows(0).n == 0 and r.rows(2).at == r.at
+
+
+@pytest.mark.parametrize("tokens,k", [(2 ** 32 + 1, 64), (1, 2 ** 32 + 64), (-2 ** 32 + 1, 64), (2 ** 31, 64), (-1, 64), (4, 40)])
+def test_workspaces_of_sizes_that_an_int_does_not_hold(native, tokens, k):
+    """Their low 32 bits would be another size."""
+    with pytest.raises(ValueError, match="no product of"):
+        D.linear_workspace(tokens, k, "cpu")
+
+
+def test_a_workspaces_size(native):
+    assert D.linear_workspace(5, 64, "cpu").numel() == D.load().moe_fp8_linear_workspace_size(5, 64) > 0
