@@ -83,9 +83,10 @@ typedef struct {
  * held in fp32 (squares too: a row whose squares add up to more than fp32 holds
  * has norm 0); y is rounded as it is written, normed and quantized are made of
  * the unrounded y and rounded once. At least one output. y and normed may each
- * be x or block (same address and strides), not both the same one. dim % 8 ==
- * 0, dim <= 16384, tokens * heads < 2^31; for quantized heads == 1 and dim %
- * 16 == 0 (else MOE_ERR_SHAPE). */
+ * be x or block (same address and strides: other strides at the same address
+ * are MOE_ERR_INVALID), not both the same one. dim % 8 == 0, dim <= 16384,
+ * tokens * heads < 2^31; for quantized heads == 1 and dim % 16 == 0 (else
+ * MOE_ERR_SHAPE). */
 int moe_residual_norm(const moe_residual_norm_t* args /* host */, cudaStream_t stream);
 
 /* x [rows, K] (row r at x + r * x_stride, in elements, a multiple of 8) as

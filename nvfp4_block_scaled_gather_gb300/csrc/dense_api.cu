@@ -45,6 +45,12 @@ bool rows_ok(const moe_fp8_rows_t* r, int rows, int K) {
 bool same(const moe_heads_t& a, const moe_heads_t& b) {
   return a.data == b.data;
 }
+// An output over an input has the input's rows in their places: else some would be read after they were written. (A stride
+// along one element says nothing.)
+bool over_ok(const moe_heads_t& out, const moe_heads_t& in, int tokens, int heads) {
+  return !out.data || !same(out, in) ||
+         ((tokens <= 1 || out.token_stride == in.token_stride) && (heads <= 1 || out.head_stride == in.head_stride));
+}
 
 int norm_status(const moe_residual_norm_t* a) {
   if (!a || a->tokens < 0 || a->heads <= 0 || a->dim <= 0 || !dtype_ok(a->dtype)) return MOE_ERR_INVALID;
@@ -63,6 +69,8 @@ int norm_status(const moe_residual_norm_t* a) {
       (a->normed.data && !out_ok(a->normed, a->tokens, a->heads, a->dim)))
     return MOE_ERR_INVALID;
   if (a->y.data && a->normed.data && same(a->y, a->normed)) return MOE_ERR_INVALID;
+  for (const moe_heads_t* in : {&a->x, &a->block})
+    if (!over_ok(a->y, *in, a->tokens, a->heads) || !over_ok(a->normed, *in, a->tokens, a->heads)) return MOE_ERR_INVALID;
   if (a->quantized.codes && !rows_ok(&a->quantized, a->tokens, a->dim)) return MOE_ERR_INVALID;
   return MOE_OK;
 }
