@@ -903,7 +903,7 @@ int pairs_at_once() {
 
 // CTAs that share a tile of tn tokens, where there are fewer tiles than CTAs that run at one time; what they send each
 // other is held in 32 KB.
-int split_of(long long tiles, int pieces, long long slots, int tn = 16) {
+int split_of(long long tiles, int pieces, long long slots, int tn) {
   int split = 1;
   if (pieces > 1)
     while (split < kMostSplit && tiles * split * 2 <= slots) split *= 2;
@@ -1028,9 +1028,10 @@ cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, 
   a.x16 = x;
   a.x16_stride = x_stride;
   const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
-  const int split = split_of(rows, a.pieces, slots);
-  if ((g.T <= 16 && split > 1) || clusters_fit(g, 16))
+  if ((g.T <= 16 && split_of(rows, a.pieces, slots, 16) > 1) || clusters_fit(g, 16))
     return dtype == MOE_BF16 ? launch<16, false, MOE_BF16>(g, a, s) : launch<16, false, MOE_FP16>(g, a, s);
+  // (32 x 12,800 x 1024, whose tiles no CTAs share, 7.7 us with a launch before it, 10.3 without)
+  const int split = split_of(rows, a.pieces, slots, 32);
   if (g.T <= 32 && split > 1 && (a.pieces + split - 1) / split * a.piece <= 512)
     return dtype == MOE_BF16 ? launch<32, false, MOE_BF16>(g, a, s) : launch<32, false, MOE_FP16>(g, a, s);
   const cudaError_t e = launch_fp8_quantize(x, x_stride, g.T, g.K, dtype, g.x, s);

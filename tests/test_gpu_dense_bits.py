@@ -79,3 +79,11 @@ def test_sums_keep_all_24_bits(cuda, t, n, signs):
     most = float((x.dequantized().double().abs() @ w.dequantized().double().T).max())
     assert 2 ** 23 < most < 2 ** 24
     assert torch.equal(gemm(x, w), want.float()) and torch.equal(want.float().double(), want)
+
+
+@pytest.mark.parametrize("t,n,k", [(31, 12800, 1024), (32, 19000, 640), (17, 10000, 1024)])
+def test_tokens_of_tiles_that_no_cluster_shares_are_quantized_once(cuda, t, n, k):
+    """Else every CTA would do it again for all of K."""
+    x, w = normal((t, k), "bf16", t), quantize(normal((n, k), "bf16", n, k ** -0.5))
+    y, on_the_way = quantized_on_the_way(x, w)
+    assert not on_the_way and torch.equal(y, gemm(quantize(x), w, "bf16"))
