@@ -876,7 +876,24 @@ bool make_map(CUtensorMap* map, const moe_fp8_rows_t& m, int rows, int K, int bo
          CUDA_SUCCESS;
 }
 
-// Pairs of CTAs that run at one time on the current device (a GPC with an odd number of SMs leaves one out).
+// Clusters of `ctas` CTAs of this footprint that run at one time on the current device, asked of the runtime: a cluster lies in
+// one GPC, and GPCs differ in their SMs.
+int clusters_of(const void* kernel, int ctas, int threads, int smem) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas * 2 * num_sms());
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
+// Of pairs. (A GPC with an odd number of SMs leaves one out.)
 template <int kCols>
 int pairs_at_once() {
   static std::atomic<int> known[64];  // (zero)
@@ -884,29 +901,33 @@ int pairs_at_once() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (known[dev] == 0) {
     using S = Shape<kCols, true>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * num_sms());
-    cfg.blockDim = dim3(S::threads);
-    cfg.dynamicSmemBytes = S::smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<kCols, true, kFromRows>, &cfg) != cudaSuccess || n < 1) return 0;
-    known[dev] = n;
+    known[dev] = clusters_of((const void*)fp8_gemm_kernel<kCols, true, kFromRows>, 2, S::threads, S::smem);
   }
   return known[dev];
 }
 
-// CTAs that share a tile of tn tokens, where there are fewer tiles than CTAs that run at one time; what they send each
+// Of 2, 4 or 8 CTAs of narrow tiles. The runtime counts one CTA an SM for a kernel that allocates tensor memory, however
+// little, where two of these run: one of the same footprint stands in, which is not launched. (74 of 4 and 36 of 8 where 304
+// CTAs' room would be 76 and 38: 36 of 8, 64 tokens x 4608 rows of w x 4096, 9.4 us, 37 of them, x 4736, 14.0, in pairs 11.2;
+// 74 of 4, one token x 9472 x 4096, 9.3, 75, x 9600, 13.5, 75 of 2 10.4.)
+using Narrow = Shape<16, false>;
+__global__ void __launch_bounds__(Narrow::threads, Narrow::per_sm) narrow_footprint() {}
+int clusters_at_once(int ctas) {
+  static std::atomic<int> known[64][kMostSplit + 1];  // (zero)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& n = known[dev][ctas];
+  if (n == 0 && allow_smem<narrow_footprint, Narrow::smem>() == cudaSuccess)
+    n = clusters_of((const void*)narrow_footprint, ctas, Narrow::threads, Narrow::smem);
+  return n;
+}
+
+// CTAs that share a tile of tn tokens, where there are no more tiles than clusters that run at one time; what they send each
 // other is held in 32 KB.
-int split_of(long long tiles, int pieces, long long slots, int tn) {
+int split_of(long long tiles, int pieces, int tn) {
   int split = 1;
   if (pieces > 1)
-    while (split < kMostSplit && tiles * split * 2 <= slots) split *= 2;
+    while (split < kMostSplit && tiles <= clusters_at_once(2 * split)) split *= 2;
   return tn > 8 * split ? 1 : split;
 }
 
@@ -939,7 +960,7 @@ cudaError_t launch(const Fp8Gemm& g, Args a, cudaStream_t s) {
   a.tiles_t = (g.T + a.tn - 1) / a.tn;
   a.tiles = a.tiles_n * a.tiles_t;
   a.split = 1;
-  if (!S::wide) a.split = split_of(a.tiles, a.pieces, slots, a.tn);
+  if (!S::wide) a.split = split_of(a.tiles, a.pieces, a.tn);
   const int recv = a.split > 1 ? a.pieces * a.tn * (kRows / a.split) * 4 : 0;
   const int room = (S::smem - 1024 - kHeader - recv) / (S::deep * (kWBytes + a.tn / S::ctas * kBlockK));
   a.stages = room < S::most_stages ? room : S::most_stages;
@@ -988,12 +1009,10 @@ Args common_args(const Fp8Gemm& g) {
   return a;
 }
 
-constexpr int kNarrowPerSm = Shape<16, false>::per_sm;
-
 // Whether all tiles of so many tokens run at one time, a cluster each.
 bool clusters_fit(const Fp8Gemm& g, int cols) {
-  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
-  return rows * ((g.T + cols - 1) / cols) * kMostSplit <= slots;
+  const long long rows = (g.N + kRows - 1) / kRows;
+  return rows * ((g.T + cols - 1) / cols) <= clusters_at_once(kMostSplit);
 }
 
 }  // namespace
@@ -1007,10 +1026,10 @@ bool clusters_fit(const Fp8Gemm& g, int cols) {
 // (32 x 20,000 x 1024 6.8 and 7.2).
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   const Args a = common_args(g);
-  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
+  const long long rows = (g.N + kRows - 1) / kRows;
   // clusters rather than pairs (of one tile of w half of a pair's rows would be none)
   const bool pays = (g.T + 7) / 8 * 8LL * g.N <= (long long)g.K * g.K / 36 + 8000 || g.N <= kRows;
-  const bool by_itself = split_of(rows, a.pieces, slots, (g.T + 15) / 16 * 16) == 1;
+  const bool by_itself = split_of(rows, a.pieces, (g.T + 15) / 16 * 16) == 1;
   const bool few = pays || by_itself || g.K > 1536;
   auto fits = [&](int cols) { return (pays || a.pieces == 1) && clusters_fit(g, cols); };
   if (g.T <= 16 ? few : fits(16)) return launch<16, false>(g, a, s);
@@ -1027,11 +1046,11 @@ cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, 
   Args a = common_args(g);
   a.x16 = x;
   a.x16_stride = x_stride;
-  const long long rows = (g.N + kRows - 1) / kRows, slots = (long long)num_sms() * kNarrowPerSm;
-  if ((g.T <= 16 && split_of(rows, a.pieces, slots, 16) > 1) || clusters_fit(g, 16))
+  const long long rows = (g.N + kRows - 1) / kRows;
+  if ((g.T <= 16 && split_of(rows, a.pieces, 16) > 1) || clusters_fit(g, 16))
     return dtype == MOE_BF16 ? launch<16, false, MOE_BF16>(g, a, s) : launch<16, false, MOE_FP16>(g, a, s);
   // (32 x 12,800 x 1024, whose tiles no CTAs share, 7.7 us with a launch before it, 10.3 without)
-  const int split = split_of(rows, a.pieces, slots, 32);
+  const int split = split_of(rows, a.pieces, 32);
   if (g.T <= 32 && split > 1 && (a.pieces + split - 1) / split * a.piece <= 512)
     return dtype == MOE_BF16 ? launch<32, false, MOE_BF16>(g, a, s) : launch<32, false, MOE_FP16>(g, a, s);
   const cudaError_t e = launch_fp8_quantize(x, x_stride, g.T, g.K, dtype, g.x, s);

@@ -87,3 +87,15 @@ def test_tokens_of_tiles_that_no_cluster_shares_are_quantized_once(cuda, t, n, k
     x, w = normal((t, k), "bf16", t), quantize(normal((n, k), "bf16", n, k ** -0.5))
     y, on_the_way = quantized_on_the_way(x, w)
     assert not on_the_way and torch.equal(y, gemm(quantize(x), w, "bf16"))
+
+
+@pytest.mark.parametrize("n", [4608, 4609, 4864, 9472, 9473, 9728])
+@pytest.mark.parametrize("t", [1, 30, 64])
+def test_tiles_about_as_many_as_clusters_at_one_time(cuda, t, n):
+    """A few more or less than the clusters of eight and four CTAs that run at one time: the bits of a row do not tell."""
+    x, w = quantize(normal((t, 4096), "bf16", t)), quantize(normal((n, 4096), "bf16", n, 4096 ** -0.5))
+    got = gemm(x, w)
+    for a, b in ((0, 128), (n - 200, n)):
+        some = D.Fp8Rows(w.codes[a:b], w.scales[a:b])
+        assert torch.equal(got[:, a:b].contiguous().view(torch.int32), gemm(x, some).view(torch.int32))
+    assert torch.equal(gemm(x.rows(1), w).view(torch.int32), got[:1].view(torch.int32))
