@@ -1047,7 +1047,14 @@ cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, 
   a.x16 = x;
   a.x16_stride = x_stride;
   const long long rows = (g.N + kRows - 1) / kRows;
-  if ((g.T <= 16 && split_of(rows, a.pieces, 16) > 1) || clusters_fit(g, 16))
+  // Values of K that a CTA would quantize. 1024 take it about 5 us, during which the GPU reads 32 MB: more are worth it as far
+  // as w's bytes, and the four that a launch before this one moves for each value of x, take longer (16 tokens x 512 x 16,384
+  // 9.6 us with a launch before it, 12.9 without, x 65,536 21.7 and 45.6; but one token x 4096 x 11,008 13.1 and 11.1, x 8192
+  // x 16,384 26.1 and 24.0).
+  const int split16 = split_of(rows * ((g.T + 15) / 16), a.pieces, 16);
+  const int values = (a.pieces + split16 - 1) / split16 * a.piece;
+  const bool hidden = values <= 1024 + (g.N + 4LL * g.T) * g.K / 32768;
+  if (((g.T <= 16 && split16 > 1) || clusters_fit(g, 16)) && hidden)
     return dtype == MOE_BF16 ? launch<16, false, MOE_BF16>(g, a, s) : launch<16, false, MOE_FP16>(g, a, s);
   // (32 x 12,800 x 1024, whose tiles no CTAs share, 7.7 us with a launch before it, 10.3 without)
   const int split = split_of(rows, a.pieces, 32);

@@ -99,3 +99,14 @@ def test_tiles_about_as_many_as_clusters_at_one_time(cuda, t, n):
         some = D.Fp8Rows(w.codes[a:b], w.scales[a:b])
         assert torch.equal(got[:, a:b].contiguous().view(torch.int32), gemm(x, some).view(torch.int32))
     assert torch.equal(gemm(x.rows(1), w).view(torch.int32), got[:1].view(torch.int32))
+
+
+@pytest.mark.parametrize("t,n,k,want", [(1, 512, 16384, False), (16, 512, 65536, False), (64, 512, 16384, False), (9, 64, 1 << 18, False),
+                                        (16, 512, 8192, True), (1, 4096, 11008, True), (1, 8192, 16384, True), (300, 100, 11008, False), (500, 100, 11008, True)])
+def test_a_long_k_is_quantized_on_the_way_where_reading_w_takes_as_long(cuda, t, n, k, want):
+    """Up to 1024 + (n + 4 t) k / 32768 values of K a CTA, of eight pieces of K (four of which 64 tiles of w share): 300 x 100 x
+    11,008 has 1536 and may have 1460, 500 x 100 may have 1729, 8192 x 16,384 has 4096 and may have 5122."""
+    x, w = normal((t, k), "bf16", t), quantize(normal((n, k), "bf16", n, k ** -0.5))
+    y, on_the_way = quantized_on_the_way(x, w)
+    assert on_the_way == want
+    assert torch.equal(y.view(torch.int16), gemm(quantize(x), w, "bf16").view(torch.int16))
