@@ -95,9 +95,26 @@ class Fp8Rows:
         self.codes, self.scales, self.n, self.k, self.device = codes, scales, rows, k, codes.get_device()
         # (held here too: memory at an address that is still the tensors' is still theirs, whatever became of its shape)
         self.held = codes.detach(), scales.detach()
-        self.at = codes.data_ptr(), scales.data_ptr()
+        self.at = self.codes_were_at, self.scales_were_at = codes.data_ptr(), scales.data_ptr()
         self.bytes = _rows_bytes(*self.at, codes.stride(0) if rows > 1 else 0,
                                  scales.stride(0) if rows > 1 else 0)
+
+    # (each with what tells its address, which every call asks)
+    @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, t):
+        self._codes, self.codes_at = t, t.data_ptr
+
+    @property
+    def scales(self):
+        return self._scales
+
+    @scales.setter
+    def scales(self, t):
+        self._scales, self.scales_at = t, t.data_ptr
 
     @classmethod
     def empty(cls, rows, k, device="cuda"):
@@ -151,17 +168,14 @@ def _input16(name, t, device: int):
     return p, rs, rows, k, code
 
 
-def _handle(name, r) -> int:
-    """The device of a handle's rows."""
-    if not isinstance(r, Fp8Rows):
-        raise ValueError(f"{name} must be Fp8Rows, got {type(r).__name__}")
-    return r.device
+def _no_handle(name, r):
+    raise ValueError(f"{name} must be Fp8Rows, got {type(r).__name__}")
 
 
 def _rows_of(name, r, device: int):
     if r.device != device:
         raise ValueError(f"{name} must be on cuda:{device}, got {r.codes.device}")
-    if (r.codes.data_ptr(), r.scales.data_ptr()) != r.at:
+    if r.codes_at() != r.codes_were_at or r.scales_at() != r.scales_were_at:
         raise ValueError(f"{name}: its tensors are not where they were when the handle was made: make a new one")
     return r.bytes
 
@@ -181,7 +195,9 @@ def _output(y, rows, n, device: int):
 
 def moe_fp8_quantize_rows(x, out: Fp8Rows, stream=None):
     """x [rows, k], bfloat16 or float16, as 8-bit rows."""
-    dev = _handle("out", out)
+    if not isinstance(out, Fp8Rows):
+        _no_handle("out", out)
+    dev = out.device
     p, rs, rows, k, code = _input16("x", x, dev)
     if (rows, k) != (out.n, out.k):
         raise ValueError(f"out must have {rows} rows of {k}, got {out.n} of {out.k}")
@@ -192,8 +208,11 @@ def moe_fp8_quantize_rows(x, out: Fp8Rows, stream=None):
 
 def moe_fp8_gemm(x: Fp8Rows, w: Fp8Rows, y, stream=None):
     """y [x's rows, w's rows] = x w^T over dequantized values, bfloat16, float16 or float32."""
-    dev = _handle("w", w)
-    _handle("x", x)
+    if not isinstance(w, Fp8Rows):
+        _no_handle("w", w)
+    dev = w.device
+    if not isinstance(x, Fp8Rows):
+        _no_handle("x", x)
     if x.k != w.k:
         raise ValueError(f"x and w must have rows of one length, got {x.k} and {w.k}")
     p, rs, code = _output(y, x.n, w.n, dev)
@@ -214,7 +233,9 @@ def linear_workspace(tokens: int, k: int, device="cuda"):
 def moe_fp8_linear(x, w: Fp8Rows, y, workspace, stream=None):
     """y = x w^T with x [rows, k], bfloat16 or float16, quantized on the way: moe_fp8_quantize_rows, then
     moe_fp8_gemm."""
-    dev = _handle("w", w)
+    if not isinstance(w, Fp8Rows):
+        _no_handle("w", w)
+    dev = w.device
     p, rs, rows, k, code = _input16("x", x, dev)
     if k != w.k:
         raise ValueError(f"x and w must have rows of one length, got {k} and {w.k}")
@@ -319,7 +340,8 @@ def moe_residual_norm(x, block=None, *, y=None, normed=None, quantized: Fp8Rows 
 
     rows = _NO_ROWS
     if quantized is not None:
-        _handle("quantized", quantized)
+        if not isinstance(quantized, Fp8Rows):
+            _no_handle("quantized", quantized)
         rows = _rows_of("quantized", quantized, dev)
         if quantized.n != tokens or quantized.k != dim or heads != 1:
             raise ValueError(f"quantized must have {tokens} rows of {dim} (of one head), got {quantized.n} of {quantized.k}")
