@@ -34,7 +34,7 @@
 // for each 32 values 216 to 220. Of decode batches over many rows of w the reads
 // of w (32 tokens x 100,003 x 4096: 67 us, 6.3 TB/s). Of small ones the chain
 // from the launch over the first tiles, the MMAs and the joined sums to the
-// store: 3.3 us for 256 x 1024, 6.6 for 5120 x 4096, one token.
+// store: 3.4 us for 256 x 1024, 6.8 for 5120 x 4096, one token.
 #include <atomic>
 #include <cstdint>
 
@@ -1023,7 +1023,8 @@ bool clusters_fit(const Fp8Gemm& g, int cols) {
 // 64 x 1024 x 2048 5.3 and 5.7, 64 x 512 x 1024 3.9 and 4.3, but 64 x 2048 x 1024 5.8 and 4.4, 32 x 4096 x 1024 5.8 and 4.5,
 // 200 x 1024 x 1536 6.5 and 5.4. Many rows of w for few tokens are read faster by more CTAs (16 x 8192 x 2048 6.2 us and 7.5,
 // 32 x 8192 x 2048 6.8 and 7.4; but 16 x 4096 x 1536 5.8 and 5.5). Tiles that no CTAs share read w at least as fast as pairs
-// (32 x 20,000 x 1024 6.8 and 7.2).
+// (32 x 20,000 x 1024 6.8 and 7.2). The border T N = K^2 / 36 + 8000, and K of 1536, are drawn between such sizes; they follow
+// from no count of cycles or bytes.
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   const Args a = common_args(g);
   const long long rows = (g.N + kRows - 1) / kRows;
@@ -1040,9 +1041,9 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
 
 cudaError_t launch_fp8_linear(const uint16_t* x, long long x_stride, int dtype, const Fp8Gemm& g, cudaStream_t s) {
   // Where a cluster shares a tile each CTA quantizes its part of K on the way; CTAs that go from tile to tile would do it
-  // again for each. (One token x 5120 x 4096 7.5 us, 10.0 with a launch before it; 16 tokens 9.4 and 10.6; 32 tokens x 4096
-  // x 4096, 512 values of K a CTA, 9.5 and 10.1, but x 11008, 1536 values, 16.9 and 14.8: the quantizing takes longer than
-  // the tiles of w.)
+  // again for each. (One token x 5120 x 4096 7.5 us, 10.0 with a launch before it; 16 tokens 9.0 and 10.5; 32 tokens x 4096
+  // x 4096, 512 values of K a CTA, 9.2 and 9.9, but x 11008, 1536 values, 16.9 and 14.8 when tried: the quantizing takes longer
+  // than the tiles of w.)
   Args a = common_args(g);
   a.x16 = x;
   a.x16_stride = x_stride;

@@ -10,7 +10,7 @@
 // same in every call.
 //
 //  * Rows of at most 256: 8, 16 or 32 threads a row, several rows a thread in
-//    flight (the heads of queries and keys; 3001 x 40 heads of 128: 15 us, where
+//    flight (the heads of queries and keys; 3001 x 40 heads of 128: 14 us, where
 //    a CTA a row took 46).
 //  * Longer rows, few of them (decode): a CTA a row, eight values a thread,
 //    everything asked for at once (one row of 4096 2.3 us, 152 rows 3.1: launch,
@@ -19,8 +19,8 @@
 //    after row, the next ones on their way while the present ones are worked on;
 //    one copy of the norms' weights waits in shared memory (read from L2 for
 //    every row they would be as many bytes again). The rows come to shared
-//    memory by bulk copies: 16,384 x 4096 with both norms 85 to 91 us, 5.9 to 6.3
-//    TB/s (120 with a CTA a row); to 8-bit rows 8192 x 4096 44 us, 5.3 TB/s,
+//    memory by bulk copies: 16,384 x 4096 with both norms 84 to 90 us, 6.0 to 6.4
+//    TB/s (120 with a CTA a row); to 8-bit rows 8192 x 4096 43 us, 5.4 TB/s,
 //    short of issue slots.
 //  * The longest, whose weights and rows would not fit shared memory, come to
 //    registers.
@@ -573,8 +573,8 @@ cudaError_t launch_small_by(int per_sm, const moe_residual_norm_t& a, const Shap
 // A CTA's start and end take as long as several turns of its loop, so few CTAs that stay: with a block one an SM, more for
 // rows that keep each busy for twelve turns (3000 rows of 256: one an SM 5.8 us, two 6.9, three 10.4; 30,000: 23.6, 18.3 and
 // 19.7; 300,000 of 128: 96, 64, 59 and with four 55). Without one, two rows of a thread at a time where all run at once
-// (200 tokens of 40 heads of 128: 3.4 us, four rows 3.6; 64 tokens 1.9 and 2.5), else four and three CTAs an SM (3001 tokens
-// 14.5 us, two rows and five CTAs 16.3).
+// (200 tokens of 40 heads of 128: 3.1 us, four rows 0.2 more; 64 tokens 2.0 and 2.6), else four and three CTAs an SM (3001
+// tokens 14 us, two rows and five CTAs 16).
 template <int kType, int G>
 cudaError_t launch_small(const moe_residual_norm_t& a, const Shape& shape, cudaStream_t s) {
   const long long rows = (long long)a.tokens * a.heads;
